@@ -40,6 +40,7 @@ __all__ = [
     "fp8_cast_transpose_amax_dbias_noalloc", "NOALLOC_SCRATCH_BYTES",
     "fp8_cast_transpose_amax_cached", "fp8_reference_copy", "fp8_produce_modulate_backward",
     "fp8_gemm_workspace_bytes", "fp8_cast_transpose_amax_group", "CAST_GROUP_MAX",
+    "Dropout", "fp8_dropout", "fp8_dropout_cast_transpose_amax",
     "library_path", "lib",
 ]
 
@@ -90,6 +91,15 @@ class _GroupItem(ctypes.Structure):
     ]
 
 
+class _DropoutDesc(ctypes.Structure):
+    """Mirror of fp8_dropout_t."""
+    _fields_ = [
+        ("rng", ctypes.c_void_p),
+        ("p", ctypes.c_float),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
 _lib: Optional[ctypes.CDLL] = None
 
 
@@ -130,7 +140,11 @@ def lib() -> ctypes.CDLL:
         L.fp8_linear_fwd_ws.argtypes = [dp, dp, vp, vp, vp, i64, vp]
         L.fp8_linear_dgrad_ws.argtypes = [dp, dp, vp, vp, i64, vp]
         L.fp8_linear_wgrad_ws.argtypes = [dp, dp, vp, i32, vp, i64, vp]
-        for f in (L.fp8_scale_update, L.fp8_cast_transpose_amax, L.fp8_cast_transpose_amax_dbias,
+        pp = ctypes.POINTER(_DropoutDesc)
+        L.fp8_dropout.argtypes = [pp, vp, i64, vp, i64, vp, i64, i32, i64, i64, vp]
+        L.fp8_dropout_cast_transpose_amax.argtypes = [pp, vp, i64, vp, i64, vp, i64, i64, i64, vp,
+                                                      dp, vp, vp, vp, i64, vp, vp]
+        for f in (L.fp8_dropout, L.fp8_dropout_cast_transpose_amax, L.fp8_scale_update, L.fp8_cast_transpose_amax, L.fp8_cast_transpose_amax_dbias,
                   L.fp8_cast_transpose_amax_dbias_noalloc, L.fp8_cast_transpose_amax_cached,
                   L.fp8_reference_copy,
                   L.fp8_produce_cast_transpose_amax, L.fp8_cast_transpose_dynamic,
@@ -502,6 +516,135 @@ def fp8_produce_modulate_backward(op: int, dy: torch.Tensor, x: torch.Tensor, a:
         _row_stride(a), b.data_ptr(), _row_stride(b), dx.data_ptr(), _row_stride(dx),
         da.data_ptr(), _row_stride(da), db.data_ptr(), _row_stride(db), dy.shape[0],
         dy.shape[1], _stream(stream)), "fp8_produce_modulate_backward")
+
+
+@dataclass
+class Dropout:
+    """A dropout: probability p and rng, a device int64 tensor {seed, offset}
+    (a row of a [sites, 2] tensor is fine).  The mask follows from them and an
+    element's position alone and is never stored; the calls read rng on the
+    device when they run."""
+    p: float
+    rng: torch.Tensor
+
+    def desc(self) -> _DropoutDesc:
+        if self.rng is None or self.rng.numel() != 2:
+            raise ValueError("Dropout.rng must hold two elements (seed, offset)")
+        return _DropoutDesc(_ptr(self.rng, torch.int64, "Dropout.rng"), self.p, 0)
+
+
+def _on_current_device(*tensors) -> None:
+    """The calls run on the current device: tensors of another one are refused."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != dev:
+            raise ValueError(f"tensors must be on the current device cuda:{dev}, got {t.device}")
+
+
+def _matrix(t: torch.Tensor, shape, dtype, what: str) -> None:
+    """t: a 2-D device tensor of this shape and type with unit column stride."""
+    if t.dim() != 2 or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
+    if t.numel() > 0 and (t.stride(1) != 1 and t.shape[1] > 1):
+        raise ValueError(f"{what} must have unit stride in the last dimension")
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a device tensor")
+
+
+def _stride_of(t: Optional[torch.Tensor]) -> int:
+    """Row stride of an optional matrix; a single row's stride plays no part."""
+    if t is None:
+        return 0
+    return t.stride(0) if t.shape[0] > 1 and t.numel() > 0 else t.shape[1]
+
+
+def _may_share(y: Optional[torch.Tensor], inputs, what: str) -> None:
+    """y may be one of the inputs (same pointer and stride) or lie apart from them."""
+    if y is None or y.numel() == 0:
+        return
+    end = lambda t: t.data_ptr() + ((t.shape[0] - 1) * _stride_of(t) + t.shape[1]) * t.element_size()
+    for t in inputs:
+        if t is None or t.numel() == 0:
+            continue
+        if y.data_ptr() == t.data_ptr() and _stride_of(y) == _stride_of(t):
+            continue
+        if y.data_ptr() < end(t) and t.data_ptr() < end(y) and not _columns_apart(y, t):
+            raise ValueError(f"{what} must be an input itself or not overlap it")
+
+
+def _columns_apart(y: torch.Tensor, t: torch.Tensor) -> bool:
+    """Whether two matrices of one row stride lie in columns of their own."""
+    ld = _stride_of(y)
+    if ld != _stride_of(t) or y.element_size() != t.element_size():
+        return False
+    gap = (t.data_ptr() - y.data_ptr()) // y.element_size() % ld
+    return y.shape[1] <= gap and gap + t.shape[1] <= ld
+
+
+def fp8_dropout(x: torch.Tensor, drop: Dropout, y: torch.Tensor,
+                residual: Optional[torch.Tensor] = None, stream=None) -> None:
+    """y = dropout(x), or residual + dropout(x): bf16 or fp32 2-D device
+    tensors of one shape and type with unit column stride (column slices are
+    fine).  The gradient of x is the same call on the gradient of y without
+    the residual.  y may be x or residual."""
+    if x.dtype == torch.bfloat16:
+        dt = DTYPE_BF16
+    elif x.dtype == torch.float32:
+        dt = DTYPE_FP32
+    else:
+        raise TypeError("x must be bf16 or fp32")
+    _matrix(x, x.shape, x.dtype, "x")
+    _matrix(y, x.shape, x.dtype, "y")
+    if residual is not None:
+        _matrix(residual, x.shape, x.dtype, "residual")
+    d = drop.desc()
+    _on_current_device(x, y, residual, drop.rng)
+    _may_share(y, (x, residual), "y")
+    _check(lib().fp8_dropout(ctypes.byref(d), x.data_ptr(), _stride_of(x),
+                             None if residual is None else residual.data_ptr(),
+                             _stride_of(residual), y.data_ptr(), _stride_of(y), dt, x.shape[0],
+                             x.shape[1], _stream(stream)), "fp8_dropout")
+
+
+def fp8_dropout_cast_transpose_amax(x: torch.Tensor, drop: Dropout, scale: torch.Tensor,
+                                    out: Float8Tensor, amax_cur: Optional[torch.Tensor] = None,
+                                    residual: Optional[torch.Tensor] = None,
+                                    y: Optional[torch.Tensor] = None,
+                                    dbias: Optional[torch.Tensor] = None,
+                                    workspace: Optional[torch.Tensor] = None,
+                                    noop_flag: Optional[torch.Tensor] = None,
+                                    stream=None) -> None:
+    """y = bf16(dropout(x)), or bf16(residual + dropout(x)), and the cast of y
+    into `out` as fp8_cast_transpose_amax casts it.  x, residual, y: bf16 2-D
+    device tensors of one shape with unit column stride; y may be None (only
+    the codes are wanted), x or residual.  `dbias` [cols] (fp32) receives the
+    column sums of y and needs a `workspace` of
+    fp8_cast_dbias_workspace_bytes(rows, cols) bytes."""
+    _need_scalar(scale, "scale")
+    _need_scalar(amax_cur, "amax_cur")
+    _need_scalar(noop_flag, "noop_flag")
+    _matrix(x, x.shape, torch.bfloat16, "x")
+    for t, n in ((residual, "residual"), (y, "y")):
+        if t is not None:
+            _matrix(t, x.shape, torch.bfloat16, n)
+    _need_shape(dbias, (x.shape[1],), "dbias")
+    if dbias is not None and workspace is None:
+        raise ValueError("dbias needs a workspace")
+    d, o = drop.desc(), out.desc()
+    _on_current_device(x, residual, y, drop.rng, scale, out.data, out.data_t, out.scale_inv,
+                       amax_cur, dbias, workspace, noop_flag)
+    _may_share(y, (x, residual), "y")
+    ws, ws_bytes = _ws(workspace)
+    _check(lib().fp8_dropout_cast_transpose_amax(
+        ctypes.byref(d), x.data_ptr(), _stride_of(x),
+        None if residual is None else residual.data_ptr(), _stride_of(residual),
+        None if y is None else y.data_ptr(), _stride_of(y), x.shape[0], x.shape[1],
+        _ptr(scale, torch.float32, "scale"), ctypes.byref(o),
+        _ptr(amax_cur, torch.float32, "amax_cur"), _ptr(dbias, torch.float32, "dbias"), ws,
+        ws_bytes, _ptr(noop_flag, torch.int32, "noop_flag"), _stream(stream)),
+        "fp8_dropout_cast_transpose_amax")
 
 
 def fp8_cast_transpose_dynamic(x: torch.Tensor, scale: torch.Tensor, out: Float8Tensor,

@@ -6,6 +6,7 @@
 // a HIP graph (the class of bug "[PyTorch] Refactor FP8 workspaces in linear
 // modules" describes for transpose caches filled outside the captured region
 // cannot arise: the cast always writes the transpose it is asked for).
+#include <math.h>
 #include <string.h>
 
 #include "fp8dsl_internal.h"
@@ -61,6 +62,20 @@ int check_cast(const void *x, int32_t src, int64_t rows, int64_t cols, int64_t l
     if ((x && !aligned16(x)) || (out->data && !aligned16(out->data)) ||
         (out->data_t && !aligned16(out->data_t)))
         return FP8_ERR_ALIGN;
+    return FP8_OK;
+}
+
+// A dropout descriptor as the kernels take it.
+int dropout_args(const fp8_dropout_t *drop, DropoutArgs *out) {
+    if (drop == nullptr) return FP8_ERR_NULL;
+    if (drop->reserved != 0 || !(drop->p >= 0.0f && drop->p <= 1.0f)) return FP8_ERR_ARG;
+    const double t = nearbyint((double)drop->p * 65536.0);
+    if (t > 65535.0) return FP8_ERR_ARG;
+    if (drop->rng == nullptr) return FP8_ERR_NULL;
+    if ((reinterpret_cast<uintptr_t>(drop->rng) & 7) != 0) return FP8_ERR_ALIGN;
+    out->rng = drop->rng;
+    out->threshold = (uint32_t)t;
+    out->factor = (float)(65536.0 / (65536.0 - t));
     return FP8_OK;
 }
 
@@ -346,6 +361,69 @@ int fp8_produce_cast_transpose_amax(int32_t op, const uint16_t *x, int64_t ldx,
     return status_of(launch_produce_cast(op, x, ldx, a, lda, reads_b ? b : nullptr, ldb, y, rows,
                                          cols, scale, out->fmt, out->data, out->data_t, amax_cur,
                                          out->scale_inv, noop_flag, s));
+}
+
+int fp8_dropout(const fp8_dropout_t *drop, const void *x, int64_t ldx, const void *residual,
+                int64_t ldres, void *y, int64_t ldy, int32_t dtype, int64_t rows, int64_t cols,
+                fp8_stream_t stream) {
+    if (dtype != FP8_DTYPE_BF16 && dtype != FP8_DTYPE_FP32) return FP8_ERR_ARG;
+    DropoutArgs args;
+    if (int e = dropout_args(drop, &args)) return e;
+    const int64_t unit = dtype == FP8_DTYPE_BF16 ? 8 : 4;
+    if (rows < 0 || cols < 0 || rows > INT32_MAX || cols > INT32_MAX || (cols % 8) != 0 ||
+        ldx < cols || ldy < cols || (ldx % unit) != 0 || (ldy % unit) != 0 ||
+        (residual && (ldres < cols || (ldres % unit) != 0)))
+        return FP8_ERR_SHAPE;
+    if (rows == 0 || cols == 0) return FP8_OK;
+    // The launch: at most 64 lanes a row in x, a workgroup per 2048 columns in y.
+    if (rows > ((int64_t)1 << 25) || cols > ((int64_t)1 << 26)) return FP8_ERR_SHAPE;
+    for (int64_t ld : {ldx, ldy, residual ? ldres : cols})
+        if (ld > INT64_MAX / 4 / rows) return FP8_ERR_SHAPE;
+    if (x == nullptr || y == nullptr) return FP8_ERR_NULL;
+    if (!aligned16(x) || !aligned16(y) || !aligned16(residual)) return FP8_ERR_ALIGN;
+    return status_of(launch_dropout(x, ldx, residual, ldres, y, ldy, dtype, rows, cols, args,
+                                    static_cast<hipStream_t>(stream)));
+}
+
+int fp8_dropout_cast_transpose_amax(const fp8_dropout_t *drop, const uint16_t *x, int64_t ldx,
+                                    const uint16_t *residual, int64_t ldres, uint16_t *y,
+                                    int64_t ldy, int64_t rows, int64_t cols, const float *scale,
+                                    const fp8_tensor_t *out, float *amax_cur, float *dbias,
+                                    void *workspace, int64_t workspace_bytes,
+                                    const int32_t *noop_flag, fp8_stream_t stream) {
+    DropoutArgs args;
+    if (int e = dropout_args(drop, &args)) return e;
+    if (int e = check_cast(x, FP8_DTYPE_BF16, rows, cols, ldx, scale, out)) return e;
+    if ((residual && (ldres < cols || (ldres % 8) != 0)) ||
+        (y && (ldy < cols || (ldy % 8) != 0)))
+        return FP8_ERR_SHAPE;
+    const int64_t tiles_r = (rows + 127) / 128, tiles_c = (cols + 127) / 128;
+    // The launch's thread count, 256 per tile.
+    if (tiles_r * tiles_c >= ((int64_t)1 << 24)) return FP8_ERR_SHAPE;
+    if (!aligned16(residual) || !aligned16(y)) return FP8_ERR_ALIGN;
+    if (dbias && (reinterpret_cast<uintptr_t>(dbias) & 3) != 0) return FP8_ERR_ALIGN;
+    const bool empty = (rows == 0 || cols == 0);
+    if (dbias && !empty) {
+        if (workspace == nullptr) return FP8_ERR_NULL;
+        if (workspace_bytes < fp8_cast_dbias_workspace_bytes(rows, cols)) return FP8_ERR_SHAPE;
+        if (!aligned16(workspace)) return FP8_ERR_ALIGN;
+    }
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    float *ws = dbias ? static_cast<float *>(workspace) : nullptr;
+    if (empty) {
+        if (out->scale_inv) {
+            if (int e = status_of(launch_scale_inv_only(scale, out->scale_inv, noop_flag, s)))
+                return e;
+        }
+        if (dbias == nullptr) return FP8_OK;
+        return status_of(launch_dbias_reduce(nullptr, 0, 0, cols, dbias, noop_flag, s));
+    }
+    if (int e = status_of(launch_dropout_cast(x, ldx, residual, ldres, y, ldy, rows, cols, args,
+                                              scale, out->fmt, out->data, out->data_t, amax_cur,
+                                              out->scale_inv, noop_flag, ws, 128 * tiles_c, s)))
+        return e;
+    if (dbias == nullptr) return FP8_OK;
+    return status_of(launch_dbias_reduce(ws, tiles_r, 128 * tiles_c, cols, dbias, noop_flag, s));
 }
 
 int fp8_produce_modulate_backward(int32_t op, const uint16_t *dy, int64_t lddy,

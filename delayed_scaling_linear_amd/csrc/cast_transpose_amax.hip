@@ -42,6 +42,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "dropout.h"
 #include "fp8_codec.h"
 #include "fp8dsl_internal.h"
 
@@ -883,6 +884,126 @@ hipError_t launch_produce_op_fmt(const uint16_t *x, int64_t ldx, const uint16_t 
     return hipGetLastError();
 }
 
+// Dropout in front of a cast, one pass: y = bf16(residual + dropout(x)) (or
+// the dropout alone; the arithmetic of dropout.hip), y cast exactly as
+// fp8_cast_transpose_amax casts a bf16 source, its column sums as
+// fp8_cast_transpose_amax_dbias takes them.  One workgroup per 128 x 128
+// tile in the lane layout of the cast: a lane's 8-column source chunk is one
+// group of the generator, so a lane makes eight Philox calls for its 64
+// elements while its loads are in flight.  A lane stores y where it alone has
+// read x and the residual, so y may be either of them.
+template <int FMT, bool WANT_Q, bool WANT_QT, bool DBIAS>
+__global__ __launch_bounds__(THREADS) void dropout_cast_kernel(
+    const uint16_t *x, int64_t ldx, const uint16_t *res, int64_t ldres, uint16_t *y, int64_t ldy,
+    int64_t rows, int64_t cols, DropoutArgs drop,
+    const float *__restrict__ scale_ptr, uint8_t *__restrict__ q, uint8_t *__restrict__ qt,
+    float *__restrict__ amax_cur, float *__restrict__ scale_inv_out,
+    const int32_t *__restrict__ noop, int64_t tiles_c, float *__restrict__ dbias_ws,
+    int64_t ws_ld) {
+#pragma clang fp contract(off)
+    if (noop != nullptr && *noop != 0) return;
+    __shared__ uint32_t lds_t[TILE * (TILE / 4)];
+    __shared__ uint32_t lds_amax[THREADS / 64];
+    __shared__ float lds_db[DBIAS ? (THREADS / 64) * TILE : 1];
+
+    const int tid = threadIdx.x;
+    const int lane = tid & 63;
+    const int wave = tid >> 6;
+    const int cc = lane & 7;
+    const int cq = store_chunk<FP8_DTYPE_BF16>(cc);
+    const int rg = wave * 8 + (lane >> 3);
+    const float s = *scale_ptr;
+    const bool s_special = !(fabsf(s) > 0.0f && fabsf(s) <= 3.402823466e38f);
+    if (blockIdx.x == 0 && tid == 0 && scale_inv_out != nullptr) *scale_inv_out = 1.0f / s;
+    const DropoutKey dkey(drop.rng);
+
+    const int64_t t = blockIdx.x;
+    const int64_t tr = t / tiles_c, tcn = t - tr * tiles_c;
+    const int64_t row0 = tr * TILE, col0 = tcn * TILE;
+    const int64_t r = row0 + 4 * rg, c = col0 + 16 * cq;
+    const bool valid = (r < rows) && (c < cols);   // rows, cols are multiples of 16
+    const bool add = res != nullptr;
+
+    // All loads first: the lane's two chunks of its four rows.
+    u32x4 xs[4][2], rs[4][2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int64_t ch = col0 + 64 * h + 8 * cc;
+        const bool in = r < rows && ch < cols;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            xs[i][h] = rs[i][h] = u32x4{0u, 0u, 0u, 0u};
+            if (in) {
+                xs[i][h] = *reinterpret_cast<const u32x4 *>(x + (r + i) * ldx + ch);
+                if (add) rs[i][h] = *reinterpret_cast<const u32x4 *>(res + (r + i) * ldres + ch);
+            }
+        }
+    }
+    SrcRow<FP8_DTYPE_BF16> ys[4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int64_t ch = col0 + 64 * h + 8 * cc;
+        const bool in = r < rows && ch < cols;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t w[4];
+            dropout_words(dkey, (uint64_t)((r + i) * (cols >> 3) + (ch >> 3)), w);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t xw = xs[i][h][k], rw = rs[i][h][k];
+                const bool keep0 = (w[k] & 0xFFFFu) >= drop.threshold;
+                const bool keep1 = (w[k] >> 16) >= drop.threshold;
+                float v0 = keep0 ? bf16_lo(xw) * drop.factor : 0.0f;
+                float v1 = keep1 ? bf16_hi(xw) * drop.factor : 0.0f;
+                if (add) {
+                    v0 = bf16_lo(rw) + v0;
+                    v1 = bf16_hi(rw) + v1;
+                }
+                const uint32_t y0 = (v0 != v0) ? 0x7FC0u : f32_to_bf16_bits_rne(v0);
+                const uint32_t y1 = (v1 != v1) ? 0x7FC0u : f32_to_bf16_bits_rne(v1);
+                ys[i].v[h][k] = y0 | (y1 << 16);
+            }
+            if (y != nullptr && in) *reinterpret_cast<u32x4 *>(y + (r + i) * ldy + ch) = ys[i].v[h];
+        }
+    }
+    uint32_t key = 0;
+    encode_block<FP8_DTYPE_BF16, FMT, WANT_Q, WANT_QT>(ys, s, s_special, valid, q, r, c, cols, cq,
+                                                       rg, lane, nullptr, lds_t, key);
+    if constexpr (DBIAS) tile_col_sums_to_lds<FP8_DTYPE_BF16>(ys, &lds_db[wave * TILE], lane, cc);
+    __syncthreads();
+    if constexpr (WANT_QT) store_transposed(lds_t, qt, rows, cols, row0, col0, lane, wave);
+    if constexpr (DBIAS) tile_col_sums_out(lds_db, tid, dbias_ws, ws_ld, tr, tcn);
+    if (amax_cur != nullptr) flush_amax(key, amax_cur, lds_amax, lane, wave, tid);
+}
+
+template <int FMT>
+hipError_t launch_dropout_cast_fmt(const uint16_t *x, int64_t ldx, const uint16_t *res,
+                                   int64_t ldres, uint16_t *y, int64_t ldy, int64_t rows,
+                                   int64_t cols, const DropoutArgs &drop, const float *scale,
+                                   uint8_t *q, uint8_t *qt, float *amax_cur, float *scale_inv_out,
+                                   const int32_t *noop, float *dbias_ws, int64_t ws_ld,
+                                   hipStream_t stream) {
+    const int64_t tiles_c = (cols + TILE - 1) / TILE;
+    const dim3 grid((unsigned)(((rows + TILE - 1) / TILE) * tiles_c));
+    auto launch = [&](auto wq, auto wqt, auto db) {
+        hipLaunchKernelGGL((dropout_cast_kernel<FMT, decltype(wq)::value, decltype(wqt)::value,
+                                                decltype(db)::value>),
+                           grid, dim3(THREADS), 0, stream, x, ldx, res, ldres, y, ldy, rows, cols,
+                           drop, scale, q, qt, amax_cur, scale_inv_out, noop, tiles_c, dbias_ws,
+                           ws_ld);
+    };
+    using T1 = std::true_type;
+    using F1 = std::false_type;
+    auto by_layout = [&](auto db) {
+        if (q && qt) launch(T1{}, T1{}, db);
+        else if (q) launch(T1{}, F1{}, db);
+        else launch(F1{}, T1{}, db);
+    };
+    if (dbias_ws) by_layout(T1{});
+    else by_layout(F1{});
+    return hipGetLastError();
+}
+
 // Gradient of the modulation producer y = a * x / b (FP8_PRODUCE_MODULATE,
 // or _FINITE) with respect to x, a and b, for the output gradient dy of y.
 // fp32 on the widened bf16 inputs, each step rounded to nearest even:
@@ -1019,6 +1140,21 @@ hipError_t launch_produce_cast(int op, const uint16_t *x, int64_t ldx, const uin
     return launch_produce_op_fmt<FP8_PRODUCE_ADD, FP8_E5M2>(x, ldx, a, lda, b, ldb, y, rows, cols,
                                                             scale, q, qt, amax_cur, scale_inv_out,
                                                             noop, stream);
+}
+
+hipError_t launch_dropout_cast(const uint16_t *x, int64_t ldx, const uint16_t *residual,
+                               int64_t ldres, uint16_t *y, int64_t ldy, int64_t rows, int64_t cols,
+                               const DropoutArgs &drop, const float *scale, int fmt, uint8_t *q,
+                               uint8_t *qt, float *amax_cur, float *scale_inv_out,
+                               const int32_t *noop, float *dbias_ws, int64_t ws_ld,
+                               hipStream_t stream) {
+    if (fmt == FP8_E4M3)
+        return launch_dropout_cast_fmt<FP8_E4M3>(x, ldx, residual, ldres, y, ldy, rows, cols, drop,
+                                                 scale, q, qt, amax_cur, scale_inv_out, noop,
+                                                 dbias_ws, ws_ld, stream);
+    return launch_dropout_cast_fmt<FP8_E5M2>(x, ldx, residual, ldres, y, ldy, rows, cols, drop,
+                                             scale, q, qt, amax_cur, scale_inv_out, noop, dbias_ws,
+                                             ws_ld, stream);
 }
 
 hipError_t launch_modulate_backward(bool finite, const uint16_t *dy, int64_t lddy,

@@ -7,6 +7,7 @@
 
 #include <atomic>
 
+#include "dropout.h"
 #include "fp8dsl.h"
 
 namespace fp8dsl {
@@ -105,6 +106,20 @@ hipError_t launch_modulate_backward(bool finite, const uint16_t *dy, int64_t ldd
                                     int64_t lddx, uint16_t *da, int64_t ldda, uint16_t *db,
                                     int64_t lddb, int64_t rows, int64_t cols,
                                     hipStream_t stream);
+
+// y = residual + dropout(x) (residual may be null), bf16 or fp32; cols % 8 == 0.
+hipError_t launch_dropout(const void *x, int64_t ldx, const void *residual, int64_t ldres, void *y,
+                          int64_t ldy, int dtype, int64_t rows, int64_t cols,
+                          const DropoutArgs &drop, hipStream_t stream);
+
+// The same in bf16, then the cast of y; y and residual may be null.  dbias_ws
+// as launch_cast_transpose_amax.
+hipError_t launch_dropout_cast(const uint16_t *x, int64_t ldx, const uint16_t *residual,
+                               int64_t ldres, uint16_t *y, int64_t ldy, int64_t rows, int64_t cols,
+                               const DropoutArgs &drop, const float *scale, int fmt, uint8_t *q,
+                               uint8_t *qt, float *amax_cur, float *scale_inv_out,
+                               const int32_t *noop, float *dbias_ws, int64_t ws_ld,
+                               hipStream_t stream);
 
 // Dynamic scaling: *amax = max |x| (cleared first), then *scale = fp8_max /
 // (amax * 2^margin) unless zero / non-finite (the scale update's guard).

@@ -20,6 +20,8 @@
  * (fp8_cast_transpose_amax_dbias, also as a no-allocation entry point), the
  * toy block's elementwise producers fused into the cast and the modulation's
  * gradient (fp8_produce_cast_transpose_amax, fp8_produce_modulate_backward),
+ * dropout from a counter-based generator, alone or fused into the cast
+ * (fp8_dropout, fp8_dropout_cast_transpose_amax),
  * dynamic scaling as the comparator (fp8_cast_transpose_dynamic), the
  * forward with FP8 output and output amax (fp8_linear_fwd_fp8out), the three
  * products split over K through a caller workspace for shapes that alone
@@ -379,6 +381,83 @@ int fp8_produce_cast_transpose_amax(int32_t op, const uint16_t *x, int64_t ldx,
                                     const uint16_t *a, int64_t lda, const uint16_t *b,
                                     int64_t ldb, uint16_t *y, int64_t rows, int64_t cols,
                                     const float *scale, const fp8_tensor_t *out, float *amax_cur,
+                                    const int32_t *noop_flag, fp8_stream_t stream);
+
+/*
+ * A dropout: which elements of a [rows, cols] tensor are kept, as a function
+ * of their position alone.  No mask is stored anywhere; a call with the same
+ * {seed, offset} and p derives the same one again.  Element (r, c) belongs to
+ * group e = (r * cols + c) / 8 (strides play no part), and group e takes the
+ * four words of Philox4x32 with 7 rounds for counter words (e low, e high,
+ * offset low, offset high) and key (seed low, seed high): the element's
+ * number u is the low (c even) or high (c odd) 16 bits of word (c % 8) / 2.
+ * With T = p * 65536 rounded to the nearest integer (ties to even), the
+ * element is kept where u >= T and scaled by f = 65536 / (65536 - T) rounded
+ * to fp32: the rate is p to within 2^-17, and f is the reciprocal of the exact
+ * keep rate.  A p that rounds to T = 0 keeps every element.
+ *
+ * rng is read on the device when the kernel runs, so a captured graph draws a
+ * new mask whenever the program changes offset between replays.
+ */
+typedef struct fp8_dropout_desc {
+    const int64_t *rng;  /* device {seed, offset}, 8-byte aligned              */
+    float p;             /* drop probability, 0 <= p, T <= 65535               */
+    int32_t reserved;    /* must be 0                                          */
+} fp8_dropout_t;
+
+/*
+ * fp8_dropout -- y = dropout(x), or y = residual + dropout(x).
+ *
+ *   t = kept(r, c) ? x[r, c] * f : +0          (fp32 product)
+ *   y[r, c] = residual[r, c] + t               (fp32 sum; t alone without one)
+ *
+ * rounded once (to nearest even) to the tensors' type; a NaN y in bf16 is
+ * written 0x7FC0.  A dropped element is +0 even where x is infinite or NaN.
+ * The gradient with respect to x is this call on the gradient of y, without
+ * the residual; the residual's is the gradient of y itself.
+ *
+ * dtype   FP8_DTYPE_BF16 or FP8_DTYPE_FP32, of x, residual and y.
+ * x, residual (or NULL), y   device [rows, cols] with row strides ldx, ldres,
+ *         ldy (elements): cols a multiple of 8, each stride >= cols and a
+ *         multiple of 8 (bf16) or 4 (fp32), 16-byte aligned pointers.  y may
+ *         be x or residual (same pointer and stride), else must not overlap
+ *         them.  At most 2^25 rows and 2^26 columns.
+ * Errors: FP8_ERR_NULL, FP8_ERR_ARG (dtype, p), FP8_ERR_SHAPE, FP8_ERR_ALIGN,
+ * FP8_ERR_LAUNCH / FP8_ERR_DEVICE.  rows or cols 0: no work.
+ */
+int fp8_dropout(const fp8_dropout_t *drop, const void *x, int64_t ldx, const void *residual,
+                int64_t ldres, void *y, int64_t ldy, int32_t dtype, int64_t rows, int64_t cols,
+                fp8_stream_t stream);
+
+/*
+ * fp8_dropout_cast_transpose_amax -- dropout in front of a linear, fused with
+ * the cast of its result: the producer of a linear's input (the residual
+ * stream plus a dropped branch, or a dropped activation) and, on an output
+ * gradient, the backward of a dropout behind a linear.
+ *
+ *   y = bf16 result of fp8_dropout on bf16 x (and residual)
+ *
+ * then exactly what fp8_cast_transpose_amax writes for the source y with this
+ * scale, and, if dbias is not NULL, what fp8_cast_transpose_amax_dbias writes
+ * there (the fp32 column sums of y), in one pass over x.
+ *
+ * x, residual (or NULL)   device bf16 [rows, cols], row strides ldx, ldres
+ *         (>= cols, multiples of 8; 16-byte aligned).
+ * y       device bf16 [rows, cols], row stride ldy (as ldx), or NULL: only the
+ *         codes are wanted.  May be x or residual (same pointer and stride),
+ *         else must not overlap them.
+ * dbias   NULL, or as fp8_cast_transpose_amax_dbias, with its workspace of
+ *         fp8_cast_dbias_workspace_bytes(rows, cols) bytes (workspace and
+ *         workspace_bytes are not read without dbias).
+ * scale, out, amax_cur, noop_flag, constraints (rows, cols multiples of 16)
+ * and errors as fp8_cast_transpose_amax; FP8_ERR_ARG for p; fewer than 2^24
+ * tiles of 128 x 128.
+ */
+int fp8_dropout_cast_transpose_amax(const fp8_dropout_t *drop, const uint16_t *x, int64_t ldx,
+                                    const uint16_t *residual, int64_t ldres, uint16_t *y,
+                                    int64_t ldy, int64_t rows, int64_t cols, const float *scale,
+                                    const fp8_tensor_t *out, float *amax_cur, float *dbias,
+                                    void *workspace, int64_t workspace_bytes,
                                     const int32_t *noop_flag, fp8_stream_t stream);
 
 /*
