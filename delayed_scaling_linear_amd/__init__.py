@@ -41,6 +41,8 @@ __all__ = [
     "fp8_cast_transpose_amax_cached", "fp8_reference_copy", "fp8_produce_modulate_backward",
     "fp8_gemm_workspace_bytes", "fp8_cast_transpose_amax_group", "CAST_GROUP_MAX",
     "Dropout", "fp8_dropout", "fp8_dropout_cast_transpose_amax",
+    "Adapters", "AdapterPlan", "fp8_adapter_plan", "fp8_adapter_plan_bytes",
+    "fp8_adapter_workspace_bytes", "fp8_adapter_fwd", "fp8_adapter_backward",
     "library_path", "lib",
 ]
 
@@ -100,6 +102,19 @@ class _DropoutDesc(ctypes.Structure):
     ]
 
 
+class _AdaptersDesc(ctypes.Structure):
+    """Mirror of fp8_adapters_t."""
+    _fields_ = [
+        ("a", ctypes.c_void_p),
+        ("b", ctypes.c_void_p),
+        ("alpha", ctypes.c_void_p),
+        ("count", ctypes.c_int32),
+        ("rank", ctypes.c_int32),
+        ("in_", ctypes.c_int64),
+        ("out", ctypes.c_int64),
+    ]
+
+
 _lib: Optional[ctypes.CDLL] = None
 
 
@@ -144,7 +159,18 @@ def lib() -> ctypes.CDLL:
         L.fp8_dropout.argtypes = [pp, vp, i64, vp, i64, vp, i64, i32, i64, i64, vp]
         L.fp8_dropout_cast_transpose_amax.argtypes = [pp, vp, i64, vp, i64, vp, i64, i64, i64, vp,
                                                       dp, vp, vp, vp, i64, vp, vp]
-        for f in (L.fp8_dropout, L.fp8_dropout_cast_transpose_amax, L.fp8_scale_update, L.fp8_cast_transpose_amax, L.fp8_cast_transpose_amax_dbias,
+        ap = ctypes.POINTER(_AdaptersDesc)
+        L.fp8_adapter_plan_bytes.argtypes = [i64, i32]
+        L.fp8_adapter_plan_bytes.restype = i64
+        L.fp8_adapter_workspace_bytes.argtypes = [i64, i32, i32, i64, i64]
+        L.fp8_adapter_workspace_bytes.restype = i64
+        L.fp8_adapter_plan.argtypes = [vp, i64, i32, vp, i64, vp]
+        L.fp8_adapter_fwd.argtypes = [ap, vp, i64, pp, vp, i64, vp, i64, vp, i64, i64, vp, vp, i64,
+                                      vp]
+        L.fp8_adapter_backward.argtypes = [ap, vp, i64, pp, vp, i64, vp, i64, vp, vp, i64, vp, i64,
+                                           i64, vp, vp, i32, vp, i64, vp]
+        for f in (L.fp8_adapter_plan, L.fp8_adapter_fwd, L.fp8_adapter_backward, L.fp8_dropout,
+                  L.fp8_dropout_cast_transpose_amax, L.fp8_scale_update, L.fp8_cast_transpose_amax, L.fp8_cast_transpose_amax_dbias,
                   L.fp8_cast_transpose_amax_dbias_noalloc, L.fp8_cast_transpose_amax_cached,
                   L.fp8_reference_copy,
                   L.fp8_produce_cast_transpose_amax, L.fp8_cast_transpose_dynamic,
@@ -645,6 +671,161 @@ def fp8_dropout_cast_transpose_amax(x: torch.Tensor, drop: Dropout, scale: torch
         _ptr(amax_cur, torch.float32, "amax_cur"), _ptr(dbias, torch.float32, "dbias"), ws,
         ws_bytes, _ptr(noop_flag, torch.int32, "noop_flag"), _stream(stream)),
         "fp8_dropout_cast_transpose_amax")
+
+
+@dataclass
+class Adapters:
+    """Low-rank adapters of one linear: a [count, rank, in] and b [count, out,
+    rank] (bf16) and each adapter's factor alpha [count] (fp32)."""
+    a: torch.Tensor
+    b: torch.Tensor
+    alpha: torch.Tensor
+
+    def desc(self) -> _AdaptersDesc:
+        if self.a.dim() != 3 or self.b.dim() != 3:
+            raise ValueError("Adapters.a and Adapters.b must be 3-D")
+        count, rank, n_in = self.a.shape
+        n_out = self.b.shape[1]
+        _need_shape(self.b, (count, n_out, rank), "Adapters.b")
+        _need_shape(self.alpha, (count,), "Adapters.alpha")
+        return _AdaptersDesc(_ptr(self.a, torch.bfloat16, "Adapters.a"),
+                             _ptr(self.b, torch.bfloat16, "Adapters.b"),
+                             _ptr(self.alpha, torch.float32, "Adapters.alpha"), count, rank, n_in,
+                             n_out)
+
+
+@dataclass
+class AdapterPlan:
+    """The rows of a batch grouped by adapter (fp8_adapter_plan), for the
+    calls of every layer until it is built again."""
+    buf: torch.Tensor
+    rows: int
+    adapters: int
+    built: bool = False
+
+    @staticmethod
+    def empty(rows: int, adapters: int, device="cuda") -> "AdapterPlan":
+        return AdapterPlan(torch.empty(fp8_adapter_plan_bytes(rows, adapters), dtype=torch.uint8,
+                                       device=device), rows, adapters)
+
+
+def fp8_adapter_plan_bytes(rows: int, adapters: int) -> int:
+    """Device bytes of the plan of a batch."""
+    n = lib().fp8_adapter_plan_bytes(rows, adapters)
+    if n < 0:
+        raise Fp8Error(n, "fp8_adapter_plan_bytes")
+    return n
+
+
+def fp8_adapter_workspace_bytes(rows: int, adapters: int, rank: int, n_in: int, n_out: int) -> int:
+    """Device workspace bytes of fp8_adapter_fwd and fp8_adapter_backward."""
+    n = lib().fp8_adapter_workspace_bytes(rows, adapters, rank, n_in, n_out)
+    if n < 0:
+        raise Fp8Error(n, "fp8_adapter_workspace_bytes")
+    return n
+
+
+def fp8_adapter_plan(row_adapter: torch.Tensor, plan: AdapterPlan, stream=None) -> None:
+    """Build `plan` for row_adapter [rows] (int32; any value outside
+    0 .. adapters - 1 marks a row without an adapter)."""
+    _need_shape(row_adapter, (plan.rows,), "row_adapter")
+    buf, size = _ws(plan.buf)
+    ids = _ptr(row_adapter, torch.int32, "row_adapter")
+    _on_current_device(row_adapter, plan.buf)
+    _check(lib().fp8_adapter_plan(ids, plan.rows, plan.adapters, buf, size, _stream(stream)),
+           "fp8_adapter_plan")
+    plan.built = True
+
+
+def _adapter_call(w: Adapters, plan: AdapterPlan, rows: int, workspace, drop):
+    if not plan.built:
+        raise ValueError("the plan has not been built (fp8_adapter_plan)")
+    if plan.rows != rows or plan.adapters != w.a.shape[0]:
+        raise ValueError(f"the plan is for {plan.rows} rows and {plan.adapters} adapters, the call "
+                         f"has {rows} and {w.a.shape[0]}")
+    if workspace is None:
+        raise ValueError("workspace is required (fp8_adapter_workspace_bytes)")
+    ws, ws_bytes = _ws(workspace)
+    dw, (buf, size) = w.desc(), _ws(plan.buf)
+    dd = None if drop is None else drop.desc()
+    _on_current_device(w.a, w.b, w.alpha, plan.buf, workspace, None if drop is None else drop.rng)
+    return (ctypes.byref(dw), buf, size, None if dd is None else ctypes.byref(dd)), ws, ws_bytes
+
+
+def _strided(t: Optional[torch.Tensor]):
+    return (None, 0) if t is None else (t.data_ptr(), _stride_of(t))
+
+
+def fp8_adapter_fwd(w: Adapters, plan: AdapterPlan, x: torch.Tensor,
+                    base: Optional[torch.Tensor], y: torch.Tensor,
+                    h: Optional[torch.Tensor] = None, drop: Optional[Dropout] = None,
+                    workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """y [rows, out] = base + h B^T with h = alpha * dropout(x) A^T of each
+    row's adapter; rows without one: y = base, h = 0.  x [rows, in], base
+    (None: zeros) and y are bf16 with unit column stride; y may be base.  h
+    [rows, rank] (fp32) is kept for fp8_adapter_backward if it is given."""
+    rows, n_out = x.shape[0], w.b.shape[1]
+    _matrix(x, (rows, w.a.shape[2]), torch.bfloat16, "x")
+    _matrix(y, (rows, n_out), torch.bfloat16, "y")
+    if base is not None:
+        _matrix(base, (rows, n_out), torch.bfloat16, "base")
+    _need_shape(h, (rows, w.a.shape[1]), "h")
+    head, ws, ws_bytes = _adapter_call(w, plan, rows, workspace, drop)
+    _on_current_device(x, y, base, h)
+    _may_share(y, (base,), "y")
+    _apart(y, x, "y", "x")
+    _check(lib().fp8_adapter_fwd(*head, *_strided(x), *_strided(base), *_strided(y), rows,
+                                 _ptr(h, torch.float32, "h"), ws, ws_bytes, _stream(stream)),
+           "fp8_adapter_fwd")
+
+
+def _apart(y: Optional[torch.Tensor], t: Optional[torch.Tensor], what: str, other: str) -> None:
+    if y is not None and t is not None and y.numel() and t.numel() \
+            and y.data_ptr() == t.data_ptr():
+        raise ValueError(f"{what} must not be {other}")
+    _may_share(y, (t,), what)
+
+
+def fp8_adapter_backward(w: Adapters, plan: AdapterPlan, x: Optional[torch.Tensor],
+                         dy: torch.Tensor, h: Optional[torch.Tensor] = None,
+                         dx_base: Optional[torch.Tensor] = None,
+                         dx: Optional[torch.Tensor] = None, da: Optional[torch.Tensor] = None,
+                         db: Optional[torch.Tensor] = None, drop: Optional[Dropout] = None,
+                         workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """The gradients of fp8_adapter_fwd for the output gradient dy [rows, out]
+    (bf16): dx [rows, in] = dx_base + ... (bf16; None: no data gradient; dx
+    may be dx_base, and dx_base None stands for zeros) and da [count, rank,
+    in], db [count, out, rank] (both fp32 or both bf16; both None: none, and
+    x and h are not read).  `drop`, x and h as in the forward."""
+    rows = dy.shape[0]
+    count, rank, n_in = w.a.shape
+    n_out = w.b.shape[1]
+    _matrix(dy, (rows, n_out), torch.bfloat16, "dy")
+    for t, n in ((dx, "dx"), (dx_base, "dx_base"), (x, "x")):
+        if t is not None:
+            _matrix(t, (rows, n_in), torch.bfloat16, n)
+    _need_shape(h, (rows, rank), "h")
+    _need_shape(da, (count, rank, n_in), "da")
+    _need_shape(db, (count, n_out, rank), "db")
+    if (da is None) != (db is None):
+        raise ValueError("da and db come together")
+    dtype = DTYPE_FP32
+    if da is not None:
+        if x is None or h is None:
+            raise ValueError("da and db need x and h")
+        if da.dtype != db.dtype or da.dtype not in (torch.float32, torch.bfloat16):
+            raise TypeError("da and db must both be fp32 or both bf16")
+        dtype = DTYPE_FP32 if da.dtype == torch.float32 else DTYPE_BF16
+    head, ws, ws_bytes = _adapter_call(w, plan, rows, workspace, drop)
+    _on_current_device(x, dy, h, dx, dx_base, da, db)
+    _may_share(dx, (dx_base,), "dx")
+    _apart(dx, dy, "dx", "dy")
+    _apart(dx, x, "dx", "x")
+    _check(lib().fp8_adapter_backward(*head, *_strided(x), *_strided(dy),
+                                      _ptr(h, torch.float32, "h"), *_strided(dx_base),
+                                      *_strided(dx), rows, _ptr(da, None, "da"),
+                                      _ptr(db, None, "db"), dtype, ws, ws_bytes, _stream(stream)),
+           "fp8_adapter_backward")
 
 
 def fp8_cast_transpose_dynamic(x: torch.Tensor, scale: torch.Tensor, out: Float8Tensor,

@@ -1,0 +1,107 @@
+// Shapes and work splits of the low-rank adapter kernels, shared by the
+// launchers and the C-ABI layer (which sizes the caller's buffers).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "dropout.h"
+
+namespace fp8dsl {
+
+// Rows of one tile: two 16-row MFMA blocks.  A tile holds rows of one adapter.
+constexpr int kAdapterTile = 32;
+constexpr int kAdapterMaxRank = 128;
+constexpr int kAdapterMaxCount = 4096;
+// Columns of one workgroup of the expand and of the weight-gradient kernel.
+constexpr int kAdapterCols = 512;
+
+// Device layout of a plan (int32 words): the batch's rows sorted by adapter,
+// every adapter's rows starting a new tile.
+//   header       {magic, rows, adapters, tiles, tiles that have an adapter}
+//   group_tile0  [adapters + 2]: first tile of each adapter, then of the rows
+//                without one, then the tile count
+//   group_rank   [adapters]: adapters before this one that have rows
+//   tile_adapter [tiles_max]: an adapter, -1 (rows without one), -2 (unused)
+//   tile_row     [32 * tiles_max]: row of each position, -1 past a group's end
+constexpr int32_t kPlanMagic = 0x414c5031;
+constexpr int kPlanHeader = 16;
+struct AdapterPlanShape {
+    int64_t rows, adapters, tiles_max;
+    int64_t group_tile0, group_rank, tile_adapter, tile_row, words;
+    AdapterPlanShape(int64_t rows_, int64_t adapters_) : rows(rows_), adapters(adapters_) {
+        const int64_t groups = std::min(adapters + 1, rows);
+        tiles_max = (rows + (kAdapterTile - 1) * groups) / kAdapterTile;
+        const auto up = [](int64_t v) { return (v + 15) / 16 * 16; };
+        group_tile0 = kPlanHeader;
+        group_rank = group_tile0 + up(adapters + 2);
+        tile_adapter = group_rank + up(adapters);
+        tile_row = tile_adapter + up(tiles_max);
+        words = tile_row + kAdapterTile * tiles_max;
+    }
+};
+
+// K parts of the contraction over C columns (workgroups per tile of the
+// shrink kernel): enough for about two workgroups per CU, each at least 256
+// columns, at most 16.
+inline int adapter_parts(int64_t tiles, int64_t C) {
+    const int64_t want = (512 + tiles - 1) / std::max<int64_t>(tiles, 1);
+    return (int)std::max<int64_t>(1, std::min<int64_t>({want, C / 256, 16}));
+}
+
+// Tiles of one weight-gradient workgroup: a partial sum of R fp32 per column
+// is written and read per workgroup, against 32 rows of bf16 per tile.
+inline int64_t adapter_chunk(int64_t tiles, int64_t rank, int64_t in, int64_t out) {
+    const int64_t blocks = (in + kAdapterCols - 1) / kAdapterCols +
+                           (out + kAdapterCols - 1) / kAdapterCols;
+    return std::max<int64_t>(1, std::min<int64_t>(rank / 4, tiles * blocks / 512));
+}
+
+// Partial sums of the weight gradients: one per (chunk of tiles, adapter
+// with rows in it); chunk + rank of the adapter is distinct for each.
+inline int64_t adapter_slots(const AdapterPlanShape &p, int64_t chunk) {
+    return (p.tiles_max + chunk - 1) / chunk + std::min(p.adapters, p.rows);
+}
+
+// Workspace: K-part sums of h or g, then the weight gradients' partial sums.
+struct AdapterWorkspace {
+    int64_t sums, grads, bytes;
+    AdapterWorkspace(const AdapterPlanShape &p, int64_t rank, int64_t in, int64_t out) {
+        const int64_t parts = std::max(adapter_parts(p.tiles_max, in),
+                                       adapter_parts(p.tiles_max, out));
+        sums = (parts * p.rows * rank * 4 + 255) / 256 * 256;
+        grads = adapter_slots(p, adapter_chunk(p.tiles_max, rank, in, out)) * rank * (in + out) * 4;
+        bytes = sums + grads;
+    }
+};
+
+struct AdapterArgs {
+    const uint16_t *a, *b;      // bf16 [count, rank, in], [count, out, rank]
+    const float *alpha;         // [count]
+    int32_t count, rank;
+    int64_t in, out;
+};
+
+hipError_t launch_adapter_plan(const int32_t *row_adapter, const AdapterPlanShape &shape,
+                               int32_t *plan, hipStream_t stream);
+
+hipError_t launch_adapter_fwd(const AdapterArgs &w, const AdapterPlanShape &shape,
+                              const int32_t *plan, const DropoutArgs &drop, const uint16_t *x,
+                              int64_t ldx, const uint16_t *base, int64_t ldbase, uint16_t *y,
+                              int64_t ldy, float *h, void *ws, hipStream_t stream);
+
+// dx may be null (no data gradient), da and db both null (no weight gradient).
+hipError_t launch_adapter_backward(const AdapterArgs &w, const AdapterPlanShape &shape,
+                                   const int32_t *plan, const DropoutArgs &drop,
+                                   const uint16_t *x, int64_t ldx, const uint16_t *dy,
+                                   int64_t lddy, const float *h, const uint16_t *base,
+                                   int64_t ldbase, uint16_t *dx, int64_t lddx, void *da, void *db,
+                                   int out_dtype, void *ws, hipStream_t stream);
+
+// da = db = 0 (a batch without rows).
+hipError_t launch_adapter_clear_grads(const AdapterArgs &w, void *da, void *db, int out_dtype,
+                                      hipStream_t stream);
+
+}  // namespace fp8dsl

@@ -9,6 +9,7 @@
 #include <math.h>
 #include <string.h>
 
+#include "adapter.h"
 #include "fp8dsl_internal.h"
 
 using namespace fp8dsl;
@@ -77,6 +78,48 @@ int dropout_args(const fp8_dropout_t *drop, DropoutArgs *out) {
     out->threshold = (uint32_t)t;
     out->factor = (float)(65536.0 / (65536.0 - t));
     return FP8_OK;
+}
+
+// Sizes of an adapter call.
+int check_adapter_sizes(int64_t rows, int32_t adapters, int32_t rank, int64_t in, int64_t out) {
+    constexpr int64_t kMost = (int64_t)1 << 22;
+    if (rows < 0 || rows > ((int64_t)1 << 28) || adapters < 1 || adapters > kAdapterMaxCount)
+        return FP8_ERR_SHAPE;
+    if (rank < 8 || rank > kAdapterMaxRank || (rank % 8) != 0) return FP8_ERR_SHAPE;
+    if (in < 8 || in > kMost || (in % 8) != 0 || out < 8 || out > kMost || (out % 8) != 0)
+        return FP8_ERR_SHAPE;
+    return FP8_OK;
+}
+
+// What the two adapter calls share: the adapters, the plan, the workspace and
+// the dropout (rng null where there is none).
+int check_adapter(const fp8_adapters_t *w, const void *plan, int64_t plan_bytes,
+                  const fp8_dropout_t *drop, int64_t rows, const void *workspace,
+                  int64_t workspace_bytes, DropoutArgs *args) {
+    if (w == nullptr) return FP8_ERR_NULL;
+    if (int e = check_adapter_sizes(rows, w->count, w->rank, w->in, w->out)) return e;
+    *args = {nullptr, 0, 1.0f};
+    if (drop) {
+        if (int e = dropout_args(drop, args)) return e;
+    }
+    if (rows == 0) return FP8_OK;
+    if (!w->a || !w->b || !w->alpha || !plan || !workspace) return FP8_ERR_NULL;
+    if (!aligned16(w->a) || !aligned16(w->b) || (reinterpret_cast<uintptr_t>(w->alpha) & 3) != 0 ||
+        !aligned16(plan) || !aligned16(workspace))
+        return FP8_ERR_ALIGN;
+    if (plan_bytes < fp8_adapter_plan_bytes(rows, w->count) ||
+        workspace_bytes < fp8_adapter_workspace_bytes(rows, w->count, w->rank, w->in, w->out))
+        return FP8_ERR_SHAPE;
+    return FP8_OK;
+}
+
+// A row stride of a [rows, cols] bf16 tensor.
+bool bad_stride(int64_t ld, int64_t cols, int64_t rows) {
+    return ld < cols || (ld % 8) != 0 || ld > INT64_MAX / 2 / (rows > 0 ? rows : 1);
+}
+
+AdapterArgs adapter_args(const fp8_adapters_t *w) {
+    return {w->a, w->b, w->alpha, w->count, w->rank, w->in, w->out};
 }
 
 // Scratch of fp8_cast_transpose_amax_dbias_noalloc: each GPU holds its own
@@ -446,6 +489,83 @@ int fp8_produce_modulate_backward(int32_t op, const uint16_t *dy, int64_t lddy,
     return status_of(launch_modulate_backward(op == FP8_PRODUCE_MODULATE_FINITE, dy, lddy, x, ldx,
                                               a, lda, b, ldb, dx, lddx, da, ldda, db, lddb, rows,
                                               cols, static_cast<hipStream_t>(stream)));
+}
+
+int64_t fp8_adapter_plan_bytes(int64_t rows, int32_t adapters) {
+    if (int e = check_adapter_sizes(rows, adapters, 8, 8, 8)) return e;
+    return AdapterPlanShape(rows, adapters).words * (int64_t)sizeof(int32_t);
+}
+
+int fp8_adapter_plan(const int32_t *row_adapter, int64_t rows, int32_t adapters, void *plan,
+                     int64_t plan_bytes, fp8_stream_t stream) {
+    const int64_t need = fp8_adapter_plan_bytes(rows, adapters);
+    if (need < 0) return (int)need;
+    if (rows == 0) return FP8_OK;
+    if (row_adapter == nullptr || plan == nullptr) return FP8_ERR_NULL;
+    if ((reinterpret_cast<uintptr_t>(row_adapter) & 3) != 0 || !aligned16(plan))
+        return FP8_ERR_ALIGN;
+    if (plan_bytes < need) return FP8_ERR_SHAPE;
+    return status_of(launch_adapter_plan(row_adapter, AdapterPlanShape(rows, adapters),
+                                         static_cast<int32_t *>(plan),
+                                         static_cast<hipStream_t>(stream)));
+}
+
+int64_t fp8_adapter_workspace_bytes(int64_t rows, int32_t adapters, int32_t rank, int64_t in,
+                                    int64_t out) {
+    if (int e = check_adapter_sizes(rows, adapters, rank, in, out)) return e;
+    return AdapterWorkspace(AdapterPlanShape(rows, adapters), rank, in, out).bytes;
+}
+
+int fp8_adapter_fwd(const fp8_adapters_t *w, const void *plan, int64_t plan_bytes,
+                    const fp8_dropout_t *drop, const uint16_t *x, int64_t ldx,
+                    const uint16_t *base, int64_t ldbase, uint16_t *y, int64_t ldy, int64_t rows,
+                    float *h, void *workspace, int64_t workspace_bytes, fp8_stream_t stream) {
+    DropoutArgs args;
+    if (int e = check_adapter(w, plan, plan_bytes, drop, rows, workspace, workspace_bytes, &args))
+        return e;
+    if (bad_stride(ldx, w->in, rows) || bad_stride(ldy, w->out, rows) ||
+        (base && bad_stride(ldbase, w->out, rows)))
+        return FP8_ERR_SHAPE;
+    if (rows == 0) return FP8_OK;
+    if (x == nullptr || y == nullptr) return FP8_ERR_NULL;
+    if (!aligned16(x) || !aligned16(base) || !aligned16(y) || !aligned16(h)) return FP8_ERR_ALIGN;
+    return status_of(launch_adapter_fwd(adapter_args(w), AdapterPlanShape(rows, w->count),
+                                        static_cast<const int32_t *>(plan), args, x, ldx, base,
+                                        ldbase, y, ldy, h, workspace,
+                                        static_cast<hipStream_t>(stream)));
+}
+
+int fp8_adapter_backward(const fp8_adapters_t *w, const void *plan, int64_t plan_bytes,
+                         const fp8_dropout_t *drop, const uint16_t *x, int64_t ldx,
+                         const uint16_t *dy, int64_t lddy, const float *h,
+                         const uint16_t *dx_base, int64_t lddxbase, uint16_t *dx, int64_t lddx,
+                         int64_t rows, void *da, void *db, int32_t out_dtype, void *workspace,
+                         int64_t workspace_bytes, fp8_stream_t stream) {
+    DropoutArgs args;
+    if (int e = check_adapter(w, plan, plan_bytes, drop, rows, workspace, workspace_bytes, &args))
+        return e;
+    if (out_dtype != FP8_DTYPE_FP32 && out_dtype != FP8_DTYPE_BF16) return FP8_ERR_ARG;
+    if ((da == nullptr) != (db == nullptr)) return FP8_ERR_ARG;
+    if (bad_stride(lddy, w->out, rows) || (da && bad_stride(ldx, w->in, rows)) ||
+        (dx && (bad_stride(lddx, w->in, rows) ||
+                (dx_base && bad_stride(lddxbase, w->in, rows)))))
+        return FP8_ERR_SHAPE;
+    if (!aligned16(da) || !aligned16(db)) return FP8_ERR_ALIGN;
+    const AdapterPlanShape shape(rows, w->count);
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (rows == 0) {
+        if (da == nullptr) return FP8_OK;
+        return status_of(launch_adapter_clear_grads(adapter_args(w), da, db, out_dtype, s));
+    }
+    if (dy == nullptr || (da && (x == nullptr || h == nullptr))) return FP8_ERR_NULL;
+    if (!aligned16(dy) || (da && (!aligned16(x) || !aligned16(h))) ||
+        (dx && (!aligned16(dx) || !aligned16(dx_base))))
+        return FP8_ERR_ALIGN;
+    if (dx == nullptr && da == nullptr) return FP8_OK;
+    return status_of(launch_adapter_backward(adapter_args(w), shape,
+                                             static_cast<const int32_t *>(plan), args, x, ldx, dy,
+                                             lddy, h, dx_base, lddxbase, dx, lddx, da, db,
+                                             out_dtype, workspace, s));
 }
 
 int fp8_cast_transpose_dynamic(const void *x, int32_t src, int64_t rows, int64_t cols,

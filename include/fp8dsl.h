@@ -22,6 +22,8 @@
  * gradient (fp8_produce_cast_transpose_amax, fp8_produce_modulate_backward),
  * dropout from a counter-based generator, alone or fused into the cast
  * (fp8_dropout, fp8_dropout_cast_transpose_amax),
+ * low-rank adapters of many requests beside a shared projection, forward and
+ * backward (fp8_adapter_plan, fp8_adapter_fwd, fp8_adapter_backward),
  * dynamic scaling as the comparator (fp8_cast_transpose_dynamic), the
  * forward with FP8 output and output amax (fp8_linear_fwd_fp8out), the three
  * products split over K through a caller workspace for shapes that alone
@@ -644,6 +646,117 @@ int fp8_linear_dgrad_ws(const fp8_tensor_t *dy, const fp8_tensor_t *w, uint16_t 
 int fp8_linear_wgrad_ws(const fp8_tensor_t *dy, const fp8_tensor_t *x, void *dw,
                         int32_t out_dtype, void *workspace, int64_t workspace_bytes,
                         fp8_stream_t stream);
+
+/*
+ * Low-rank adapters of many requests beside a shared projection.
+ *
+ * A linear whose weight is shared by every row of a batch (a cached FP8
+ * weight, or a frozen one in fine-tuning) takes a correction of its own for
+ * each row's request: adapter a holds A_a [rank, in] and B_a [out, rank], and
+ * row r belongs to adapter row_adapter[r], or to none.
+ *
+ *   forward    h[r]  = alpha[a] * dropout(x[r]) A_a^T               (fp32)
+ *              y[r]  = bf16(base[r] + h[r] B_a^T)
+ *   backward   g[r]  = alpha[a] * dy[r] B_a                         (fp32)
+ *              dx[r] = bf16(dx_base[r] + f * kept * (g[r] A_a))
+ *              dA_a  = sum over the adapter's rows of g[r]^T dropout(x[r])
+ *              dB_a  = sum over the adapter's rows of dy[r]^T h[r]
+ *
+ * base is what the shared projection wrote (fp8_linear_fwd, fp8_linear_dgrad).
+ * Products and sums are taken in fp32; the products over `rank` see h and g as
+ * sums of bf16 parts, within 2^-16 of each value (2^-23 where the result is
+ * stored in fp32).  Each row's result depends on that row and its adapter
+ * alone.  Repeated calls give identical bits.
+ */
+typedef struct fp8_adapters {
+    const uint16_t *a;      /* device bf16 [count, rank, in], 16-byte aligned  */
+    const uint16_t *b;      /* device bf16 [count, out, rank], 16-byte aligned */
+    const float *alpha;     /* device [count]: each adapter's factor           */
+    int32_t count;          /* 1 .. FP8DSL_ADAPTERS_MAX                        */
+    int32_t rank;           /* 8 .. FP8DSL_ADAPTER_RANK_MAX, a multiple of 8   */
+    int64_t in;             /* features of x, a multiple of 8, 8 .. 2^22       */
+    int64_t out;            /* features of y, a multiple of 8, 8 .. 2^22       */
+} fp8_adapters_t;
+
+#define FP8DSL_ADAPTERS_MAX 4096
+#define FP8DSL_ADAPTER_RANK_MAX 128
+
+/*
+ * fp8_adapter_plan -- groups the rows of a batch by adapter.
+ *
+ * A batch's requests are known once per step, so this is called once per step
+ * and its plan is used by the calls of every layer.  Rows may come in any
+ * order; an adapter may own any number of them.
+ *
+ * row_adapter  device int32 [rows]; a value outside 0 .. adapters - 1 (-1, say)
+ *              marks a row without an adapter.
+ * plan         device, 16-byte aligned, fp8_adapter_plan_bytes(rows,
+ *              adapters) bytes, owned by the caller; read by the calls below
+ *              until it is built again.
+ * 0 <= rows <= 2^28, 1 <= adapters <= FP8DSL_ADAPTERS_MAX.  rows 0: no work.
+ * fp8_adapter_plan_bytes returns a negative status for sizes out of range.
+ * Errors: FP8_ERR_SHAPE (sizes, plan_bytes), FP8_ERR_NULL, FP8_ERR_ALIGN,
+ * FP8_ERR_LAUNCH / FP8_ERR_DEVICE.
+ */
+int64_t fp8_adapter_plan_bytes(int64_t rows, int32_t adapters);
+int fp8_adapter_plan(const int32_t *row_adapter, int64_t rows, int32_t adapters, void *plan,
+                     int64_t plan_bytes, fp8_stream_t stream);
+
+/* Device workspace (bytes) of either call below; a negative status for sizes
+ * out of range. */
+int64_t fp8_adapter_workspace_bytes(int64_t rows, int32_t adapters, int32_t rank, int64_t in,
+                                    int64_t out);
+
+/*
+ * fp8_adapter_fwd -- y = base + the adapters' forward.
+ *
+ * plan      built for these rows and w->count (a buffer that holds no such
+ *           plan leaves the outputs unwritten).
+ * drop      the dropout of x [rows, in], or NULL.
+ * x         device bf16 [rows, in], row stride ldx.
+ * base, y   device bf16 [rows, out], row strides ldbase, ldy.  base NULL stands
+ *           for zeros.  y may be base (same pointer and stride: rows without an
+ *           adapter are then left untouched), else must not overlap the inputs.
+ *           Rows without an adapter: y = base.
+ * h         device fp32 [rows, rank], 16-byte aligned, for the backward, or
+ *           NULL.  Rows without an adapter: 0.
+ * workspace device, 16-byte aligned, at least fp8_adapter_workspace_bytes;
+ *           its contents on entry do not matter and on return are
+ *           unspecified; calls that overlap on one workspace race.
+ * Strides are multiples of 8 and at least the row's length; tensors 16-byte
+ * aligned.  rows 0: no work.
+ * Errors: FP8_ERR_NULL, FP8_ERR_SHAPE (sizes, strides, plan_bytes,
+ * workspace_bytes), FP8_ERR_ALIGN, FP8_ERR_ARG (p), FP8_ERR_LAUNCH /
+ * FP8_ERR_DEVICE.
+ */
+int fp8_adapter_fwd(const fp8_adapters_t *w, const void *plan, int64_t plan_bytes,
+                    const fp8_dropout_t *drop, const uint16_t *x, int64_t ldx,
+                    const uint16_t *base, int64_t ldbase, uint16_t *y, int64_t ldy, int64_t rows,
+                    float *h, void *workspace, int64_t workspace_bytes, fp8_stream_t stream);
+
+/*
+ * fp8_adapter_backward -- the gradients of fp8_adapter_fwd.
+ *
+ * drop, x   those of the forward (x is read for da only).
+ * dy        device bf16 [rows, out], row stride lddy.
+ * h         as the forward wrote it (read for db only).
+ * dx_base, dx  device bf16 [rows, in], row strides lddxbase, lddx, as base and
+ *           y of the forward (dx_base: fp8_linear_dgrad's output); dx NULL: no
+ *           data gradient.
+ * da, db    device [count, rank, in] and [count, out, rank] in out_dtype
+ *           (FP8_DTYPE_FP32 or FP8_DTYPE_BF16), 16-byte aligned, overwritten;
+ *           an adapter without rows gets zeros.  Both NULL: no weight
+ *           gradients (x and h are not read).
+ * workspace as the forward's.  rows 0: da and db are cleared.
+ * Errors: those of fp8_adapter_fwd; FP8_ERR_ARG also for another out_dtype and
+ * for one of da, db alone.
+ */
+int fp8_adapter_backward(const fp8_adapters_t *w, const void *plan, int64_t plan_bytes,
+                         const fp8_dropout_t *drop, const uint16_t *x, int64_t ldx,
+                         const uint16_t *dy, int64_t lddy, const float *h,
+                         const uint16_t *dx_base, int64_t lddxbase, uint16_t *dx, int64_t lddx,
+                         int64_t rows, void *da, void *db, int32_t out_dtype, void *workspace,
+                         int64_t workspace_bytes, fp8_stream_t stream);
 
 /* Human-readable name of a status code (static storage). */
 const char *fp8_status_string(int status);

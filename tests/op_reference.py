@@ -57,3 +57,34 @@ def dropout(x32: np.ndarray, mask: np.ndarray, f: np.float32, residual32=None) -
     with np.errstate(all="ignore"):
         t = np.where(mask, x32.astype(np.float32) * f, np.float32(0))
         return t if residual32 is None else residual32.astype(np.float32) + t
+
+
+def adapter_forward(x, a, b, alpha, ids, base=None, mask=None, f=1.0):
+    """float64 (y, h); ids outside [0, count) mark rows without an adapter."""
+    rows, count = x.shape[0], a.shape[0]
+    xd = x if mask is None else np.where(mask, x, 0.0)
+    y = np.zeros((rows, b.shape[1])) if base is None else base.astype(np.float64).copy()
+    h = np.zeros((rows, a.shape[1]))
+    for i in range(count):
+        at = np.nonzero(ids == i)[0]
+        if at.size:
+            h[at] = alpha[i] * f * (xd[at] @ a[i].T)
+            y[at] += h[at] @ b[i].T
+    return y, h
+
+
+def adapter_backward(x, a, b, alpha, ids, dy, h, base=None, mask=None, f=1.0):
+    """float64 (dx, da, db, g)."""
+    rows, count = x.shape[0], a.shape[0]
+    keep = np.ones(x.shape) if mask is None else mask.astype(np.float64)
+    xd = np.where(keep > 0, x, 0.0) * f
+    dx = np.zeros(x.shape) if base is None else base.astype(np.float64).copy()
+    da, db, g = np.zeros(a.shape), np.zeros(b.shape), np.zeros((rows, a.shape[1]))
+    for i in range(count):
+        at = np.nonzero(ids == i)[0]
+        if at.size:
+            g[at] = alpha[i] * (dy[at] @ b[i])
+            dx[at] += f * keep[at] * (g[at] @ a[i])
+            da[i] = g[at].T @ xd[at]
+            db[i] = dy[at].T @ h[at]
+    return dx, da, db, g
