@@ -44,10 +44,10 @@ struct AdapterPlanShape {
 };
 
 // K parts of the contraction over C columns (workgroups per tile of the
-// shrink kernel): enough for about two workgroups per CU, each at least 256
+// shrink kernel): enough for a workgroup per CU, each at least 256
 // columns, at most 16.
 inline int adapter_parts(int64_t tiles, int64_t C) {
-    const int64_t want = (512 + tiles - 1) / std::max<int64_t>(tiles, 1);
+    const int64_t want = 256 / std::max<int64_t>(tiles, 1);
     return (int)std::max<int64_t>(1, std::min<int64_t>({want, C / 256, 16}));
 }
 

@@ -103,7 +103,7 @@ struct PlanView {
     int32_t rows, adapters;
     // A buffer that no plan of these sizes was written to has no work in it.
     __device__ __forceinline__ bool built() const {
-        return header[0] == kPlanMagic && header[1] == rows && header[2] == adapters;
+        return (header[0] == kPlanMagic) & (header[1] == rows) & (header[2] == adapters);
     }
 };
 
@@ -212,37 +212,33 @@ __device__ __forceinline__ int shrink_rank(int jb, int col) {
 
 template <int RP, bool TRANS>
 __device__ __forceinline__ void load_shrink_weights(const uint16_t *w, int64_t C, int R, int64_t k,
-                                                    bool k_ok, int col, u32x4 (&out)[RP / 16]) {
+                                                    int col, u32x4 (&out)[RP / 16]) {
     constexpr int W = RP / 16;
+    // Ranks past R read rank 0: their result columns are not stored.
     if constexpr (!TRANS) {
 #pragma unroll
         for (int jb = 0; jb < W; ++jb) {
             const int j = jb * 16 + col;
-            out[jb] = u32x4{0u, 0u, 0u, 0u};
-            if (k_ok && j < R) out[jb] = *reinterpret_cast<const u32x4 *>(w + j * C + k);
+            out[jb] = *reinterpret_cast<const u32x4 *>(w + (j < R ? j : 0) * C + k);
         }
     } else {
         uint32_t t[8][(W + 1) / 2];
-        const int j = col * W;
+        const int j = col * W < R ? col * W : 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
+            const uint16_t *p = w + (k + i) * R + j;
+            if constexpr (W == 1) {
+                t[i][0] = *p;
+            } else if constexpr (W == 2) {
+                t[i][0] = *reinterpret_cast<const uint32_t *>(p);
+            } else if constexpr (W == 4) {
+                const u32x2 v = *reinterpret_cast<const u32x2 *>(p);
+                t[i][0] = v.x;
+                t[i][1] = v.y;
+            } else {
+                const u32x4 v = *reinterpret_cast<const u32x4 *>(p);
 #pragma unroll
-            for (int d = 0; d < (W + 1) / 2; ++d) t[i][d] = 0u;
-            if (k_ok && j < R) {
-                const uint16_t *p = w + (k + i) * R + j;
-                if constexpr (W == 1) {
-                    t[i][0] = *p;
-                } else if constexpr (W == 2) {
-                    t[i][0] = *reinterpret_cast<const uint32_t *>(p);
-                } else if constexpr (W == 4) {
-                    const u32x2 v = *reinterpret_cast<const u32x2 *>(p);
-                    t[i][0] = v.x;
-                    t[i][1] = v.y;
-                } else {
-                    const u32x4 v = *reinterpret_cast<const u32x4 *>(p);
-#pragma unroll
-                    for (int d = 0; d < 4; ++d) t[i][d] = v[d];
-                }
+                for (int d = 0; d < 4; ++d) t[i][d] = v[d];
             }
         }
 #pragma unroll
@@ -273,11 +269,17 @@ __global__ __launch_bounds__(THREADS) void adapter_shrink_kernel(
     __shared__ float red[WAVES][16 * RP];
     __shared__ int rows[TILE];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, g = lane >> 4;
-    if (!plan.built()) return;
+    // All of the plan's words for this tile in one round trip.
+    const bool built = plan.built();
     const int tile = blockIdx.x, a = plan.tile_adapter[tile];
-    if (a < 0) return;
-    if (tid < TILE) rows[tid] = plan.tile_row[tile * TILE + tid];
-    __syncthreads();
+    int my_row[2];
+#pragma unroll
+    for (int mb = 0; mb < 2; ++mb) my_row[mb] = plan.tile_row[(int64_t)tile * TILE + 16 * mb + col];
+    if (!built || a < 0) return;
+    if (tid < 16) {
+        rows[tid] = my_row[0];
+        rows[16 + tid] = my_row[1];
+    }
     const uint16_t *w = weights + (int64_t)a * R * C;
 
     int64_t kw = ((kpart + WAVES - 1) / WAVES + 31) / 32 * 32;   // a wave's columns
@@ -286,12 +288,9 @@ __global__ __launch_bounds__(THREADS) void adapter_shrink_kernel(
 
     const uint16_t *px[2];
     int64_t row[2];
-    bool row_ok[2];
 #pragma unroll
     for (int mb = 0; mb < 2; ++mb) {
-        const int r = rows[mb * 16 + col];
-        row_ok[mb] = r >= 0;
-        row[mb] = max(r, 0);
+        row[mb] = max(my_row[mb], 0);        // a position without a row reads row 0, unstored
         px[mb] = src + row[mb] * ld;
     }
     f32x4 acc[2][RP / 16];
@@ -302,17 +301,24 @@ __global__ __launch_bounds__(THREADS) void adapter_shrink_kernel(
 
     constexpr int U = RP >= 128 ? 2 : 4;
     for (int64_t kk = k0; kk < k1; kk += 32 * U) {
+        // Past the end both operands read the part's first columns, and x
+        // counts as zero there.
         u32x4 xs[U][2], ws[U][RP / 16];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int64_t k = kk + 32 * u + 8 * g;
-            const bool ok = k < k1;
+            const int64_t k = kk + 32 * u + 8 * g, kc = k < k1 ? k : k0;
 #pragma unroll
-            for (int mb = 0; mb < 2; ++mb) {
-                xs[u][mb] = u32x4{0u, 0u, 0u, 0u};
-                if (ok && row_ok[mb]) xs[u][mb] = *reinterpret_cast<const u32x4 *>(px[mb] + k);
-            }
-            load_shrink_weights<RP, TRANS>(w, C, R, k, ok, col, ws[u]);
+            for (int mb = 0; mb < 2; ++mb) xs[u][mb] = *reinterpret_cast<const u32x4 *>(px[mb] + kc);
+            load_shrink_weights<RP, TRANS>(w, C, R, kc, col, ws[u]);
+        }
+        if (kk + 32 * U > k1) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int mb = 0; mb < 2; ++mb)
+#pragma unroll
+                    for (int d = 0; d < 4; ++d)
+                        xs[u][mb][d] = kk + 32 * u + 8 * g < k1 ? xs[u][mb][d] : 0u;
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -352,209 +358,269 @@ __global__ __launch_bounds__(THREADS) void adapter_shrink_kernel(
 
 // ---- expand: out = base + f keep (h W) ---------------------------------------
 
-// Eight ranks j .. j + 7 of one row of h, the K parts added in order.
-__device__ __forceinline__ void load_h8(const float *h, int parts, int64_t part_stride, int R,
-                                        int64_t row, int j, bool ok, float v[8]) {
+// L bf16 columns, as loaded and stored.
+template <int L>
+struct Cols {
+    uint32_t d[L / 2];
+    __device__ __forceinline__ void load(const uint16_t *p) {
+        if constexpr (L == 8) {
+            const u32x4 v = *reinterpret_cast<const u32x4 *>(p);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-    if (!ok) return;
-    const float *p = h + row * R + j;
-    for (int s = 0; s < parts; ++s, p += part_stride) {
-        const f32x4 a = *reinterpret_cast<const f32x4 *>(p);
-        const f32x4 b = *reinterpret_cast<const f32x4 *>(p + 4);
+            for (int i = 0; i < 4; ++i) d[i] = v[i];
+        } else {
+            const u32x2 v = *reinterpret_cast<const u32x2 *>(p);
+            d[0] = v.x;
+            d[1] = v.y;
+        }
+    }
+    __device__ __forceinline__ void store(uint16_t *p) const {
+        if constexpr (L == 8)
+            *reinterpret_cast<u32x4 *>(p) = u32x4{d[0], d[1], d[2], d[3]};
+        else
+            *reinterpret_cast<u32x2 *>(p) = u32x2{d[0], d[1]};
+    }
+    __device__ __forceinline__ void clear_unless(bool ok) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[i] += a[i];
-            v[4 + i] += b[i];
+        for (int i = 0; i < L / 2; ++i) d[i] = ok ? d[i] : 0u;
+    }
+};
+
+// The dropout's numbers of L columns c .. (c a multiple of L).
+template <int L>
+__device__ __forceinline__ void numbers_of(const DropoutKey &key, int64_t row, int64_t c, int64_t C,
+                                           uint32_t (&n)[L / 2]) {
+    uint32_t w[4];
+    dropout_words(key, (uint64_t)(row * (C >> 3) + (c >> 3)), w);
+#pragma unroll
+    for (int d = 0; d < L / 2; ++d) n[d] = L == 8 ? w[d] : (c & 4) ? w[2 + d] : w[d];
+}
+
+// The weights of a lane's 8 columns c .. as MFMA columns of 8 blocks (block t:
+// column c + t), S contraction steps of 32 ranks each.
+//   TRANS false, W [C, R] (B in the forward): 8 ranks of a column are 16 bytes.
+//   TRANS true, W [R, C] (A in the backward): a lane reads its 8 columns of its
+//   8 ranks and turns them in registers.
+template <int RP, bool TRANS, int S>
+__device__ __forceinline__ void load_expand_weights(const uint16_t *w, int64_t C, int R, int64_t c,
+                                                    int g, u32x4 (&ws)[8][S]) {
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+        const int j = RP == 16 ? 8 * (g & 1) : 32 * s + 8 * g;
+        const bool ok = j < R;
+        const int js = ok ? j : 0;
+        if constexpr (!TRANS) {
+#pragma unroll
+            for (int t = 0; t < 8; ++t)
+                ws[t][s] = *reinterpret_cast<const u32x4 *>(w + (c + t) * R + js);
+        } else {
+            u32x4 in[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                in[i] = *reinterpret_cast<const u32x4 *>(w + (int64_t)(js + i) * C + c);
+#pragma unroll
+            for (int t = 0; t < 8; ++t)
+#pragma unroll
+                for (int d = 0; d < 4; ++d)
+                    ws[t][s][d] = (t & 1) ? high_halves(in[2 * d][t >> 1], in[2 * d + 1][t >> 1])
+                                          : low_halves(in[2 * d][t >> 1], in[2 * d + 1][t >> 1]);
+        }
+        if (RP > 16 || R < 16) {
+#pragma unroll
+            for (int t = 0; t < 8; ++t)
+#pragma unroll
+                for (int d = 0; d < 4; ++d) ws[t][s][d] = ok ? ws[t][s][d] : 0u;
         }
     }
 }
 
-// out = base + f keep v for eight columns of a row.
-template <bool DROP>
-__device__ __forceinline__ void add_store8(const float v[8], const uint16_t *base, uint16_t *out,
-                                           uint64_t e, const DropoutArgs &drop) {
-    u32x4 b = {0u, 0u, 0u, 0u}, o;
-    if (base != nullptr) b = *reinterpret_cast<const u32x4 *>(base);
-    uint32_t w[4] = {0u, 0u, 0u, 0u};
-    if constexpr (DROP) {
-        const DropoutKey key(drop.rng);
-        dropout_words(key, e, w);
-    }
-#pragma unroll
-    for (int d = 0; d < 4; ++d) {
-        float lo = v[2 * d], hi = v[2 * d + 1];
-        if constexpr (DROP) {
-            lo = (w[d] & 0xFFFFu) >= drop.threshold ? lo * drop.factor : 0.0f;
-            hi = (w[d] >> 16) >= drop.threshold ? hi * drop.factor : 0.0f;
-        }
-        lo += __uint_as_float(b[d] << 16);
-        hi += __uint_as_float(b[d] & 0xFFFF0000u);
-        o[d] = bf16_rne(lo) | (bf16_rne(hi) << 16);
-    }
-    *reinterpret_cast<u32x4 *>(out) = o;
+// Which chunk of tiles a workgroup takes: column blocks are the grid's fastest
+// dimension, so that workgroups in flight together cover whole rows and with
+// them all memory channels; the chunks are spread over the other two.
+constexpr int64_t GRID_Y = 32768;
+__device__ __forceinline__ int64_t chunk_of_block() {
+    return (int64_t)blockIdx.z * GRID_Y + blockIdx.y;
+}
+dim3 grid_of(int64_t blocks, int64_t chunks) {
+    return dim3((unsigned)blocks, (unsigned)std::min(chunks, GRID_Y),
+                (unsigned)((chunks + GRID_Y - 1) / GRID_Y));
 }
 
-// Grid: (tiles, blocks of 512 columns).  The product is taken transposed
-// (weights' columns are the MFMA rows), so a lane holds adjacent columns of
-// one row of the output.  TRANS false: W [C, R] (B in the forward), MFMA row q
-// of block t is column 8 (q / 4) + 4 t + q % 4 of 32: a lane holds 8 columns.
-// TRANS true: W [R, C] (A in the backward): a lane reads 8 columns of its 8
-// ranks and turns them in registers; row q of block t is column
-// 32 (q % 4) + 8 (q / 4) + t of 128: a lane holds 4 x 8 columns.
+// Grid: (blocks of 512 columns, chunks of tiles).  h is the MFMA's row operand
+// and a lane's 8 adjacent columns are 8 column blocks, so a lane holds 8
+// adjacent columns of rows 4 g .. 4 g + 3 of the result and the sixteen lanes of
+// a row load the base and store the output in one run of 256 bytes.  The
+// workgroup sums h's parts, splits h and lays it out in LDS as MFMA operands
+// once for its four waves (each wave reading it from memory by itself made the
+// L1 the bound: 2.3 GB through it for 200 MB of base and output).  A wave keeps
+// the weights of its columns while its tiles' adapter stays the same.
 template <int RP, bool TRANS, bool DROP>
-__global__ __launch_bounds__(THREADS) void adapter_expand_kernel(
-    PlanView plan, const float *h, int parts, int64_t part_stride,
+__global__ __launch_bounds__(THREADS, 2) void adapter_expand_kernel(
+    PlanView plan, int tiles_max, int chunk, const float *h, int parts, int64_t part_stride,
     const uint16_t *__restrict__ weights, int R, int64_t C, const uint16_t *base, int64_t ldbase,
     uint16_t *out, int64_t ldo, float *h_out, DropoutArgs drop) {
-    __shared__ int rows[TILE];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, g = lane >> 4;
-    if (!plan.built()) return;
-    const int tile = blockIdx.x, a = plan.tile_adapter[tile];
-    if (a == -2) return;
-    if (tid < TILE) rows[tid] = plan.tile_row[tile * TILE + tid];
-    __syncthreads();
-    if (h_out != nullptr && blockIdx.y == 0 && (a < 0 || parts > 1)) {
-        for (int e = tid; e < TILE * (R / 8); e += THREADS) {
-            const int r = rows[e / (R / 8)], j = e % (R / 8) * 8;
-            if (r < 0) continue;
-            float v[8];
-            load_h8(h, parts, part_stride, R, r, j, a >= 0, v);
-            float *p = h_out + (int64_t)r * R + j;
-            *reinterpret_cast<f32x4 *>(p) = f32x4{v[0], v[1], v[2], v[3]};
-            *reinterpret_cast<f32x4 *>(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
-        }
-    }
-    const int64_t c0 = (int64_t)blockIdx.y * kAdapterCols;
-    if (a < 0) {
-        // Rows without an adapter: out = base.
-        if (base == out && ldbase == ldo) return;
-        const int64_t c = c0 + 8 * lane;
-        if (c >= C) return;
-        for (int p = wave; p < TILE; p += WAVES) {
-            if (rows[p] < 0) break;
-            u32x4 v = {0u, 0u, 0u, 0u};
-            if (base) v = *reinterpret_cast<const u32x4 *>(base + rows[p] * ldbase + c);
-            *reinterpret_cast<u32x4 *>(out + rows[p] * ldo + c) = v;
-        }
-        return;
-    }
-    const uint16_t *w = weights + (int64_t)a * R * C;
-
-    // h as the MFMA columns: S contraction steps of 32 ranks, high and low
-    // parts.  RP = 16: one step, ranks 0 .. 15 of the high part in its first
-    // half and of the low part in its second.
+    // RP = 16: one contraction step, ranks 0 .. 15 of h's high part in its
+    // first half and of the low part in its second.
     constexpr int S = RP == 16 ? 1 : RP / 32;
     constexpr int P = RP == 16 ? 1 : 2;
-    u32x4 hs[2][S][P];
-    int64_t row[2];
-#pragma unroll
-    for (int mb = 0; mb < 2; ++mb) {
-        row[mb] = rows[mb * 16 + col];
-#pragma unroll
-        for (int s = 0; s < S; ++s) {
-            const int j = RP == 16 ? 8 * (g & 1) : 32 * s + 8 * g;
-            float v[8];
-            load_h8(h, parts, part_stride, R, row[mb], j, row[mb] >= 0 && j < R, v);
-            u32x4 part[2];
-            split8<2>(v, part);
-            if constexpr (RP == 16)
-                hs[mb][s][0] = g < 2 ? part[0] : part[1];
-            else {
-                hs[mb][s][0] = part[0];
-                hs[mb][s][P - 1] = part[1];
-            }
-        }
-    }
+    constexpr int OCTS = RP / 8;                               // groups of 8 ranks in a row
+    constexpr int ITEMS = (TILE * OCTS + THREADS - 1) / THREADS;
+    __shared__ u32x4 hs[2][S][P][64];                          // [half][step][part][lane]
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, g = lane >> 4;
+    const int64_t c_lane = (int64_t)blockIdx.x * kAdapterCols + wave * (kAdapterCols / WAVES) + 8 * col;
+    const bool c_ok = c_lane < C;
+    const int64_t c = c_ok ? c_lane : 0;     // lanes past the end compute column 0, unstored
+    const int64_t tile0 = chunk_of_block() * chunk;
+    const int tile1 = (int)min(tile0 + chunk, (int64_t)tiles_max);
+    if (tile0 >= tile1) return;
 
-    const int64_t cw = c0 + wave * (kAdapterCols / WAVES);
-    if constexpr (!TRANS) {
-#pragma unroll 2
-        for (int step = 0; step < 4; ++step) {
-            const int64_t c = cw + 32 * step;
-            if (c >= C) return;
-            f32x4 acc[2][2];
+    // A tile's words of the plan: its adapter, the rows of h that this thread
+    // stages and the rows of the result that this lane holds.
+    int a_next, h_next[ITEMS];
+    int4 rows_next[2];
+    auto load_ids = [&](int64_t tile) {
+        const int32_t *p = plan.tile_row + tile * TILE;
+        a_next = plan.tile_adapter[tile];
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const int64_t n = c + 8 * (col >> 2) + 4 * t + (col & 3);
-                u32x4 ws[S];
+        for (int it = 0; it < ITEMS; ++it)
+            h_next[it] = p[min((tid + it * THREADS) / OCTS, TILE - 1)];
 #pragma unroll
-                for (int s = 0; s < S; ++s) {
-                    const int j = RP == 16 ? 8 * (g & 1) : 32 * s + 8 * g;
-                    ws[s] = u32x4{0u, 0u, 0u, 0u};
-                    if (n < C && j < R) ws[s] = *reinterpret_cast<const u32x4 *>(w + n * R + j);
-                }
+        for (int mb = 0; mb < 2; ++mb)
+            rows_next[mb] = *reinterpret_cast<const int4 *>(p + 16 * mb + 4 * g);
+    };
+    load_ids(tile0);
+    if (!plan.built()) return;
+    const bool in_place = base == out && ldbase == ldo;
+    const DropoutKey key(DROP ? drop.rng : nullptr, DROP);
+
+    u32x4 ws[8][S];
+    int a_held = -1;
+    for (int tile = (int)tile0; tile < tile1; ++tile) {
+        const int a = a_next;
+        if (a == -2) return;
+        int rows[2][4], hr[ITEMS];
 #pragma unroll
-                for (int mb = 0; mb < 2; ++mb) {
-                    acc[mb][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int it = 0; it < ITEMS; ++it) hr[it] = h_next[it];
 #pragma unroll
-                    for (int s = 0; s < S; ++s)
+        for (int mb = 0; mb < 2; ++mb) {
+            rows[mb][0] = rows_next[mb].x, rows[mb][1] = rows_next[mb].y;
+            rows[mb][2] = rows_next[mb].z, rows[mb][3] = rows_next[mb].w;
+        }
+        // h, then the weights, then the base: what is waited for first is
+        // loaded first.
+        float v[ITEMS][8];
 #pragma unroll
-                        for (int p = 0; p < P; ++p)
-                            acc[mb][t] = mfma(ws[s], hs[mb][s][p], acc[mb][t]);
-                }
+        for (int it = 0; it < ITEMS; ++it) {
+            const int item = tid + it * THREADS, j = 8 * (item % OCTS);
+            const bool ok = a >= 0 && item < TILE * OCTS && hr[it] >= 0 && j < R;
+            const float *p = h + (ok ? (int64_t)hr[it] * R + j : 0);
+            const f32x4 lo = *reinterpret_cast<const f32x4 *>(p);
+            const f32x4 hi = *reinterpret_cast<const f32x4 *>(p + 4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[it][i] = ok ? lo[i] : 0.0f;
+                v[it][4 + i] = ok ? hi[i] : 0.0f;
             }
-            const int64_t n = c + 8 * g;
-            if (n < C) {
+            // Few rows: the other parts, three in flight at a time.
+            for (int s0 = 1; s0 < parts; s0 += 3) {
+                f32x4 q[3][2];
 #pragma unroll
-                for (int mb = 0; mb < 2; ++mb) {
-                    if (row[mb] < 0) continue;
-                    float v[8];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        v[i] = acc[mb][0][i];
-                        v[4 + i] = acc[mb][1][i];
-                    }
-                    add_store8<DROP>(v, base ? base + row[mb] * ldbase + n : nullptr,
-                                     out + row[mb] * ldo + n,
-                                     (uint64_t)(row[mb] * (C >> 3) + (n >> 3)), drop);
+                for (int s = 0; s < 3; ++s) {
+                    const float *at = p + min(s0 + s, parts - 1) * part_stride;
+                    q[s][0] = *reinterpret_cast<const f32x4 *>(at);
+                    q[s][1] = *reinterpret_cast<const f32x4 *>(at + 4);
                 }
+#pragma unroll
+                for (int s = 0; s < 3; ++s)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        v[it][i] += ok && s0 + s < parts ? q[s][i >> 2][i & 3] : 0.0f;
+            }
+            if (h_out != nullptr && (a < 0 || parts > 1) && blockIdx.x == 0 &&
+                item < TILE * OCTS && hr[it] >= 0 && j < R) {
+                float *to = h_out + (int64_t)hr[it] * R + j;
+                *reinterpret_cast<f32x4 *>(to) = f32x4{v[it][0], v[it][1], v[it][2], v[it][3]};
+                *reinterpret_cast<f32x4 *>(to + 4) = f32x4{v[it][4], v[it][5], v[it][6], v[it][7]};
             }
         }
-    } else {
-        if (cw >= C) return;
-        f32x4 acc[2][8];
+        if (a >= 0 && a != a_held) {
+            load_expand_weights<RP, TRANS, S>(weights + (int64_t)a * R * C, C, R, c, g, ws);
+            a_held = a;
+        }
+        u32x4 bases[2][4];
+        const bool read_base = base != nullptr && !(in_place && a < 0);
 #pragma unroll
         for (int mb = 0; mb < 2; ++mb)
 #pragma unroll
-            for (int t = 0; t < 8; ++t) acc[mb][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-        const int64_t k = cw + 32 * (col & 3) + 8 * (col >> 2);
-#pragma unroll
-        for (int s = 0; s < S; ++s) {
-            const int j = RP == 16 ? 8 * (g & 1) : 32 * s + 8 * g;
-            u32x4 in[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                in[i] = u32x4{0u, 0u, 0u, 0u};
-                if (k < C && j < R)
-                    in[i] = *reinterpret_cast<const u32x4 *>(w + (int64_t)(j + i) * C + k);
+            for (int i = 0; i < 4; ++i) {
+                bases[mb][i] = u32x4{0u, 0u, 0u, 0u};
+                if (read_base)
+                    bases[mb][i] = *reinterpret_cast<const u32x4 *>(
+                        base + (int64_t)max(rows[mb][i], 0) * ldbase + c);
             }
-#pragma unroll
-            for (int t = 0; t < 8; ++t) {
-                u32x4 ws;
-#pragma unroll
-                for (int d = 0; d < 4; ++d)
-                    ws[d] = (t & 1) ? high_halves(in[2 * d][t >> 1], in[2 * d + 1][t >> 1])
-                                    : low_halves(in[2 * d][t >> 1], in[2 * d + 1][t >> 1]);
+        if (tile + 1 < tile1) load_ids(tile + 1);
+        if (a < 0) {
+            // Rows without an adapter: out = base.
+            if (!in_place && c_ok) {
 #pragma unroll
                 for (int mb = 0; mb < 2; ++mb)
 #pragma unroll
-                    for (int p = 0; p < P; ++p) acc[mb][t] = mfma(ws, hs[mb][s][p], acc[mb][t]);
+                    for (int i = 0; i < 4; ++i)
+                        if (rows[mb][i] >= 0)
+                            *reinterpret_cast<u32x4 *>(out + (int64_t)rows[mb][i] * ldo + c) =
+                                bases[mb][i];
+            }
+            continue;
+        }
+        if (tile > tile0) __syncthreads();   // the tile before has been read
+#pragma unroll
+        for (int it = 0; it < ITEMS; ++it) {
+            const int item = tid + it * THREADS, p = item / OCTS, o = item % OCTS;
+            u32x4 part[2];
+            split8<2>(v[it], part);
+            if (item < TILE * OCTS) {
+                if constexpr (RP == 16) {
+                    hs[p >> 4][0][0][16 * o + (p & 15)] = part[0];
+                    hs[p >> 4][0][0][32 + 16 * o + (p & 15)] = part[1];
+                } else {
+                    hs[p >> 4][o >> 2][0][16 * (o & 3) + (p & 15)] = part[0];
+                    hs[p >> 4][o >> 2][P - 1][16 * (o & 3) + (p & 15)] = part[1];
+                }
             }
         }
+        __syncthreads();
 #pragma unroll
         for (int mb = 0; mb < 2; ++mb) {
-            if (row[mb] < 0) continue;
+            f32x4 acc[8];
+#pragma unroll
+            for (int t = 0; t < 8; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int s = 0; s < S; ++s)
+#pragma unroll
+                for (int p = 0; p < P; ++p) {
+                    const u32x4 operand = hs[mb][s][p][lane];
+#pragma unroll
+                    for (int t = 0; t < 8; ++t) acc[t] = mfma(operand, ws[t][s], acc[t]);
+                }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int64_t n = cw + 32 * i + 8 * g;
-                if (n >= C) continue;
-                float v[8];
+                const int row = rows[mb][i];
+                if (row < 0 || !c_ok) continue;
+                uint32_t n[4];
+                if constexpr (DROP)
+                    dropout_words(key, (uint64_t)((int64_t)row * (C >> 3) + (c >> 3)), n);
+                u32x4 o;
 #pragma unroll
-                for (int t = 0; t < 8; ++t) v[t] = acc[mb][t][i];
-                add_store8<DROP>(v, base ? base + row[mb] * ldbase + n : nullptr,
-                                 out + row[mb] * ldo + n,
-                                 (uint64_t)(row[mb] * (C >> 3) + (n >> 3)), drop);
+                for (int d = 0; d < 4; ++d) {
+                    float lo = acc[2 * d][i], hi = acc[2 * d + 1][i];
+                    if constexpr (DROP) {
+                        lo = (n[d] & 0xFFFFu) >= drop.threshold ? lo * drop.factor : 0.0f;
+                        hi = (n[d] >> 16) >= drop.threshold ? hi * drop.factor : 0.0f;
+                    }
+                    lo += __uint_as_float(bases[mb][i][d] << 16);
+                    hi += __uint_as_float(bases[mb][i][d] & 0xFFFF0000u);
+                    o[d] = pack_bf16(lo, hi);
+                }
+                *reinterpret_cast<u32x4 *>(out + (int64_t)row * ldo + c) = o;
             }
         }
     }
@@ -574,99 +640,163 @@ struct WgradSide {
     int drop;                   // src takes the dropout's mask
 };
 
-// Grid: (chunks, column blocks of both sides).  A wave owns 128 columns: a
-// lane reads 8 columns of its 8 rows and turns them in registers into the
-// operands of eight MFMA row blocks (row q of block t is column 8 q + t).
+// Columns of a lane (its loads' width) and of a workgroup.  Rank 128 takes
+// half as many, so that its sums fit two waves' registers on a SIMD.
+constexpr int wgrad_lane_cols(int rp) { return rp >= 128 ? 4 : 8; }
+constexpr int wgrad_cols(int rp) { return WAVES * 16 * wgrad_lane_cols(rp); }
+
+// Grid: (column blocks of both sides, chunks of tiles).  Per tile of 32 rows a
+// lane reads L columns of its 8 rows and turns them in registers into the
+// operands of L MFMA row blocks (row q of block t is column L q + t of the
+// wave's 16 L); the short operand is split into bf16 parts once per workgroup
+// and held in LDS in operand order.  The next tile's loads of both are in
+// flight while the current one is multiplied.
 template <int RP, int PARTS, bool DROP>
-__global__ __launch_bounds__(THREADS) void adapter_wgrad_kernel(PlanView plan, WgradSide left,
-                                                               WgradSide right, int left_blocks,
-                                                               int R, int chunk,
-                                                               DropoutArgs drop) {
+__global__ __launch_bounds__(THREADS, 2) void adapter_wgrad_kernel(PlanView plan, WgradSide left,
+                                                                  WgradSide right, int left_blocks,
+                                                                  int R, int chunk,
+                                                                  DropoutArgs drop) {
+    constexpr int L = wgrad_lane_cols(RP);
+    constexpr int J = RP / 16;
+    constexpr int ITEMS = (RP * 4 + THREADS - 1) / THREADS;   // (rank, 8 rows) per thread
+    __shared__ u32x4 hs[2][PARTS][J][64];
     if (!plan.built()) return;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, g = lane >> 4;
-    const bool first = (int)blockIdx.y < left_blocks;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, g = lane >> 4;
+    const bool first = (int)blockIdx.x < left_blocks;
     const WgradSide side = first ? left : right;
-    const int block = first ? blockIdx.y : blockIdx.y - left_blocks;
-    const int64_t cw = (int64_t)block * kAdapterCols + wave * (kAdapterCols / WAVES);
+    const int block = first ? blockIdx.x : blockIdx.x - left_blocks;
+    const int64_t cw = (int64_t)block * wgrad_cols(RP) + wave * (16 * L);
     const int64_t C = side.C;
-    if (cw >= C) return;
     const int live = plan.header[4];
-    int tile = blockIdx.x * chunk;
+    const int64_t slot = chunk_of_block();
+    int tile = (int)min(slot * chunk, (int64_t)live);
     const int tile_end = min(tile + chunk, live);
-    const int64_t c = cw + 8 * col;
+    const int64_t c = cw + L * col;
     const bool c_ok = c < C;
+    const DropoutKey key(DROP ? drop.rng : nullptr, DROP);
+
+    int rows[8];
+    Cols<L> in[8], in_next[8];
+    float h_next[ITEMS][8];
+    auto load_rows = [&](int t) {
+        const int4 *p = reinterpret_cast<const int4 *>(plan.tile_row + (int64_t)t * TILE + 8 * g);
+        const int4 lo = p[0], hi = p[1];
+        rows[0] = lo.x, rows[1] = lo.y, rows[2] = lo.z, rows[3] = lo.w;
+        rows[4] = hi.x, rows[5] = hi.y, rows[6] = hi.z, rows[7] = hi.w;
+    };
+    auto load_src = [&]() {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            in_next[i].load(side.src + (int64_t)max(rows[i], 0) * side.ld + (c_ok ? c : 0));
+    };
+    auto load_short = [&](int t) {
+#pragma unroll
+        for (int it = 0; it < ITEMS; ++it) {
+            const int item = tid + it * THREADS, j = item % RP, oct = item / RP;
+            if (ITEMS == 1 && RP * 4 < THREADS && oct >= 4) break;
+            const int4 *q = reinterpret_cast<const int4 *>(plan.tile_row + (int64_t)t * TILE + 8 * oct);
+            const int4 lo = q[0], hi = q[1];
+            const int r[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+            const float *p = side.h + (j < R ? j : 0);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) h_next[it][i] = p[(int64_t)max(r[i], 0) * R];
+            for (int s = 1; s < side.parts; ++s) {
+                p += side.part_stride;
+                float more[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) more[i] = p[(int64_t)max(r[i], 0) * R];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) h_next[it][i] += more[i];
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) h_next[it][i] = r[i] >= 0 && j < R ? h_next[it][i] : 0.0f;
+        }
+    };
+    auto stage_short = [&](int buf) {
+#pragma unroll
+        for (int it = 0; it < ITEMS; ++it) {
+            const int item = tid + it * THREADS, j = item % RP, oct = item / RP;
+            if (oct < 4) {
+                u32x4 part[PARTS];
+                split8<PARTS>(h_next[it], part);
+#pragma unroll
+                for (int p = 0; p < PARTS; ++p) hs[buf][p][j >> 4][16 * oct + (j & 15)] = part[p];
+            }
+        }
+    };
 
     while (tile < tile_end) {
         const int a = plan.tile_adapter[tile];
         const int stop = min(tile_end, plan.group_tile0[a + 1]);
-        f32x4 acc[8][RP / 16];
+        f32x4 acc[L][J];
 #pragma unroll
-        for (int t = 0; t < 8; ++t)
+        for (int t = 0; t < L; ++t)
 #pragma unroll
-            for (int jb = 0; jb < RP / 16; ++jb) acc[t][jb] = f32x4{0.f, 0.f, 0.f, 0.f};
-        for (; tile < stop; ++tile) {
-            int rows[8];
-            u32x4 in[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) rows[i] = plan.tile_row[tile * TILE + 8 * g + i];
+            for (int jb = 0; jb < J; ++jb) acc[t][jb] = f32x4{0.f, 0.f, 0.f, 0.f};
+        load_rows(tile);
+        load_src();
+        load_short(tile);
+        int buf = 0;
+        __syncthreads();                     // the run before has read both buffers
+        stage_short(0);
+        __syncthreads();
+        for (; tile < stop; ++tile, buf ^= 1) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                in[i] = u32x4{0u, 0u, 0u, 0u};
-                if (c_ok && rows[i] >= 0)
-                    in[i] = *reinterpret_cast<const u32x4 *>(side.src + rows[i] * side.ld + c);
+                in[i] = in_next[i];
+                in[i].clear_unless(c_ok && rows[i] >= 0);
             }
             if constexpr (DROP) {
                 if (side.drop) {
-                    const DropoutKey key(drop.rng);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        in[i] = keep_chunk(in[i], key,
-                                           (uint64_t)((int64_t)rows[i] * (C >> 3) + (c >> 3)),
-                                           drop.threshold);
-                }
-            }
-            u32x4 hs[RP / 16][PARTS];
+                    for (int i = 0; i < 8; ++i) {
+                        uint32_t n[L / 2];
+                        numbers_of<L>(key, rows[i], c, C, n);
 #pragma unroll
-            for (int jb = 0; jb < RP / 16; ++jb) {
-                const int j = jb * 16 + col;
-                float v[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    v[i] = 0.0f;
-                    if (rows[i] >= 0 && j < R) {
-                        const float *p = side.h + (int64_t)rows[i] * R + j;
-                        for (int s = 0; s < side.parts; ++s) v[i] += p[s * side.part_stride];
+                        for (int d = 0; d < L / 2; ++d)
+                            in[i].d[d] &= dropout_keep2(n[d], drop.threshold);
                     }
                 }
-                split8<PARTS>(v, hs[jb]);
             }
+            const bool more = tile + 1 < stop;
+            if (more) {
+                load_rows(tile + 1);
+                load_src();
+                load_short(tile + 1);
+            }
+            u32x4 xs[L];
 #pragma unroll
-            for (int t = 0; t < 8; ++t) {
-                u32x4 xs;
+            for (int t = 0; t < L; ++t)
 #pragma unroll
                 for (int d = 0; d < 4; ++d)
-                    xs[d] = (t & 1) ? high_halves(in[2 * d][t >> 1], in[2 * d + 1][t >> 1])
-                                    : low_halves(in[2 * d][t >> 1], in[2 * d + 1][t >> 1]);
+                    xs[t][d] = (t & 1)
+                                   ? high_halves(in[2 * d].d[t >> 1], in[2 * d + 1].d[t >> 1])
+                                   : low_halves(in[2 * d].d[t >> 1], in[2 * d + 1].d[t >> 1]);
 #pragma unroll
-                for (int jb = 0; jb < RP / 16; ++jb)
+            for (int jb = 0; jb < J; ++jb)
 #pragma unroll
-                    for (int p = 0; p < PARTS; ++p) acc[t][jb] = mfma(xs, hs[jb][p], acc[t][jb]);
-            }
+                for (int p = 0; p < PARTS; ++p) {
+                    const u32x4 b = hs[buf][p][jb][lane];
+#pragma unroll
+                    for (int t = 0; t < L; ++t) acc[t][jb] = mfma(xs[t], b, acc[t][jb]);
+                }
+            if (more) stage_short(buf ^ 1);
+            __syncthreads();
         }
-        float *out = side.partial + (int64_t)(blockIdx.x + plan.group_rank[a]) * R * C;
+        float *out = side.partial + (slot + plan.group_rank[a]) * R * C;
 #pragma unroll
-        for (int jb = 0; jb < RP / 16; ++jb) {
+        for (int jb = 0; jb < J; ++jb) {
             const int j = jb * 16 + col;
             if (j >= R) continue;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int64_t n = cw + 8 * (4 * g + i);
+                const int64_t n = cw + L * (4 * g + i);
                 if (n >= C) continue;
                 float *p = out + (int64_t)j * C + n;
-                *reinterpret_cast<f32x4 *>(p) =
-                    f32x4{acc[0][jb][i], acc[1][jb][i], acc[2][jb][i], acc[3][jb][i]};
-                *reinterpret_cast<f32x4 *>(p + 4) =
-                    f32x4{acc[4][jb][i], acc[5][jb][i], acc[6][jb][i], acc[7][jb][i]};
+#pragma unroll
+                for (int t = 0; t < L; t += 4)
+                    *reinterpret_cast<f32x4 *>(p + t) = f32x4{acc[t][jb][i], acc[t + 1][jb][i],
+                                                              acc[t + 2][jb][i], acc[t + 3][jb][i]};
             }
         }
     }
@@ -740,6 +870,13 @@ hipError_t by_rank(int rank, F f) {
     return hipGetLastError();
 }
 
+// Tiles of one expand workgroup: more where its weights (rank x 2 bytes a
+// column) weigh more against a tile's base and output (128 bytes a column),
+// while enough workgroups are left.
+int64_t expand_chunk(int64_t tiles, int64_t blocks, int64_t rank) {
+    return std::max<int64_t>(1, std::min<int64_t>(rank / 16, tiles * blocks / 1024));
+}
+
 int64_t part_columns(int64_t C, int parts) { return ((C + parts - 1) / parts + 31) / 32 * 32; }
 
 template <bool TRANS>
@@ -769,13 +906,16 @@ hipError_t launch_expand(const AdapterArgs &w, const AdapterPlanShape &shape, co
                          const uint16_t *base, int64_t ldbase, uint16_t *out, int64_t ldo,
                          float *h_out, hipStream_t stream) {
     const PlanView v = view_of(shape, plan);
-    const dim3 grid((unsigned)shape.tiles_max, (unsigned)((C + kAdapterCols - 1) / kAdapterCols));
     return by_rank(w.rank, [&](auto rp) {
+        const int64_t blocks = (C + kAdapterCols - 1) / kAdapterCols;
+        const int64_t chunk = expand_chunk(shape.tiles_max, blocks, w.rank);
+        const dim3 grid = grid_of(blocks, (shape.tiles_max + chunk - 1) / chunk);
         auto go = [&](auto dropped) {
             hipLaunchKernelGGL((adapter_expand_kernel<decltype(rp)::value, TRANS,
                                                       decltype(dropped)::value>),
-                               grid, dim3(THREADS), 0, stream, v, h, parts, shape.rows * w.rank,
-                               TRANS ? w.a : w.b, w.rank, C, base, ldbase, out, ldo, h_out, drop);
+                               grid, dim3(THREADS), 0, stream, v, (int)shape.tiles_max, (int)chunk,
+                               h, parts, shape.rows * w.rank, TRANS ? w.a : w.b, w.rank, C, base, ldbase,
+                               out, ldo, h_out, drop);
         };
         if constexpr (TRANS) {
             if (drop.rng) return go(std::true_type{});
@@ -854,10 +994,11 @@ hipError_t launch_adapter_backward(const AdapterArgs &w, const AdapterPlanShape 
     float *part_b = part_a + slots * w.rank * w.in;
     const WgradSide left = {x, ldx, w.in, g, parts, shape.rows * w.rank, part_a, 1};
     const WgradSide right = {dy, lddy, w.out, h, 1, 0, part_b, 0};
-    const int left_blocks = (int)((w.in + kAdapterCols - 1) / kAdapterCols);
-    const int right_blocks = (int)((w.out + kAdapterCols - 1) / kAdapterCols);
-    const dim3 grid((unsigned)chunks, (unsigned)(left_blocks + right_blocks));
     hipError_t e = by_rank(w.rank, [&](auto rp) {
+        constexpr int cols = wgrad_cols(decltype(rp)::value);
+        const int left_blocks = (int)((w.in + cols - 1) / cols);
+        const int right_blocks = (int)((w.out + cols - 1) / cols);
+        const dim3 grid = grid_of(left_blocks + right_blocks, chunks);
         auto go = [&](auto split, auto dropped) {
             hipLaunchKernelGGL((adapter_wgrad_kernel<decltype(rp)::value, decltype(split)::value,
                                                      decltype(dropped)::value>),

@@ -31,8 +31,9 @@ struct DropoutArgs {
 // The generator's key and stream, read once per kernel (wave-uniform).
 struct DropoutKey {
     uint32_t seed_lo, seed_hi, off_lo, off_hi;
-    __device__ __forceinline__ explicit DropoutKey(const int64_t *rng) {
-        const uint64_t s = (uint64_t)rng[0], o = (uint64_t)rng[1];
+    // used false: no dropout, rng is not read.
+    __device__ __forceinline__ explicit DropoutKey(const int64_t *rng, bool used = true) {
+        const uint64_t s = used ? (uint64_t)rng[0] : 0, o = used ? (uint64_t)rng[1] : 0;
         seed_lo = (uint32_t)s;
         seed_hi = (uint32_t)(s >> 32);
         off_lo = (uint32_t)o;
