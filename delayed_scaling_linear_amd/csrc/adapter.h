@@ -51,12 +51,19 @@ inline int adapter_parts(int64_t tiles, int64_t C) {
     return (int)std::max<int64_t>(1, std::min<int64_t>({want, C / 256, 16}));
 }
 
+// Ranks as the kernels see them: the next of 16, 32, 64, 128.
+inline int64_t adapter_padded_rank(int64_t rank) {
+    return rank <= 16 ? 16 : rank <= 32 ? 32 : rank <= 64 ? 64 : 128;
+}
+
 // Tiles of one weight-gradient workgroup: a partial sum of R fp32 per column
-// is written and read per workgroup, against 32 rows of bf16 per tile.
+// is written and read per workgroup, so as few of them as fill the chip (two
+// workgroups per CU; one of rank 128, which has twice the threads).
 inline int64_t adapter_chunk(int64_t tiles, int64_t rank, int64_t in, int64_t out) {
     const int64_t blocks = (in + kAdapterCols - 1) / kAdapterCols +
                            (out + kAdapterCols - 1) / kAdapterCols;
-    return std::max<int64_t>(1, std::min<int64_t>(rank / 4, tiles * blocks / 512));
+    const int64_t chunks = std::max<int64_t>(1, (rank > 64 ? 256 : 512) / blocks);
+    return std::max<int64_t>(1, (tiles + chunks - 1) / chunks);
 }
 
 // Partial sums of the weight gradients: one per (chunk of tiles, adapter
@@ -65,15 +72,17 @@ inline int64_t adapter_slots(const AdapterPlanShape &p, int64_t chunk) {
     return (p.tiles_max + chunk - 1) / chunk + std::min(p.adapters, p.rows);
 }
 
-// Workspace: K-part sums of h or g, then the weight gradients' partial sums.
+// Workspace: K-part sums of h or g, both short operands of the weight
+// gradients as up to three bf16 parts, and the gradients' partial sums.
 struct AdapterWorkspace {
-    int64_t sums, grads, bytes;
+    int64_t sums, packed, grads, bytes;
     AdapterWorkspace(const AdapterPlanShape &p, int64_t rank, int64_t in, int64_t out) {
         const int64_t parts = std::max(adapter_parts(p.tiles_max, in),
                                        adapter_parts(p.tiles_max, out));
         sums = (parts * p.rows * rank * 4 + 255) / 256 * 256;
+        packed = 2 * p.tiles_max * kAdapterTile * adapter_padded_rank(rank) * 3 * 2;
         grads = adapter_slots(p, adapter_chunk(p.tiles_max, rank, in, out)) * rank * (in + out) * 4;
-        bytes = sums + grads;
+        bytes = sums + packed + grads;
     }
 };
 

@@ -67,9 +67,10 @@ __device__ __forceinline__ uint32_t bf16_rne(float f) {
 }
 
 // v as a sum of PARTS bf16 values per element: truncations, the last one
-// rounded.  An infinity or NaN goes to the first part alone.
-template <int PARTS>
-__device__ __forceinline__ void split8(const float v[8], u32x4 (&out)[PARTS]) {
+// rounded.  An infinity or NaN goes to the first part alone (rare: a wave that
+// sees none skips those steps).
+template <int PARTS, bool SPECIAL>
+__device__ __forceinline__ void split8_steps(const float v[8], u32x4 (&out)[PARTS]) {
     float rest[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) rest[i] = v[i];
@@ -87,13 +88,28 @@ __device__ __forceinline__ void split8(const float v[8], u32x4 (&out)[PARTS]) {
                 float &r = rest[2 * d + k];
                 const uint32_t u = __float_as_uint(r);
                 bits[k] = u & 0xFFFF0000u;
-                const bool special = (u & 0x7F800000u) == 0x7F800000u;
-                if (special && r != r) bits[k] |= 0x00400000u;
-                r = special ? 0.0f : r - __uint_as_float(bits[k]);
+                if constexpr (SPECIAL) {
+                    const bool special = (u & 0x7F800000u) == 0x7F800000u;
+                    if (special && r != r) bits[k] |= 0x00400000u;
+                    r = special ? 0.0f : r - __uint_as_float(bits[k]);
+                } else {
+                    r -= __uint_as_float(bits[k]);
+                }
             }
             out[p][d] = high_halves(bits[0], bits[1]);
         }
     }
+}
+
+template <int PARTS>
+__device__ __forceinline__ void split8(const float v[8], u32x4 (&out)[PARTS]) {
+    uint32_t most = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) most = max(most, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+    if (__any(most >= 0x7F800000u))
+        split8_steps<PARTS, true>(v, out);
+    else
+        split8_steps<PARTS, false>(v, out);
 }
 
 // ---- the plan ---------------------------------------------------------------
@@ -395,14 +411,20 @@ __device__ __forceinline__ void numbers_of(const DropoutKey &key, int64_t row, i
     for (int d = 0; d < L / 2; ++d) n[d] = L == 8 ? w[d] : (c & 4) ? w[2 + d] : w[d];
 }
 
-// The weights of a lane's 8 columns c .. as MFMA columns of 8 blocks (block t:
+// Columns of an expand lane and threads of a workgroup of 512 columns.  Rank 128
+// takes half the columns a lane, so that its weights leave registers for three
+// waves on a SIMD.
+constexpr int expand_lane_cols(int rp) { return rp >= 128 ? 4 : 8; }
+constexpr int expand_threads(int rp) { return kAdapterCols / expand_lane_cols(rp) * 4; }
+
+// The weights of a lane's L columns c .. as MFMA columns of L blocks (block t:
 // column c + t), S contraction steps of 32 ranks each.
 //   TRANS false, W [C, R] (B in the forward): 8 ranks of a column are 16 bytes.
-//   TRANS true, W [R, C] (A in the backward): a lane reads its 8 columns of its
+//   TRANS true, W [R, C] (A in the backward): a lane reads its L columns of its
 //   8 ranks and turns them in registers.
-template <int RP, bool TRANS, int S>
+template <int RP, bool TRANS, int S, int L>
 __device__ __forceinline__ void load_expand_weights(const uint16_t *w, int64_t C, int R, int64_t c,
-                                                    int g, u32x4 (&ws)[8][S]) {
+                                                    int g, u32x4 (&ws)[L][S]) {
 #pragma unroll
     for (int s = 0; s < S; ++s) {
         const int j = RP == 16 ? 8 * (g & 1) : 32 * s + 8 * g;
@@ -410,23 +432,23 @@ __device__ __forceinline__ void load_expand_weights(const uint16_t *w, int64_t C
         const int js = ok ? j : 0;
         if constexpr (!TRANS) {
 #pragma unroll
-            for (int t = 0; t < 8; ++t)
+            for (int t = 0; t < L; ++t)
                 ws[t][s] = *reinterpret_cast<const u32x4 *>(w + (c + t) * R + js);
         } else {
-            u32x4 in[8];
+            Cols<L> in[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                in[i] = *reinterpret_cast<const u32x4 *>(w + (int64_t)(js + i) * C + c);
+            for (int i = 0; i < 8; ++i) in[i].load(w + (int64_t)(js + i) * C + c);
 #pragma unroll
-            for (int t = 0; t < 8; ++t)
+            for (int t = 0; t < L; ++t)
 #pragma unroll
                 for (int d = 0; d < 4; ++d)
-                    ws[t][s][d] = (t & 1) ? high_halves(in[2 * d][t >> 1], in[2 * d + 1][t >> 1])
-                                          : low_halves(in[2 * d][t >> 1], in[2 * d + 1][t >> 1]);
+                    ws[t][s][d] = (t & 1)
+                                      ? high_halves(in[2 * d].d[t >> 1], in[2 * d + 1].d[t >> 1])
+                                      : low_halves(in[2 * d].d[t >> 1], in[2 * d + 1].d[t >> 1]);
         }
         if (RP > 16 || R < 16) {
 #pragma unroll
-            for (int t = 0; t < 8; ++t)
+            for (int t = 0; t < L; ++t)
 #pragma unroll
                 for (int d = 0; d < 4; ++d) ws[t][s][d] = ok ? ws[t][s][d] : 0u;
         }
@@ -445,7 +467,49 @@ dim3 grid_of(int64_t blocks, int64_t chunks) {
                 (unsigned)((chunks + GRID_Y - 1) / GRID_Y));
 }
 
-// Grid: (blocks of 512 columns, chunks of tiles).  h is the MFMA's row operand
+// The short operands of the weight gradients, split into bf16 parts and laid
+// out as MFMA operands once for all column blocks that read them:
+// packed [tile][part][16 ranks][lane], lane l of a tile holding rank l % 16 of
+// rows 8 (l / 16) ...
+struct PackSide {
+    const float *h;             // [parts][rows][R]
+    int parts;
+    u32x4 *packed;
+};
+
+template <int PARTS>
+__device__ __forceinline__ void pack_tile(const PackSide &side, const int32_t *tile_row, int64_t tile,
+                                          int R, int64_t part_stride, int blocks) {
+    for (int item = threadIdx.x; item < blocks * 64; item += blockDim.x) {
+        const int jb = item >> 6, l = item & 63, j = 16 * jb + (l & 15);
+        const int4 *q = reinterpret_cast<const int4 *>(tile_row + tile * TILE + 8 * (l >> 4));
+        const int4 lo = q[0], hi = q[1];
+        const int r[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+        const float *p = side.h + (j < R ? j : 0);
+        for (int s = 0; s < side.parts; ++s, p += part_stride)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] += p[(int64_t)max(r[i], 0) * R];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = r[i] >= 0 && j < R ? v[i] : 0.0f;
+        u32x4 part[PARTS];
+        split8<PARTS>(v, part);
+#pragma unroll
+        for (int n = 0; n < PARTS; ++n)
+            side.packed[((tile * PARTS + n) * blocks + jb) * 64 + l] = part[n];
+    }
+}
+
+struct PackArgs {
+    PackSide g, h;
+    int split;                  // bf16 parts: 2 or 3
+    int64_t rows;               // rows of the expand's grid that pack; 0: nothing to pack
+};
+
+// Grid: (blocks of 512 columns, chunks of tiles); in the backward rows of
+// workgroups before them pack both short operands of the weight gradients.  h is the MFMA's row operand
 // and a lane's 8 adjacent columns are 8 column blocks, so a lane holds 8
 // adjacent columns of rows 4 g .. 4 g + 3 of the result and the sixteen lanes of
 // a row load the base and store the output in one run of 256 bytes.  The
@@ -454,65 +518,78 @@ dim3 grid_of(int64_t blocks, int64_t chunks) {
 // L1 the bound: 2.3 GB through it for 200 MB of base and output).  A wave keeps
 // the weights of its columns while its tiles' adapter stays the same.
 template <int RP, bool TRANS, bool DROP>
-__global__ __launch_bounds__(THREADS, 2) void adapter_expand_kernel(
+__global__ __launch_bounds__(expand_threads(RP), 2) void adapter_expand_kernel(
     PlanView plan, int tiles_max, int chunk, const float *h, int parts, int64_t part_stride,
-    const uint16_t *__restrict__ weights, int R, int64_t C, const uint16_t *base, int64_t ldbase,
-    uint16_t *out, int64_t ldo, float *h_out, DropoutArgs drop) {
+    const uint16_t *__restrict__ weights, int R, int64_t C, const uint16_t *base, int32_t ldbase,
+    uint16_t *out, int32_t ldo, float *h_out, PackArgs pack, DropoutArgs drop) {
     // RP = 16: one contraction step, ranks 0 .. 15 of h's high part in its
     // first half and of the low part in its second.
     constexpr int S = RP == 16 ? 1 : RP / 32;
     constexpr int P = RP == 16 ? 1 : 2;
     constexpr int OCTS = RP / 8;                               // groups of 8 ranks in a row
-    constexpr int ITEMS = (TILE * OCTS + THREADS - 1) / THREADS;
-    __shared__ u32x4 hs[2][S][P][64];                          // [half][step][part][lane]
+    constexpr int L = expand_lane_cols(RP), NT = expand_threads(RP);
+    constexpr int ITEMS = (TILE * OCTS + NT - 1) / NT;
+    // Ranks up to 32: one tile a workgroup and more of those on a CU instead.
+    constexpr bool AHEAD = RP >= 64;
+    __shared__ u32x4 hs[AHEAD ? 2 : 1][2][S][P][64];     // [buffer][half][step][part][lane]
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, g = lane >> 4;
-    const int64_t c_lane = (int64_t)blockIdx.x * kAdapterCols + wave * (kAdapterCols / WAVES) + 8 * col;
+    const int64_t c_lane = (int64_t)blockIdx.x * kAdapterCols + wave * (16 * L) + L * col;
     const bool c_ok = c_lane < C;
     const int64_t c = c_ok ? c_lane : 0;     // lanes past the end compute column 0, unstored
-    const int64_t tile0 = chunk_of_block() * chunk;
+    int64_t part = chunk_of_block();
+    if constexpr (TRANS) {
+        // The first pack_rows rows of the grid pack a tile each (they start
+        // first: a late one would be the kernel's tail).
+        if (part < pack.rows) {
+            const int64_t tile = part * gridDim.x + blockIdx.x;
+            if (tile >= tiles_max || !plan.built() || plan.tile_adapter[tile] < 0) return;
+            if (pack.split == 3) {
+                pack_tile<3>(pack.g, plan.tile_row, tile, R, part_stride, RP / 16);
+                pack_tile<3>(pack.h, plan.tile_row, tile, R, 0, RP / 16);
+            } else {
+                pack_tile<2>(pack.g, plan.tile_row, tile, R, part_stride, RP / 16);
+                pack_tile<2>(pack.h, plan.tile_row, tile, R, 0, RP / 16);
+            }
+            return;
+        }
+        part -= pack.rows;
+    }
+    const int64_t tile0 = part * chunk;
     const int tile1 = (int)min(tile0 + chunk, (int64_t)tiles_max);
-    if (tile0 >= tile1) return;
+    if (tile0 >= tile1 || out == nullptr) return;
 
     // A tile's words of the plan: its adapter, the rows of h that this thread
     // stages and the rows of the result that this lane holds.
-    int a_next, h_next[ITEMS];
-    int4 rows_next[2];
+    struct Ids {
+        int a, h[ITEMS];
+        int4 rows[2];
+    };
     auto load_ids = [&](int64_t tile) {
+        Ids d;
         const int32_t *p = plan.tile_row + tile * TILE;
-        a_next = plan.tile_adapter[tile];
+        d.a = plan.tile_adapter[tile];
 #pragma unroll
-        for (int it = 0; it < ITEMS; ++it)
-            h_next[it] = p[min((tid + it * THREADS) / OCTS, TILE - 1)];
+        for (int it = 0; it < ITEMS; ++it) d.h[it] = p[min((tid + it * NT) / OCTS, TILE - 1)];
 #pragma unroll
         for (int mb = 0; mb < 2; ++mb)
-            rows_next[mb] = *reinterpret_cast<const int4 *>(p + 16 * mb + 4 * g);
+            d.rows[mb] = *reinterpret_cast<const int4 *>(p + 16 * mb + 4 * g);
+        return d;
     };
-    load_ids(tile0);
+    Ids next = load_ids(tile0);
     if (!plan.built()) return;
     const bool in_place = base == out && ldbase == ldo;
     const DropoutKey key(DROP ? drop.rng : nullptr, DROP);
 
-    u32x4 ws[8][S];
-    int a_held = -1;
-    for (int tile = (int)tile0; tile < tile1; ++tile) {
-        const int a = a_next;
-        if (a == -2) return;
-        int rows[2][4], hr[ITEMS];
-#pragma unroll
-        for (int it = 0; it < ITEMS; ++it) hr[it] = h_next[it];
-#pragma unroll
-        for (int mb = 0; mb < 2; ++mb) {
-            rows[mb][0] = rows_next[mb].x, rows[mb][1] = rows_next[mb].y;
-            rows[mb][2] = rows_next[mb].z, rows[mb][3] = rows_next[mb].w;
-        }
-        // h, then the weights, then the base: what is waited for first is
-        // loaded first.
-        float v[ITEMS][8];
+    // The tile ahead: its values of h (K parts still apart are added here) and
+    // its base.
+    float v[ITEMS][8];
+    Cols<L> ahead[2][4];
+    auto load_data = [&](const Ids &d) {
 #pragma unroll
         for (int it = 0; it < ITEMS; ++it) {
-            const int item = tid + it * THREADS, j = 8 * (item % OCTS);
-            const bool ok = a >= 0 && item < TILE * OCTS && hr[it] >= 0 && j < R;
-            const float *p = h + (ok ? (int64_t)hr[it] * R + j : 0);
+            const int item = tid + it * NT, j = 8 * (item % OCTS);
+            const bool ok = d.a >= 0 && item < TILE * OCTS && d.h[it] >= 0 && j < R;
+            const float *p = h + (ok ? (int64_t)d.h[it] * R + j : 0);
             const f32x4 lo = *reinterpret_cast<const f32x4 *>(p);
             const f32x4 hi = *reinterpret_cast<const f32x4 *>(p + 4);
 #pragma unroll
@@ -535,29 +612,67 @@ __global__ __launch_bounds__(THREADS, 2) void adapter_expand_kernel(
                     for (int i = 0; i < 8; ++i)
                         v[it][i] += ok && s0 + s < parts ? q[s][i >> 2][i & 3] : 0.0f;
             }
+        }
+        const bool read_base = base != nullptr && !(in_place && d.a < 0);
+#pragma unroll
+        for (int mb = 0; mb < 2; ++mb) {
+            const int rows[4] = {d.rows[mb].x, d.rows[mb].y, d.rows[mb].z, d.rows[mb].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (read_base)
+                    ahead[mb][i].load(base + (int64_t)max(rows[i], 0) * ldbase + c);
+                else
+                    ahead[mb][i].clear_unless(false);
+            }
+        }
+    };
+
+    if (next.a != -2) load_data(next);
+    u32x4 ws[L][S];
+    int a_held = -1, buf = 0;
+    for (int tile = (int)tile0; tile < tile1; ++tile) {
+        const Ids now = next;
+        const int a = now.a;
+        if (a == -2) return;
+        if (AHEAD && tile + 1 < tile1) next = load_ids(tile + 1);
+        if (a >= 0 && a != a_held) {
+            load_expand_weights<RP, TRANS, S, L>(weights + (int64_t)a * R * C, C, R, c, g, ws);
+            a_held = a;
+        }
+#pragma unroll
+        for (int it = 0; it < ITEMS; ++it) {
+            const int item = tid + it * NT, p = item / OCTS, o = item % OCTS;
             if (h_out != nullptr && (a < 0 || parts > 1) && blockIdx.x == 0 &&
-                item < TILE * OCTS && hr[it] >= 0 && j < R) {
-                float *to = h_out + (int64_t)hr[it] * R + j;
+                item < TILE * OCTS && now.h[it] >= 0 && 8 * o < R) {
+                float *to = h_out + (int64_t)now.h[it] * R + 8 * o;
                 *reinterpret_cast<f32x4 *>(to) = f32x4{v[it][0], v[it][1], v[it][2], v[it][3]};
                 *reinterpret_cast<f32x4 *>(to + 4) = f32x4{v[it][4], v[it][5], v[it][6], v[it][7]};
             }
+            u32x4 part[2];
+            split8<2>(v[it], part);
+            if (a >= 0 && item < TILE * OCTS) {
+                if constexpr (RP == 16) {
+                    hs[buf][p >> 4][0][0][16 * o + (p & 15)] = part[0];
+                    hs[buf][p >> 4][0][0][32 + 16 * o + (p & 15)] = part[1];
+                } else {
+                    hs[buf][p >> 4][o >> 2][0][16 * (o & 3) + (p & 15)] = part[0];
+                    hs[buf][p >> 4][o >> 2][P - 1][16 * (o & 3) + (p & 15)] = part[1];
+                }
+            }
         }
-        if (a >= 0 && a != a_held) {
-            load_expand_weights<RP, TRANS, S>(weights + (int64_t)a * R * C, C, R, c, g, ws);
-            a_held = a;
-        }
-        u32x4 bases[2][4];
-        const bool read_base = base != nullptr && !(in_place && a < 0);
+        Cols<L> bases[2][4];
 #pragma unroll
         for (int mb = 0; mb < 2; ++mb)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                bases[mb][i] = u32x4{0u, 0u, 0u, 0u};
-                if (read_base)
-                    bases[mb][i] = *reinterpret_cast<const u32x4 *>(
-                        base + (int64_t)max(rows[mb][i], 0) * ldbase + c);
-            }
-        if (tile + 1 < tile1) load_ids(tile + 1);
+            for (int i = 0; i < 4; ++i) bases[mb][i] = ahead[mb][i];
+        // Before this tile's stores: a load that follows a store waits for it.
+        if (AHEAD && tile + 1 < tile1 && next.a != -2) load_data(next);
+        int rows[2][4];
+#pragma unroll
+        for (int mb = 0; mb < 2; ++mb) {
+            rows[mb][0] = now.rows[mb].x, rows[mb][1] = now.rows[mb].y;
+            rows[mb][2] = now.rows[mb].z, rows[mb][3] = now.rows[mb].w;
+        }
         if (a < 0) {
             // Rows without an adapter: out = base.
             if (!in_place && c_ok) {
@@ -566,163 +681,119 @@ __global__ __launch_bounds__(THREADS, 2) void adapter_expand_kernel(
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         if (rows[mb][i] >= 0)
-                            *reinterpret_cast<u32x4 *>(out + (int64_t)rows[mb][i] * ldo + c) =
-                                bases[mb][i];
+                            bases[mb][i].store(out + (int64_t)rows[mb][i] * ldo + c);
             }
+            if constexpr (!AHEAD) return;
             continue;
         }
-        if (tile > tile0) __syncthreads();   // the tile before has been read
-#pragma unroll
-        for (int it = 0; it < ITEMS; ++it) {
-            const int item = tid + it * THREADS, p = item / OCTS, o = item % OCTS;
-            u32x4 part[2];
-            split8<2>(v[it], part);
-            if (item < TILE * OCTS) {
-                if constexpr (RP == 16) {
-                    hs[p >> 4][0][0][16 * o + (p & 15)] = part[0];
-                    hs[p >> 4][0][0][32 + 16 * o + (p & 15)] = part[1];
-                } else {
-                    hs[p >> 4][o >> 2][0][16 * (o & 3) + (p & 15)] = part[0];
-                    hs[p >> 4][o >> 2][P - 1][16 * (o & 3) + (p & 15)] = part[1];
-                }
-            }
-        }
+        // Two buffers: the next tile is staged while slower waves still read
+        // this one.
         __syncthreads();
 #pragma unroll
         for (int mb = 0; mb < 2; ++mb) {
-            f32x4 acc[8];
+            f32x4 acc[L];
 #pragma unroll
-            for (int t = 0; t < 8; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int t = 0; t < L; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int s = 0; s < S; ++s)
 #pragma unroll
                 for (int p = 0; p < P; ++p) {
-                    const u32x4 operand = hs[mb][s][p][lane];
+                    const u32x4 operand = hs[buf][mb][s][p][lane];
 #pragma unroll
-                    for (int t = 0; t < 8; ++t) acc[t] = mfma(operand, ws[t][s], acc[t]);
+                    for (int t = 0; t < L; ++t) acc[t] = mfma(operand, ws[t][s], acc[t]);
                 }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int row = rows[mb][i];
                 if (row < 0 || !c_ok) continue;
-                uint32_t n[4];
-                if constexpr (DROP)
-                    dropout_words(key, (uint64_t)((int64_t)row * (C >> 3) + (c >> 3)), n);
-                u32x4 o;
+                uint32_t n[L / 2];
+                if constexpr (DROP) numbers_of<L>(key, row, c, C, n);
+                Cols<L> o;
 #pragma unroll
-                for (int d = 0; d < 4; ++d) {
+                for (int d = 0; d < L / 2; ++d) {
                     float lo = acc[2 * d][i], hi = acc[2 * d + 1][i];
                     if constexpr (DROP) {
                         lo = (n[d] & 0xFFFFu) >= drop.threshold ? lo * drop.factor : 0.0f;
                         hi = (n[d] >> 16) >= drop.threshold ? hi * drop.factor : 0.0f;
                     }
-                    lo += __uint_as_float(bases[mb][i][d] << 16);
-                    hi += __uint_as_float(bases[mb][i][d] & 0xFFFF0000u);
-                    o[d] = pack_bf16(lo, hi);
+                    lo += __uint_as_float(bases[mb][i].d[d] << 16);
+                    hi += __uint_as_float(bases[mb][i].d[d] & 0xFFFF0000u);
+                    o.d[d] = pack_bf16(lo, hi);
                 }
-                *reinterpret_cast<u32x4 *>(out + (int64_t)row * ldo + c) = o;
+                o.store(out + (int64_t)row * ldo + c);
             }
         }
+        if constexpr (!AHEAD) return;        // its only tile
+        buf ^= 1;
     }
 }
 
 // ---- weight gradients ---------------------------------------------------------
 
 // One long operand of the weight gradients and the short one beside it:
-// part [slot][R][C] = sum over a chunk's rows of short[row, j] * src[row, c].
+// partial [slot][R][C] = sum over a chunk's rows of short[row, j] * src[row, c].
 struct WgradSide {
     const uint16_t *src;
-    int64_t ld, C;
-    const float *h;             // [parts][rows][R]
-    int parts;
-    int64_t part_stride;
+    int32_t ld;
+    int64_t C;
+    const u32x4 *packed;        // the short operand (pack_tile)
     float *partial;
     int drop;                   // src takes the dropout's mask
 };
 
-// Columns of a lane (its loads' width) and of a workgroup.  Rank 128 takes
-// half as many, so that its sums fit two waves' registers on a SIMD.
+// Columns of a lane and threads of a workgroup of 512 columns.  Rank 128 takes
+// half the columns a lane, so that its sums fit two waves' registers on a SIMD.
 constexpr int wgrad_lane_cols(int rp) { return rp >= 128 ? 4 : 8; }
-constexpr int wgrad_cols(int rp) { return WAVES * 16 * wgrad_lane_cols(rp); }
+constexpr int wgrad_threads(int rp) { return kAdapterCols / wgrad_lane_cols(rp) * 4; }
 
 // Grid: (column blocks of both sides, chunks of tiles).  Per tile of 32 rows a
 // lane reads L columns of its 8 rows and turns them in registers into the
 // operands of L MFMA row blocks (row q of block t is column L q + t of the
-// wave's 16 L); the short operand is split into bf16 parts once per workgroup
-// and held in LDS in operand order.  The next tile's loads of both are in
-// flight while the current one is multiplied.
+// wave's 16 L); the short operand comes through LDS, once for the workgroup.
+// The next tile's loads of both are in flight while the current one is
+// multiplied.
 template <int RP, int PARTS, bool DROP>
-__global__ __launch_bounds__(THREADS, 2) void adapter_wgrad_kernel(PlanView plan, WgradSide left,
-                                                                  WgradSide right, int left_blocks,
-                                                                  int R, int chunk,
-                                                                  DropoutArgs drop) {
-    constexpr int L = wgrad_lane_cols(RP);
-    constexpr int J = RP / 16;
-    constexpr int ITEMS = (RP * 4 + THREADS - 1) / THREADS;   // (rank, 8 rows) per thread
-    __shared__ u32x4 hs[2][PARTS][J][64];
+__global__ __launch_bounds__(wgrad_threads(RP), 2) void adapter_wgrad_kernel(
+    PlanView plan, WgradSide left, WgradSide right, int left_blocks, int R, int chunk,
+    DropoutArgs drop) {
+    constexpr int L = wgrad_lane_cols(RP), NT = wgrad_threads(RP);
+    constexpr int J = RP / 16, PIECES = PARTS * J * 64;
+    constexpr int ITEMS = (PIECES + NT - 1) / NT;
+    __shared__ u32x4 hs[2][PIECES];
     if (!plan.built()) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, g = lane >> 4;
     const bool first = (int)blockIdx.x < left_blocks;
     const WgradSide side = first ? left : right;
     const int block = first ? blockIdx.x : blockIdx.x - left_blocks;
-    const int64_t cw = (int64_t)block * wgrad_cols(RP) + wave * (16 * L);
     const int64_t C = side.C;
+    const int64_t c_lane = (int64_t)block * kAdapterCols + wave * (16 * L) + L * col;
+    const bool c_ok = c_lane < C;
+    const int64_t c = c_ok ? c_lane : 0;     // lanes past the end compute column 0, unstored
+    const uint16_t *src = side.src + c;
     const int live = plan.header[4];
     const int64_t slot = chunk_of_block();
     int tile = (int)min(slot * chunk, (int64_t)live);
     const int tile_end = min(tile + chunk, live);
-    const int64_t c = cw + L * col;
-    const bool c_ok = c < C;
     const DropoutKey key(DROP ? drop.rng : nullptr, DROP);
 
     int rows[8];
     Cols<L> in[8], in_next[8];
-    float h_next[ITEMS][8];
-    auto load_rows = [&](int t) {
+    u32x4 h_next[ITEMS];
+    auto load_tile = [&](int t) {
         const int4 *p = reinterpret_cast<const int4 *>(plan.tile_row + (int64_t)t * TILE + 8 * g);
         const int4 lo = p[0], hi = p[1];
+#pragma unroll
+        for (int it = 0; it < ITEMS; ++it)
+            h_next[it] = side.packed[(int64_t)t * PIECES + min(tid + it * NT, PIECES - 1)];
         rows[0] = lo.x, rows[1] = lo.y, rows[2] = lo.z, rows[3] = lo.w;
         rows[4] = hi.x, rows[5] = hi.y, rows[6] = hi.z, rows[7] = hi.w;
-    };
-    auto load_src = [&]() {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            in_next[i].load(side.src + (int64_t)max(rows[i], 0) * side.ld + (c_ok ? c : 0));
-    };
-    auto load_short = [&](int t) {
-#pragma unroll
-        for (int it = 0; it < ITEMS; ++it) {
-            const int item = tid + it * THREADS, j = item % RP, oct = item / RP;
-            if (ITEMS == 1 && RP * 4 < THREADS && oct >= 4) break;
-            const int4 *q = reinterpret_cast<const int4 *>(plan.tile_row + (int64_t)t * TILE + 8 * oct);
-            const int4 lo = q[0], hi = q[1];
-            const int r[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-            const float *p = side.h + (j < R ? j : 0);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) h_next[it][i] = p[(int64_t)max(r[i], 0) * R];
-            for (int s = 1; s < side.parts; ++s) {
-                p += side.part_stride;
-                float more[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) more[i] = p[(int64_t)max(r[i], 0) * R];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) h_next[it][i] += more[i];
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) h_next[it][i] = r[i] >= 0 && j < R ? h_next[it][i] : 0.0f;
-        }
+        for (int i = 0; i < 8; ++i) in_next[i].load(src + (int64_t)max(rows[i], 0) * side.ld);
     };
     auto stage_short = [&](int buf) {
 #pragma unroll
-        for (int it = 0; it < ITEMS; ++it) {
-            const int item = tid + it * THREADS, j = item % RP, oct = item / RP;
-            if (oct < 4) {
-                u32x4 part[PARTS];
-                split8<PARTS>(h_next[it], part);
-#pragma unroll
-                for (int p = 0; p < PARTS; ++p) hs[buf][p][j >> 4][16 * oct + (j & 15)] = part[p];
-            }
-        }
+        for (int it = 0; it < ITEMS; ++it)
+            if (PIECES % NT == 0 || tid + it * NT < PIECES) hs[buf][tid + it * NT] = h_next[it];
     };
 
     while (tile < tile_end) {
@@ -733,18 +804,18 @@ __global__ __launch_bounds__(THREADS, 2) void adapter_wgrad_kernel(PlanView plan
         for (int t = 0; t < L; ++t)
 #pragma unroll
             for (int jb = 0; jb < J; ++jb) acc[t][jb] = f32x4{0.f, 0.f, 0.f, 0.f};
-        load_rows(tile);
-        load_src();
-        load_short(tile);
+        load_tile(tile);
         int buf = 0;
         __syncthreads();                     // the run before has read both buffers
         stage_short(0);
         __syncthreads();
         for (; tile < stop; ++tile, buf ^= 1) {
+            // A position without a row: its short operand is zero, and its
+            // long one may not be an infinity.
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 in[i] = in_next[i];
-                in[i].clear_unless(c_ok && rows[i] >= 0);
+                in[i].clear_unless(rows[i] >= 0);
             }
             if constexpr (DROP) {
                 if (side.drop) {
@@ -759,11 +830,7 @@ __global__ __launch_bounds__(THREADS, 2) void adapter_wgrad_kernel(PlanView plan
                 }
             }
             const bool more = tile + 1 < stop;
-            if (more) {
-                load_rows(tile + 1);
-                load_src();
-                load_short(tile + 1);
-            }
+            if (more) load_tile(tile + 1);
             u32x4 xs[L];
 #pragma unroll
             for (int t = 0; t < L; ++t)
@@ -773,10 +840,10 @@ __global__ __launch_bounds__(THREADS, 2) void adapter_wgrad_kernel(PlanView plan
                                    ? high_halves(in[2 * d].d[t >> 1], in[2 * d + 1].d[t >> 1])
                                    : low_halves(in[2 * d].d[t >> 1], in[2 * d + 1].d[t >> 1]);
 #pragma unroll
-            for (int jb = 0; jb < J; ++jb)
+            for (int p = 0; p < PARTS; ++p)
 #pragma unroll
-                for (int p = 0; p < PARTS; ++p) {
-                    const u32x4 b = hs[buf][p][jb][lane];
+                for (int jb = 0; jb < J; ++jb) {
+                    const u32x4 b = hs[buf][(p * J + jb) * 64 + lane];
 #pragma unroll
                     for (int t = 0; t < L; ++t) acc[t][jb] = mfma(xs[t], b, acc[t][jb]);
                 }
@@ -784,13 +851,14 @@ __global__ __launch_bounds__(THREADS, 2) void adapter_wgrad_kernel(PlanView plan
             __syncthreads();
         }
         float *out = side.partial + (slot + plan.group_rank[a]) * R * C;
+        const int64_t n0 = c_lane - L * col;
 #pragma unroll
         for (int jb = 0; jb < J; ++jb) {
             const int j = jb * 16 + col;
             if (j >= R) continue;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int64_t n = cw + L * (4 * g + i);
+                const int64_t n = n0 + L * (4 * g + i);
                 if (n >= C) continue;
                 float *p = out + (int64_t)j * C + n;
 #pragma unroll
@@ -812,6 +880,9 @@ __device__ __forceinline__ void store4(void *out, int64_t at, const float v[4]) 
     }
 }
 
+// Partial sums that a thread of the sum has in flight.
+constexpr int SUM_UNROLL = 8;
+
 // Adds an adapter's partial sums in chunk order; an adapter without rows gets
 // zeros.  Grid: (blocks, adapters); a thread owns four results: of dA
 // [R, in] (scaled by the dropout's factor) four columns of a rank; of dB
@@ -831,10 +902,16 @@ __global__ __launch_bounds__(THREADS) void adapter_wgrad_sum_kernel(
         const int64_t e = ((int64_t)blockIdx.x * THREADS + threadIdx.x) * 4;
         if (e >= R * in) return;
         const float *p = part_a + slot0 * R * in + e;
-        for (int s = 0; s < slots; ++s, p += R * in) {
-            const f32x4 q = *reinterpret_cast<const f32x4 *>(p);
+        const int64_t step = R * in;
+        for (int s0 = 0; s0 < slots; s0 += SUM_UNROLL) {
+            f32x4 q[SUM_UNROLL];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] += q[i];
+            for (int s = 0; s < SUM_UNROLL; ++s)
+                q[s] = *reinterpret_cast<const f32x4 *>(p + min(s0 + s, slots - 1) * step);
+#pragma unroll
+            for (int s = 0; s < SUM_UNROLL; ++s)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] += s0 + s < slots ? q[s][i] : 0.0f;
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] *= factor;
@@ -846,9 +923,18 @@ __global__ __launch_bounds__(THREADS) void adapter_wgrad_sum_kernel(
         const int64_t n = e % outs, q = e / outs;
         if (q >= quads) return;
         const float *p = part_b + slot0 * R * outs + q * 4 * outs + n;
-        for (int s = 0; s < slots; ++s, p += R * outs)
+        const int64_t step = R * outs;
+        for (int s0 = 0; s0 < slots; s0 += SUM_UNROLL) {
+            float w[SUM_UNROLL][4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] += p[i * outs];
+            for (int s = 0; s < SUM_UNROLL; ++s)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[s][i] = p[min(s0 + s, slots - 1) * step + i * outs];
+#pragma unroll
+            for (int s = 0; s < SUM_UNROLL; ++s)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] += s0 + s < slots ? w[s][i] : 0.0f;
+        }
         store4<OUT>(db, ((int64_t)a * outs + n) * R + q * 4, v);
     }
 }
@@ -870,11 +956,11 @@ hipError_t by_rank(int rank, F f) {
     return hipGetLastError();
 }
 
-// Tiles of one expand workgroup: more where its weights (rank x 2 bytes a
-// column) weigh more against a tile's base and output (128 bytes a column),
-// while enough workgroups are left.
+// Tiles of one expand workgroup: more where its weights (2 rank bytes a column)
+// weigh more against a tile's base and output (128 bytes a column), while
+// enough workgroups are left.
 int64_t expand_chunk(int64_t tiles, int64_t blocks, int64_t rank) {
-    return std::max<int64_t>(1, std::min<int64_t>(rank / 16, tiles * blocks / 1024));
+    return rank <= 32 ? 1 : std::max<int64_t>(1, std::min(rank / 16, tiles * blocks / 1024));
 }
 
 int64_t part_columns(int64_t C, int parts) { return ((C + parts - 1) / parts + 31) / 32 * 32; }
@@ -904,18 +990,23 @@ template <bool TRANS>
 hipError_t launch_expand(const AdapterArgs &w, const AdapterPlanShape &shape, const int32_t *plan,
                          const DropoutArgs &drop, const float *h, int parts, int64_t C,
                          const uint16_t *base, int64_t ldbase, uint16_t *out, int64_t ldo,
-                         float *h_out, hipStream_t stream) {
+                         float *h_out, const PackArgs &pack, hipStream_t stream) {
     const PlanView v = view_of(shape, plan);
     return by_rank(w.rank, [&](auto rp) {
         const int64_t blocks = (C + kAdapterCols - 1) / kAdapterCols;
         const int64_t chunk = expand_chunk(shape.tiles_max, blocks, w.rank);
-        const dim3 grid = grid_of(blocks, (shape.tiles_max + chunk - 1) / chunk);
+        PackArgs packing = pack;
+        packing.rows = pack.g.packed ? (shape.tiles_max + blocks - 1) / blocks : 0;
+        // Without an output only the packing is done.
+        const dim3 grid =
+            grid_of(blocks, packing.rows + (out ? (shape.tiles_max + chunk - 1) / chunk : 0));
         auto go = [&](auto dropped) {
             hipLaunchKernelGGL((adapter_expand_kernel<decltype(rp)::value, TRANS,
                                                       decltype(dropped)::value>),
-                               grid, dim3(THREADS), 0, stream, v, (int)shape.tiles_max, (int)chunk,
-                               h, parts, shape.rows * w.rank, TRANS ? w.a : w.b, w.rank, C, base, ldbase,
-                               out, ldo, h_out, drop);
+                               grid, dim3(expand_threads(decltype(rp)::value)), 0, stream, v, (int)shape.tiles_max, (int)chunk,
+                               h, parts, shape.rows * w.rank, TRANS ? w.a : w.b, w.rank, C, base,
+                               (int32_t)ldbase,
+                               out, (int32_t)ldo, h_out, packing, drop);
         };
         if constexpr (TRANS) {
             if (drop.rng) return go(std::true_type{});
@@ -965,7 +1056,7 @@ hipError_t launch_adapter_fwd(const AdapterArgs &w, const AdapterPlanShape &shap
         return e;
     const DropoutArgs none = {nullptr, 0, 1.0f};
     return launch_expand<false>(w, shape, plan, none, sums, parts, w.out, base, ldbase, y, ldy, h,
-                                stream);
+                                PackArgs{}, stream);
 }
 
 hipError_t launch_adapter_backward(const AdapterArgs &w, const AdapterPlanShape &shape,
@@ -980,38 +1071,44 @@ hipError_t launch_adapter_backward(const AdapterArgs &w, const AdapterPlanShape 
     const DropoutArgs none = {nullptr, 0, 1.0f};
     if (hipError_t e = launch_shrink<true>(w, shape, plan, none, dy, lddy, w.out, g, parts, stream))
         return e;
-    if (dx) {
-        if (hipError_t e = launch_expand<true>(w, shape, plan, drop, g, parts, w.in, base, ldbase,
-                                               dx, lddx, nullptr, stream))
-            return e;
+    const int split = out_dtype == FP8_DTYPE_FP32 ? 3 : 2;
+    const int64_t packed = layout.packed / 2;
+    char *at = static_cast<char *>(ws) + layout.sums;
+    PackArgs pack{};
+    if (da) {
+        pack.g = {g, parts, reinterpret_cast<u32x4 *>(at)};
+        pack.h = {h, 1, reinterpret_cast<u32x4 *>(at + packed)};
+        pack.split = split;
     }
+    if (hipError_t e = launch_expand<true>(w, shape, plan, drop, g, parts, w.in, base, ldbase, dx,
+                                           lddx, nullptr, pack, stream))
+        return e;
     if (!da) return hipSuccess;
     const PlanView v = view_of(shape, plan);
     const int64_t chunk = adapter_chunk(shape.tiles_max, w.rank, w.in, w.out);
     const int64_t chunks = (shape.tiles_max + chunk - 1) / chunk;
     const int64_t slots = adapter_slots(shape, chunk);
-    float *part_a = reinterpret_cast<float *>(static_cast<char *>(ws) + layout.sums);
+    float *part_a = reinterpret_cast<float *>(at + layout.packed);
     float *part_b = part_a + slots * w.rank * w.in;
-    const WgradSide left = {x, ldx, w.in, g, parts, shape.rows * w.rank, part_a, 1};
-    const WgradSide right = {dy, lddy, w.out, h, 1, 0, part_b, 0};
+    const WgradSide left = {x, (int32_t)ldx, w.in, pack.g.packed, part_a, 1};
+    const WgradSide right = {dy, (int32_t)lddy, w.out, pack.h.packed, part_b, 0};
+    const int left_blocks = (int)((w.in + kAdapterCols - 1) / kAdapterCols);
+    const int right_blocks = (int)((w.out + kAdapterCols - 1) / kAdapterCols);
+    const dim3 grid = grid_of(left_blocks + right_blocks, chunks);
     hipError_t e = by_rank(w.rank, [&](auto rp) {
-        constexpr int cols = wgrad_cols(decltype(rp)::value);
-        const int left_blocks = (int)((w.in + cols - 1) / cols);
-        const int right_blocks = (int)((w.out + cols - 1) / cols);
-        const dim3 grid = grid_of(left_blocks + right_blocks, chunks);
-        auto go = [&](auto split, auto dropped) {
-            hipLaunchKernelGGL((adapter_wgrad_kernel<decltype(rp)::value, decltype(split)::value,
+        auto go = [&](auto parts_, auto dropped) {
+            hipLaunchKernelGGL((adapter_wgrad_kernel<decltype(rp)::value, decltype(parts_)::value,
                                                      decltype(dropped)::value>),
-                               grid, dim3(THREADS), 0, stream, v, left, right, left_blocks, w.rank,
-                               (int)chunk, drop);
+                               grid, dim3(wgrad_threads(decltype(rp)::value)), 0, stream, v, left,
+                               right, left_blocks, w.rank, (int)chunk, drop);
         };
         using Two = std::integral_constant<int, 2>;
         using Three = std::integral_constant<int, 3>;
-        auto by_drop = [&](auto split) {
-            if (drop.rng) go(split, std::true_type{});
-            else go(split, std::false_type{});
+        auto by_drop = [&](auto parts_) {
+            if (drop.rng) go(parts_, std::true_type{});
+            else go(parts_, std::false_type{});
         };
-        if (out_dtype == FP8_DTYPE_FP32) by_drop(Three{});
+        if (split == 3) by_drop(Three{});
         else by_drop(Two{});
     });
     if (e) return e;

@@ -113,9 +113,9 @@ int check_adapter(const fp8_adapters_t *w, const void *plan, int64_t plan_bytes,
     return FP8_OK;
 }
 
-// A row stride of a [rows, cols] bf16 tensor.
-bool bad_stride(int64_t ld, int64_t cols, int64_t rows) {
-    return ld < cols || (ld % 8) != 0 || ld > INT64_MAX / 2 / (rows > 0 ? rows : 1);
+// A row stride of a [rows, cols] bf16 tensor (the kernels hold it in 32 bits).
+bool bad_stride(int64_t ld, int64_t cols) {
+    return ld < cols || (ld % 8) != 0 || ld > INT32_MAX;
 }
 
 AdapterArgs adapter_args(const fp8_adapters_t *w) {
@@ -523,8 +523,8 @@ int fp8_adapter_fwd(const fp8_adapters_t *w, const void *plan, int64_t plan_byte
     DropoutArgs args;
     if (int e = check_adapter(w, plan, plan_bytes, drop, rows, workspace, workspace_bytes, &args))
         return e;
-    if (bad_stride(ldx, w->in, rows) || bad_stride(ldy, w->out, rows) ||
-        (base && bad_stride(ldbase, w->out, rows)))
+    if (bad_stride(ldx, w->in) || bad_stride(ldy, w->out) ||
+        (base && bad_stride(ldbase, w->out)))
         return FP8_ERR_SHAPE;
     if (rows == 0) return FP8_OK;
     if (x == nullptr || y == nullptr) return FP8_ERR_NULL;
@@ -546,9 +546,9 @@ int fp8_adapter_backward(const fp8_adapters_t *w, const void *plan, int64_t plan
         return e;
     if (out_dtype != FP8_DTYPE_FP32 && out_dtype != FP8_DTYPE_BF16) return FP8_ERR_ARG;
     if ((da == nullptr) != (db == nullptr)) return FP8_ERR_ARG;
-    if (bad_stride(lddy, w->out, rows) || (da && bad_stride(ldx, w->in, rows)) ||
-        (dx && (bad_stride(lddx, w->in, rows) ||
-                (dx_base && bad_stride(lddxbase, w->in, rows)))))
+    if (bad_stride(lddy, w->out) || (da && bad_stride(ldx, w->in)) ||
+        (dx && (bad_stride(lddx, w->in) ||
+                (dx_base && bad_stride(lddxbase, w->in)))))
         return FP8_ERR_SHAPE;
     if (!aligned16(da) || !aligned16(db)) return FP8_ERR_ALIGN;
     const AdapterPlanShape shape(rows, w->count);
