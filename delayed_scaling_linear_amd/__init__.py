@@ -561,52 +561,47 @@ class Dropout:
 
 def _on_current_device(*tensors) -> None:
     """The calls run on the current device: tensors of another one are refused."""
-    dev = torch.cuda.current_device()
+    dev = torch.cuda.current_device() if _raw_device is None else _raw_device()
     for t in tensors:
-        if t is not None and t.device.index != dev:
+        if t is not None and t.get_device() != dev:
             raise ValueError(f"tensors must be on the current device cuda:{dev}, got {t.device}")
 
 
-def _matrix(t: torch.Tensor, shape, dtype, what: str) -> None:
-    """t: a 2-D device tensor of this shape and type with unit column stride."""
-    if t.dim() != 2 or tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.dtype != dtype:
+def _matrix(t: torch.Tensor, rows: int, cols: int, dtype, what: str):
+    """(pointer, row stride) of a 2-D device tensor of this shape and type with
+    unit column stride.  A single row's stride plays no part."""
+    shape, stride = t.shape, t.stride()
+    if shape != (rows, cols):
+        raise ValueError(f"{what} must have shape {(rows, cols)}, got {tuple(shape)}")
+    if t.dtype is not dtype:
         raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
-    if t.numel() > 0 and (t.stride(1) != 1 and t.shape[1] > 1):
+    if stride[1] != 1 and cols > 1 and rows > 0:
         raise ValueError(f"{what} must have unit stride in the last dimension")
     if not t.is_cuda:
         raise ValueError(f"{what} must be a device tensor")
+    return t.data_ptr(), stride[0] if rows > 1 and cols > 0 else cols
 
 
-def _stride_of(t: Optional[torch.Tensor]) -> int:
-    """Row stride of an optional matrix; a single row's stride plays no part."""
-    if t is None:
-        return 0
-    return t.stride(0) if t.shape[0] > 1 and t.numel() > 0 else t.shape[1]
+_NONE = (None, 0)     # pointer and stride of a matrix that is not there
 
 
-def _may_share(y: Optional[torch.Tensor], inputs, what: str) -> None:
-    """y may be one of the inputs (same pointer and stride) or lie apart from them."""
-    if y is None or y.numel() == 0:
+def _need_apart(y, t, rows: int, y_cols: int, t_cols: int, size: int, what: str,
+                same: bool = False) -> None:
+    """Refuses an output y (pointer, stride) that overlaps the input t, unless
+    it is t itself and `same` allows that.  Columns of their own in rows of one
+    stride lie apart."""
+    yp, yld = y
+    tp, tld = t
+    if yp is None or tp is None or rows == 0 or y_cols == 0 or t_cols == 0:
         return
-    end = lambda t: t.data_ptr() + ((t.shape[0] - 1) * _stride_of(t) + t.shape[1]) * t.element_size()
-    for t in inputs:
-        if t is None or t.numel() == 0:
-            continue
-        if y.data_ptr() == t.data_ptr() and _stride_of(y) == _stride_of(t):
-            continue
-        if y.data_ptr() < end(t) and t.data_ptr() < end(y) and not _columns_apart(y, t):
-            raise ValueError(f"{what} must be an input itself or not overlap it")
-
-
-def _columns_apart(y: torch.Tensor, t: torch.Tensor) -> bool:
-    """Whether two matrices of one row stride lie in columns of their own."""
-    ld = _stride_of(y)
-    if ld != _stride_of(t) or y.element_size() != t.element_size():
-        return False
-    gap = (t.data_ptr() - y.data_ptr()) // y.element_size() % ld
-    return y.shape[1] <= gap and gap + t.shape[1] <= ld
+    if same and yp == tp and yld == tld:
+        return
+    if yp >= tp + ((rows - 1) * tld + t_cols) * size or tp >= yp + ((rows - 1) * yld + y_cols) * size:
+        return
+    gap = (tp - yp) // size % yld
+    if yld != tld or gap < y_cols or gap + t_cols > yld:
+        raise ValueError(f"{what} must not overlap an input"
+                         + (" unless it is that input itself" if same else ""))
 
 
 def fp8_dropout(x: torch.Tensor, drop: Dropout, y: torch.Tensor,
@@ -615,23 +610,25 @@ def fp8_dropout(x: torch.Tensor, drop: Dropout, y: torch.Tensor,
     tensors of one shape and type with unit column stride (column slices are
     fine).  The gradient of x is the same call on the gradient of y without
     the residual.  y may be x or residual."""
-    if x.dtype == torch.bfloat16:
-        dt = DTYPE_BF16
-    elif x.dtype == torch.float32:
-        dt = DTYPE_FP32
+    dtype = x.dtype
+    if dtype is torch.bfloat16:
+        dt, size = DTYPE_BF16, 2
+    elif dtype is torch.float32:
+        dt, size = DTYPE_FP32, 4
     else:
         raise TypeError("x must be bf16 or fp32")
-    _matrix(x, x.shape, x.dtype, "x")
-    _matrix(y, x.shape, x.dtype, "y")
-    if residual is not None:
-        _matrix(residual, x.shape, x.dtype, "residual")
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D")
+    rows, cols = x.shape
+    xm = _matrix(x, rows, cols, dtype, "x")
+    ym = _matrix(y, rows, cols, dtype, "y")
+    rm = _NONE if residual is None else _matrix(residual, rows, cols, dtype, "residual")
     d = drop.desc()
     _on_current_device(x, y, residual, drop.rng)
-    _may_share(y, (x, residual), "y")
-    _check(lib().fp8_dropout(ctypes.byref(d), x.data_ptr(), _stride_of(x),
-                             None if residual is None else residual.data_ptr(),
-                             _stride_of(residual), y.data_ptr(), _stride_of(y), dt, x.shape[0],
-                             x.shape[1], _stream(stream)), "fp8_dropout")
+    _need_apart(ym, xm, rows, cols, cols, size, "y", same=True)
+    _need_apart(ym, rm, rows, cols, cols, size, "y", same=True)
+    _check(lib().fp8_dropout(ctypes.byref(d), *xm, *rm, *ym, dt, rows, cols, _stream(stream)),
+           "fp8_dropout")
 
 
 def fp8_dropout_cast_transpose_amax(x: torch.Tensor, drop: Dropout, scale: torch.Tensor,
@@ -651,25 +648,27 @@ def fp8_dropout_cast_transpose_amax(x: torch.Tensor, drop: Dropout, scale: torch
     _need_scalar(scale, "scale")
     _need_scalar(amax_cur, "amax_cur")
     _need_scalar(noop_flag, "noop_flag")
-    _matrix(x, x.shape, torch.bfloat16, "x")
-    for t, n in ((residual, "residual"), (y, "y")):
-        if t is not None:
-            _matrix(t, x.shape, torch.bfloat16, n)
-    _need_shape(dbias, (x.shape[1],), "dbias")
-    if dbias is not None and workspace is None:
-        raise ValueError("dbias needs a workspace")
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D")
+    rows, cols = x.shape
+    xm = _matrix(x, rows, cols, torch.bfloat16, "x")
+    rm = _NONE if residual is None else _matrix(residual, rows, cols, torch.bfloat16, "residual")
+    ym = _NONE if y is None else _matrix(y, rows, cols, torch.bfloat16, "y")
+    if dbias is not None:
+        _need_shape(dbias, (cols,), "dbias")
+        if workspace is None:
+            raise ValueError("dbias needs a workspace")
     d, o = drop.desc(), out.desc()
     _on_current_device(x, residual, y, drop.rng, scale, out.data, out.data_t, out.scale_inv,
                        amax_cur, dbias, workspace, noop_flag)
-    _may_share(y, (x, residual), "y")
-    ws, ws_bytes = _ws(workspace)
+    if y is not None:
+        _need_apart(ym, xm, rows, cols, cols, 2, "y", same=True)
+        _need_apart(ym, rm, rows, cols, cols, 2, "y", same=True)
     _check(lib().fp8_dropout_cast_transpose_amax(
-        ctypes.byref(d), x.data_ptr(), _stride_of(x),
-        None if residual is None else residual.data_ptr(), _stride_of(residual),
-        None if y is None else y.data_ptr(), _stride_of(y), x.shape[0], x.shape[1],
-        _ptr(scale, torch.float32, "scale"), ctypes.byref(o),
-        _ptr(amax_cur, torch.float32, "amax_cur"), _ptr(dbias, torch.float32, "dbias"), ws,
-        ws_bytes, _ptr(noop_flag, torch.int32, "noop_flag"), _stream(stream)),
+        ctypes.byref(d), *xm, *rm, *ym, rows, cols, _ptr(scale, torch.float32, "scale"),
+        ctypes.byref(o), _ptr(amax_cur, torch.float32, "amax_cur"),
+        _ptr(dbias, torch.float32, "dbias"), *_ws(workspace),
+        _ptr(noop_flag, torch.int32, "noop_flag"), _stream(stream)),
         "fp8_dropout_cast_transpose_amax")
 
 
@@ -682,16 +681,18 @@ class Adapters:
     alpha: torch.Tensor
 
     def desc(self) -> _AdaptersDesc:
-        if self.a.dim() != 3 or self.b.dim() != 3:
+        a, b, alpha = self.a, self.b, self.alpha
+        if a.dim() != 3 or b.dim() != 3:
             raise ValueError("Adapters.a and Adapters.b must be 3-D")
-        count, rank, n_in = self.a.shape
-        n_out = self.b.shape[1]
-        _need_shape(self.b, (count, n_out, rank), "Adapters.b")
-        _need_shape(self.alpha, (count,), "Adapters.alpha")
-        return _AdaptersDesc(_ptr(self.a, torch.bfloat16, "Adapters.a"),
-                             _ptr(self.b, torch.bfloat16, "Adapters.b"),
-                             _ptr(self.alpha, torch.float32, "Adapters.alpha"), count, rank, n_in,
-                             n_out)
+        count, rank, n_in = a.shape
+        n_out = b.shape[1]
+        if b.shape != (count, n_out, rank):
+            _need_shape(b, (count, n_out, rank), "Adapters.b")
+        if alpha.shape != (count,):
+            _need_shape(alpha, (count,), "Adapters.alpha")
+        return _AdaptersDesc(_ptr(a, torch.bfloat16, "Adapters.a"),
+                             _ptr(b, torch.bfloat16, "Adapters.b"),
+                             _ptr(alpha, torch.float32, "Adapters.alpha"), count, rank, n_in, n_out)
 
 
 @dataclass
@@ -729,15 +730,15 @@ def fp8_adapter_plan(row_adapter: torch.Tensor, plan: AdapterPlan, stream=None) 
     """Build `plan` for row_adapter [rows] (int32; any value outside
     0 .. adapters - 1 marks a row without an adapter)."""
     _need_shape(row_adapter, (plan.rows,), "row_adapter")
-    buf, size = _ws(plan.buf)
     ids = _ptr(row_adapter, torch.int32, "row_adapter")
     _on_current_device(row_adapter, plan.buf)
-    _check(lib().fp8_adapter_plan(ids, plan.rows, plan.adapters, buf, size, _stream(stream)),
+    _check(lib().fp8_adapter_plan(ids, plan.rows, plan.adapters, *_ws(plan.buf), _stream(stream)),
            "fp8_adapter_plan")
     plan.built = True
 
 
 def _adapter_call(w: Adapters, plan: AdapterPlan, rows: int, workspace, drop):
+    """The arguments that both adapter calls begin with, and the workspace's."""
     if not plan.built:
         raise ValueError("the plan has not been built (fp8_adapter_plan)")
     if plan.rows != rows or plan.adapters != w.a.shape[0]:
@@ -745,15 +746,9 @@ def _adapter_call(w: Adapters, plan: AdapterPlan, rows: int, workspace, drop):
                          f"has {rows} and {w.a.shape[0]}")
     if workspace is None:
         raise ValueError("workspace is required (fp8_adapter_workspace_bytes)")
-    ws, ws_bytes = _ws(workspace)
-    dw, (buf, size) = w.desc(), _ws(plan.buf)
-    dd = None if drop is None else drop.desc()
-    _on_current_device(w.a, w.b, w.alpha, plan.buf, workspace, None if drop is None else drop.rng)
-    return (ctypes.byref(dw), buf, size, None if dd is None else ctypes.byref(dd)), ws, ws_bytes
-
-
-def _strided(t: Optional[torch.Tensor]):
-    return (None, 0) if t is None else (t.data_ptr(), _stride_of(t))
+    head = (ctypes.byref(w.desc()), *_ws(plan.buf),
+            None if drop is None else ctypes.byref(drop.desc()))
+    return head, _ws(workspace)
 
 
 def fp8_adapter_fwd(w: Adapters, plan: AdapterPlan, x: torch.Tensor,
@@ -764,26 +759,19 @@ def fp8_adapter_fwd(w: Adapters, plan: AdapterPlan, x: torch.Tensor,
     row's adapter; rows without one: y = base, h = 0.  x [rows, in], base
     (None: zeros) and y are bf16 with unit column stride; y may be base.  h
     [rows, rank] (fp32) is kept for fp8_adapter_backward if it is given."""
-    rows, n_out = x.shape[0], w.b.shape[1]
-    _matrix(x, (rows, w.a.shape[2]), torch.bfloat16, "x")
-    _matrix(y, (rows, n_out), torch.bfloat16, "y")
-    if base is not None:
-        _matrix(base, (rows, n_out), torch.bfloat16, "base")
-    _need_shape(h, (rows, w.a.shape[1]), "h")
-    head, ws, ws_bytes = _adapter_call(w, plan, rows, workspace, drop)
-    _on_current_device(x, y, base, h)
-    _may_share(y, (base,), "y")
-    _apart(y, x, "y", "x")
-    _check(lib().fp8_adapter_fwd(*head, *_strided(x), *_strided(base), *_strided(y), rows,
-                                 _ptr(h, torch.float32, "h"), ws, ws_bytes, _stream(stream)),
-           "fp8_adapter_fwd")
-
-
-def _apart(y: Optional[torch.Tensor], t: Optional[torch.Tensor], what: str, other: str) -> None:
-    if y is not None and t is not None and y.numel() and t.numel() \
-            and y.data_ptr() == t.data_ptr():
-        raise ValueError(f"{what} must not be {other}")
-    _may_share(y, (t,), what)
+    rows, (_, rank, n_in), n_out = plan.rows, w.a.shape, w.b.shape[1]
+    xm = _matrix(x, rows, n_in, torch.bfloat16, "x")
+    ym = _matrix(y, rows, n_out, torch.bfloat16, "y")
+    bm = _NONE if base is None else _matrix(base, rows, n_out, torch.bfloat16, "base")
+    if h is not None:
+        _need_shape(h, (rows, rank), "h")
+    head, ws = _adapter_call(w, plan, rows, workspace, drop)
+    _on_current_device(w.a, w.b, w.alpha, plan.buf, x, y, base, h, workspace,
+                       None if drop is None else drop.rng)
+    _need_apart(ym, bm, rows, n_out, n_out, 2, "y", same=True)
+    _need_apart(ym, xm, rows, n_out, n_in, 2, "y")
+    _check(lib().fp8_adapter_fwd(*head, *xm, *bm, *ym, rows, _ptr(h, torch.float32, "h"), *ws,
+                                 _stream(stream)), "fp8_adapter_fwd")
 
 
 def fp8_adapter_backward(w: Adapters, plan: AdapterPlan, x: Optional[torch.Tensor],
@@ -797,35 +785,34 @@ def fp8_adapter_backward(w: Adapters, plan: AdapterPlan, x: Optional[torch.Tenso
     may be dx_base, and dx_base None stands for zeros) and da [count, rank,
     in], db [count, out, rank] (both fp32 or both bf16; both None: none, and
     x and h are not read).  `drop`, x and h as in the forward."""
-    rows = dy.shape[0]
-    count, rank, n_in = w.a.shape
-    n_out = w.b.shape[1]
-    _matrix(dy, (rows, n_out), torch.bfloat16, "dy")
-    for t, n in ((dx, "dx"), (dx_base, "dx_base"), (x, "x")):
-        if t is not None:
-            _matrix(t, (rows, n_in), torch.bfloat16, n)
-    _need_shape(h, (rows, rank), "h")
-    _need_shape(da, (count, rank, n_in), "da")
-    _need_shape(db, (count, n_out, rank), "db")
+    rows, (count, rank, n_in), n_out = plan.rows, w.a.shape, w.b.shape[1]
+    bf16 = torch.bfloat16
+    gm = _matrix(dy, rows, n_out, bf16, "dy")
+    xm = _NONE if x is None else _matrix(x, rows, n_in, bf16, "x")
+    om = _NONE if dx is None else _matrix(dx, rows, n_in, bf16, "dx")
+    bm = _NONE if dx_base is None else _matrix(dx_base, rows, n_in, bf16, "dx_base")
     if (da is None) != (db is None):
         raise ValueError("da and db come together")
     dtype = DTYPE_FP32
     if da is not None:
         if x is None or h is None:
             raise ValueError("da and db need x and h")
-        if da.dtype != db.dtype or da.dtype not in (torch.float32, torch.bfloat16):
+        _need_shape(h, (rows, rank), "h")
+        _need_shape(da, (count, rank, n_in), "da")
+        _need_shape(db, (count, n_out, rank), "db")
+        if da.dtype != db.dtype or da.dtype not in (torch.float32, bf16):
             raise TypeError("da and db must both be fp32 or both bf16")
         dtype = DTYPE_FP32 if da.dtype == torch.float32 else DTYPE_BF16
-    head, ws, ws_bytes = _adapter_call(w, plan, rows, workspace, drop)
-    _on_current_device(x, dy, h, dx, dx_base, da, db)
-    _may_share(dx, (dx_base,), "dx")
-    _apart(dx, dy, "dx", "dy")
-    _apart(dx, x, "dx", "x")
-    _check(lib().fp8_adapter_backward(*head, *_strided(x), *_strided(dy),
-                                      _ptr(h, torch.float32, "h"), *_strided(dx_base),
-                                      *_strided(dx), rows, _ptr(da, None, "da"),
-                                      _ptr(db, None, "db"), dtype, ws, ws_bytes, _stream(stream)),
-           "fp8_adapter_backward")
+    head, ws = _adapter_call(w, plan, rows, workspace, drop)
+    _on_current_device(w.a, w.b, w.alpha, plan.buf, x, dy, h, dx, dx_base, da, db, workspace,
+                       None if drop is None else drop.rng)
+    if dx is not None:
+        _need_apart(om, bm, rows, n_in, n_in, 2, "dx", same=True)
+        _need_apart(om, gm, rows, n_in, n_out, 2, "dx")
+        _need_apart(om, xm, rows, n_in, n_in, 2, "dx")
+    _check(lib().fp8_adapter_backward(*head, *xm, *gm, _ptr(h, torch.float32, "h"), *bm, *om, rows,
+                                      _ptr(da, None, "da"), _ptr(db, None, "db"), dtype, *ws,
+                                      _stream(stream)), "fp8_adapter_backward")
 
 
 def fp8_cast_transpose_dynamic(x: torch.Tensor, scale: torch.Tensor, out: Float8Tensor,

@@ -728,6 +728,176 @@ __global__ __launch_bounds__(expand_threads(RP), 2) void adapter_expand_kernel(
     }
 }
 
+// ---- few rows: shrink and expand in one launch ----------------------------------
+
+// A decode step's batch is bound by the launches and by the chain of loads, not
+// by the bytes.  Here every column block of a tile computes the tile's whole h
+// by itself (the adapter's A comes from the L2) and goes on to its columns of
+// the output; the base and B are on their way while h is computed.
+// Grid: (blocks of 512 columns, tiles).  Lane layouts as in the two kernels.
+template <int RP, bool DROP>
+__global__ __launch_bounds__(THREADS, 2) void adapter_small_kernel(
+    PlanView plan, const uint16_t *__restrict__ x, int32_t ldx, int64_t K,
+    const uint16_t *__restrict__ wa, const uint16_t *__restrict__ wb,
+    const float *__restrict__ alpha, int R, int64_t C, const uint16_t *base, int32_t ldbase,
+    uint16_t *out, int32_t ldo, float *h_out, DropoutArgs drop) {
+    constexpr int S = RP == 16 ? 1 : RP / 32, P = RP == 16 ? 1 : 2, L = 8, OCTS = RP / 8;
+    __shared__ float red[WAVES][TILE * RP];
+    __shared__ u32x4 hs[2][S][P][64];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, g = lane >> 4;
+    const int64_t c_lane = (int64_t)blockIdx.x * kAdapterCols + wave * (16 * L) + L * col;
+    const bool c_ok = c_lane < C;
+    const int64_t c = c_ok ? c_lane : 0;
+    const int64_t tile = chunk_of_block();
+    const int32_t *tile_row = plan.tile_row + tile * TILE;
+    const int a = plan.tile_adapter[tile];
+    int h_row[2], rows[2][4];
+#pragma unroll
+    for (int mb = 0; mb < 2; ++mb) {
+        h_row[mb] = tile_row[16 * mb + col];
+        const int4 r = *reinterpret_cast<const int4 *>(tile_row + 16 * mb + 4 * g);
+        rows[mb][0] = r.x, rows[mb][1] = r.y, rows[mb][2] = r.z, rows[mb][3] = r.w;
+    }
+    const int stage_row = tile_row[min(tid / OCTS, TILE - 1)];
+    const bool two = tile_row[16] >= 0;                  // rows in the tile's second half
+    if (!plan.built() || a == -2) return;
+
+    Cols<L> bases[2][4];
+    const bool in_place = base == out && ldbase == ldo;
+    const bool read_base = base != nullptr && !(in_place && a < 0);
+#pragma unroll
+    for (int mb = 0; mb < 2; ++mb)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (read_base && (mb == 0 || two))
+                bases[mb][i].load(base + (int64_t)max(rows[mb][i], 0) * ldbase + c);
+            else
+                bases[mb][i].clear_unless(false);
+        }
+    const int so = tid % OCTS, sp = tid / OCTS;          // the 8 ranks of a row this thread sums
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+    auto store_h = [&]() {
+        if (h_out != nullptr && blockIdx.x == 0 && sp < TILE && stage_row >= 0 && 8 * so < R) {
+            float *to = h_out + (int64_t)stage_row * R + 8 * so;
+            *reinterpret_cast<f32x4 *>(to) = f32x4{v[0], v[1], v[2], v[3]};
+            *reinterpret_cast<f32x4 *>(to + 4) = f32x4{v[4], v[5], v[6], v[7]};
+        }
+    };
+    if (a < 0) {
+        store_h();
+        if (in_place || !c_ok) return;
+#pragma unroll
+        for (int mb = 0; mb < 2; ++mb)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (rows[mb][i] >= 0) bases[mb][i].store(out + (int64_t)rows[mb][i] * ldo + c);
+        return;
+    }
+    u32x4 ws[L][S];
+    load_expand_weights<RP, false, S, L>(wb + (int64_t)a * R * C, C, R, c, g, ws);
+
+    const DropoutKey key(DROP ? drop.rng : nullptr, DROP);
+    const uint16_t *w = wa + (int64_t)a * R * K;
+    const int64_t kw = ((K + WAVES - 1) / WAVES + 31) / 32 * 32;
+    const int64_t k0 = wave * kw, k1 = min(k0 + kw, K);
+    const uint16_t *px[2];
+#pragma unroll
+    for (int mb = 0; mb < 2; ++mb) {
+        h_row[mb] = max(h_row[mb], 0);
+        px[mb] = x + (int64_t)h_row[mb] * ldx;
+    }
+    f32x4 acc[2][RP / 16];
+#pragma unroll
+    for (int mb = 0; mb < 2; ++mb)
+#pragma unroll
+        for (int jb = 0; jb < RP / 16; ++jb) acc[mb][jb] = f32x4{0.f, 0.f, 0.f, 0.f};
+    constexpr int U = RP >= 64 ? 4 : 8;
+    for (int64_t kk = k0; kk < k1; kk += 32 * U) {
+        u32x4 xs[U][2], as[U][RP / 16];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t k = kk + 32 * u + 8 * g, kc = k < k1 ? k : k0;
+#pragma unroll
+            for (int mb = 0; mb < 2; ++mb)
+                if (mb == 0 || two) xs[u][mb] = *reinterpret_cast<const u32x4 *>(px[mb] + kc);
+            load_shrink_weights<RP, false>(w, K, R, kc, col, as[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t k = kk + 32 * u + 8 * g;
+#pragma unroll
+            for (int mb = 0; mb < 2; ++mb) {
+                if (mb == 1 && !two) continue;
+                if constexpr (DROP)
+                    xs[u][mb] = keep_chunk(xs[u][mb], key,
+                                           (uint64_t)(h_row[mb] * (K >> 3) + (k >> 3)),
+                                           drop.threshold);
+#pragma unroll
+                for (int d = 0; d < 4; ++d) xs[u][mb][d] = k < k1 ? xs[u][mb][d] : 0u;
+#pragma unroll
+                for (int jb = 0; jb < RP / 16; ++jb)
+                    acc[mb][jb] = mfma(xs[u][mb], as[u][jb], acc[mb][jb]);
+            }
+        }
+    }
+#pragma unroll
+    for (int mb = 0; mb < 2; ++mb)
+#pragma unroll
+        for (int jb = 0; jb < RP / 16; ++jb)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                red[wave][(16 * mb + 4 * g + i) * RP + jb * 16 + col] = acc[mb][jb][i];
+    __syncthreads();
+    const float scale = alpha[a] * drop.factor;
+    if (sp < TILE) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int e = sp * RP + 8 * so + i;
+            v[i] = scale * (((red[0][e] + red[1][e]) + red[2][e]) + red[3][e]);
+            v[i] = stage_row >= 0 && 8 * so < R ? v[i] : 0.0f;
+        }
+        u32x4 part[2];
+        split8<2>(v, part);
+        if constexpr (RP == 16) {
+            hs[sp >> 4][0][0][16 * so + (sp & 15)] = part[0];
+            hs[sp >> 4][0][0][32 + 16 * so + (sp & 15)] = part[1];
+        } else {
+            hs[sp >> 4][so >> 2][0][16 * (so & 3) + (sp & 15)] = part[0];
+            hs[sp >> 4][so >> 2][P - 1][16 * (so & 3) + (sp & 15)] = part[1];
+        }
+    }
+    store_h();
+    __syncthreads();
+#pragma unroll
+    for (int mb = 0; mb < 2; ++mb) {
+        if (mb == 1 && !two) break;
+        f32x4 sum[L];
+#pragma unroll
+        for (int t = 0; t < L; ++t) sum[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+                const u32x4 operand = hs[mb][s][p][lane];
+#pragma unroll
+                for (int t = 0; t < L; ++t) sum[t] = mfma(operand, ws[t][s], sum[t]);
+            }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (rows[mb][i] < 0 || !c_ok) continue;
+            Cols<L> o;
+#pragma unroll
+            for (int d = 0; d < L / 2; ++d)
+                o.d[d] = pack_bf16(sum[2 * d][i] + __uint_as_float(bases[mb][i].d[d] << 16),
+                                   sum[2 * d + 1][i] +
+                                       __uint_as_float(bases[mb][i].d[d] & 0xFFFF0000u));
+            o.store(out + (int64_t)rows[mb][i] * ldo + c);
+        }
+    }
+}
+
 // ---- weight gradients ---------------------------------------------------------
 
 // One long operand of the weight gradients and the short one beside it:
@@ -963,6 +1133,8 @@ int64_t expand_chunk(int64_t tiles, int64_t blocks, int64_t rank) {
     return rank <= 32 ? 1 : std::max<int64_t>(1, std::min(rank / 16, tiles * blocks / 1024));
 }
 
+constexpr int64_t SMALL_TILE_BYTES = 256 << 10, SMALL_ALL_BYTES = 64 << 20;
+
 int64_t part_columns(int64_t C, int parts) { return ((C + parts - 1) / parts + 31) / 32 * 32; }
 
 template <bool TRANS>
@@ -1015,6 +1187,37 @@ hipError_t launch_expand(const AdapterArgs &w, const AdapterPlanShape &shape, co
     });
 }
 
+// Whether the forward runs in one launch (adapter_small_kernel): its column
+// blocks read each tile's A and x again, which pays while a block's read and
+// all of them together stay small against the launch that is saved.
+bool one_launch(const AdapterArgs &w, const AdapterPlanShape &shape) {
+    const int64_t blocks = (w.out + kAdapterCols - 1) / kAdapterCols;
+    const int64_t a_bytes = adapter_padded_rank(w.rank) * w.in * 2;
+    return w.rank <= 64 && a_bytes <= SMALL_TILE_BYTES &&
+           shape.tiles_max * blocks * a_bytes <= SMALL_ALL_BYTES;
+}
+
+hipError_t launch_small(const AdapterArgs &w, const AdapterPlanShape &shape, const int32_t *plan,
+                        const DropoutArgs &drop, const uint16_t *x, int64_t ldx,
+                        const uint16_t *base, int64_t ldbase, uint16_t *y, int64_t ldy, float *h,
+                        hipStream_t stream) {
+    const PlanView v = view_of(shape, plan);
+    const dim3 grid = grid_of((w.out + kAdapterCols - 1) / kAdapterCols, shape.tiles_max);
+    auto go = [&](auto rp, auto dropped) {
+        hipLaunchKernelGGL((adapter_small_kernel<decltype(rp)::value, decltype(dropped)::value>),
+                           grid, dim3(THREADS), 0, stream, v, x, (int32_t)ldx, w.in, w.a, w.b,
+                           w.alpha, w.rank, w.out, base, (int32_t)ldbase, y, (int32_t)ldy, h, drop);
+    };
+    auto by_drop = [&](auto rp) {
+        if (drop.rng) go(rp, std::true_type{});
+        else go(rp, std::false_type{});
+    };
+    if (w.rank <= 16) by_drop(std::integral_constant<int, 16>{});
+    else if (w.rank <= 32) by_drop(std::integral_constant<int, 32>{});
+    else by_drop(std::integral_constant<int, 64>{});
+    return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_adapter_plan(const int32_t *row_adapter, const AdapterPlanShape &shape,
@@ -1050,6 +1253,7 @@ hipError_t launch_adapter_fwd(const AdapterArgs &w, const AdapterPlanShape &shap
                               const int32_t *plan, const DropoutArgs &drop, const uint16_t *x,
                               int64_t ldx, const uint16_t *base, int64_t ldbase, uint16_t *y,
                               int64_t ldy, float *h, void *ws, hipStream_t stream) {
+    if (one_launch(w, shape)) return launch_small(w, shape, plan, drop, x, ldx, base, ldbase, y, ldy, h, stream);
     const int parts = adapter_parts(shape.tiles_max, w.in);
     float *sums = parts == 1 && h ? h : static_cast<float *>(ws);
     if (hipError_t e = launch_shrink<false>(w, shape, plan, drop, x, ldx, w.in, sums, parts, stream))

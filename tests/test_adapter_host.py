@@ -156,6 +156,9 @@ def test_binding_refusals():
     plan.built = True
     with pytest.raises(ValueError, match="8 rows and 2 adapters"):
         dsl._adapter_call(w, plan, 9, None, None)
+    with pytest.raises(ValueError, match="8 rows and 2 adapters"):
+        dsl._adapter_call(dsl.Adapters(bf(3, 16, 64), bf(3, 128, 16), torch.ones(3)), plan, 8, None,
+                          None)
     with pytest.raises(ValueError, match="workspace is required"):
         dsl._adapter_call(w, plan, 8, None, None)
     with pytest.raises(ValueError, match="device tensor"):
@@ -164,6 +167,5 @@ def test_binding_refusals():
         dsl.fp8_adapter_fwd(w, plan, bf(8, 72), None, bf(8, 128))
     with pytest.raises(ValueError, match="dy must have shape"):
         dsl.fp8_adapter_backward(w, plan, bf(8, 64), bf(8, 120))
-    with pytest.raises(ValueError, match="must not be"):
-        t = bf(8, 64)
-        dsl._apart(t, t, "y", "x")
+    with pytest.raises(ValueError, match="overlap"):       # not even the input itself
+        dsl._need_apart((0x1000, 64), (0x1000, 64), 8, 64, 64, 2, "y")

@@ -113,15 +113,15 @@ def test_binding_refusals():
     with pytest.raises(ValueError, match="device tensor"):
         dsl.fp8_dropout(bf(4, 8), drop, bf(4, 8))
     with pytest.raises(ValueError, match="shape"):
-        dsl._matrix(bf(4, 8), (4, 16), torch.bfloat16, "y")
+        dsl._matrix(bf(4, 8), 4, 16, torch.bfloat16, "y")
     with pytest.raises(ValueError, match="two elements"):
         dsl.Dropout(0.1, torch.zeros(3, dtype=torch.int64)).desc()
     with pytest.raises(ValueError, match="device tensor"):
         drop.desc()
     with pytest.raises(ValueError, match="unit stride"):
-        dsl._matrix(bf(8, 4).t(), (4, 8), torch.bfloat16, "x")
+        dsl._matrix(bf(8, 4).t(), 4, 8, torch.bfloat16, "x")
     with pytest.raises(TypeError, match="must be"):
-        dsl._matrix(torch.zeros(4, 8), (4, 8), torch.bfloat16, "y")
+        dsl._matrix(torch.zeros(4, 8), 4, 8, torch.bfloat16, "y")
 
 
 def test_binding_overlap():
@@ -129,10 +129,19 @@ def test_binding_overlap():
     tensor included); anything else is refused."""
     wide = torch.zeros(8, 48, dtype=torch.bfloat16)
     a, b, c = wide[:, :16], wide[:, 16:32], wide[:, 8:24]
-    dsl._may_share(a, (a, b, None), "y")
-    dsl._may_share(b, (a,), "y")
-    dsl._may_share(wide[:, 32:], (a, b), "y")
-    for y, x in ((a, c), (c, a), (c, b), (wide[1:], wide[:-1])):
+
+    def check(y, t, same=True):
+        dsl._need_apart((y.data_ptr(), y.stride(0)), (t.data_ptr(), t.stride(0)), y.shape[0],
+                        y.shape[1], t.shape[1], 2, "y", same=same)
+
+    check(a, a)
+    check(a, b)
+    check(b, a)
+    check(wide[:, 32:], a)
+    check(wide[4:], wide[:4])
+    dsl._need_apart((a.data_ptr(), 48), dsl._NONE, 8, 16, 16, 2, "y")
+    for y, t in ((a, c), (c, a), (c, b), (wide[1:], wide[:-1])):
         with pytest.raises(ValueError, match="overlap"):
-            dsl._may_share(y, (x,), "y")
-    dsl._may_share(wide[4:], (wide[:4],), "y")
+            check(y, t)
+    with pytest.raises(ValueError, match="overlap"):
+        check(a, a, same=False)
