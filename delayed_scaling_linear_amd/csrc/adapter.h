@@ -43,17 +43,19 @@ struct AdapterPlanShape {
     }
 };
 
-// K parts of the contraction over C columns (workgroups per tile of the
-// shrink kernel): enough for a workgroup per CU, each at least 256
-// columns, at most 16.
-inline int adapter_parts(int64_t tiles, int64_t C) {
-    const int64_t want = 256 / std::max<int64_t>(tiles, 1);
-    return (int)std::max<int64_t>(1, std::min<int64_t>({want, C / 256, 16}));
-}
-
 // Ranks as the kernels see them: the next of 16, 32, 64, 128.
 inline int64_t adapter_padded_rank(int64_t rank) {
     return rank <= 16 ? 16 : rank <= 32 ? 32 : rank <= 64 ? 64 : 128;
+}
+
+// K parts of the contraction over C columns (workgroups per tile, or per two
+// tiles of rank 128, of the shrink kernel): a workgroup per CU, each at least 256
+// columns, at most 16.  (More of them than CUs measured no faster at 257 and 265
+// tiles, and every part is one more read of the sums for the kernels behind.)
+inline int adapter_parts(int64_t tiles, int64_t C, int64_t rank) {
+    const int64_t groups = rank > 64 ? (tiles + 1) / 2 : tiles;
+    const int64_t want = 256 / std::max<int64_t>(groups, 1);
+    return (int)std::max<int64_t>(1, std::min<int64_t>({want, C / 256, 16}));
 }
 
 // Tiles of one weight-gradient workgroup: a partial sum of R fp32 per column
@@ -77,8 +79,8 @@ inline int64_t adapter_slots(const AdapterPlanShape &p, int64_t chunk) {
 struct AdapterWorkspace {
     int64_t sums, packed, grads, bytes;
     AdapterWorkspace(const AdapterPlanShape &p, int64_t rank, int64_t in, int64_t out) {
-        const int64_t parts = std::max(adapter_parts(p.tiles_max, in),
-                                       adapter_parts(p.tiles_max, out));
+        const int64_t parts = std::max(adapter_parts(p.tiles_max, in, rank),
+                                       adapter_parts(p.tiles_max, out, rank));
         sums = (parts * p.rows * rank * 4 + 255) / 256 * 256;
         packed = 2 * p.tiles_max * kAdapterTile * adapter_padded_rank(rank) * 3 * 2;
         grads = adapter_slots(p, adapter_chunk(p.tiles_max, rank, in, out)) * rank * (in + out) * 4;

@@ -216,163 +216,15 @@ __global__ __launch_bounds__(THREADS) void adapter_plan_rows_kernel(
 
 // ---- shrink: h = alpha f (keep x) W ------------------------------------------
 
-// W of adapter a as the contraction sees it: TRANS false, [R, C] (A in the
-// forward): a lane's 8 contraction indices are 16 contiguous bytes; TRANS
-// true, [C, R] (B in the backward): a lane reads RP / 16 adjacent ranks of
-// its 8 rows and turns them in registers, so result column l % 16 of block jb
-// is rank (l % 16) * (RP / 16) + jb.
-template <int RP, bool TRANS>
-__device__ __forceinline__ int shrink_rank(int jb, int col) {
-    return TRANS ? col * (RP / 16) + jb : jb * 16 + col;
+// Element 0 of row `row` (not negative) of a bf16 matrix: one 32 x 32 + 64 bit
+// multiply-add with the stride in bytes.
+__device__ __forceinline__ const uint16_t *row_at(const uint16_t *p, int row, uint32_t ld_bytes) {
+    return reinterpret_cast<const uint16_t *>(reinterpret_cast<uintptr_t>(p) +
+                                              (uint64_t)(uint32_t)row * ld_bytes);
 }
-
-template <int RP, bool TRANS>
-__device__ __forceinline__ void load_shrink_weights(const uint16_t *w, int64_t C, int R, int64_t k,
-                                                    int col, u32x4 (&out)[RP / 16]) {
-    constexpr int W = RP / 16;
-    // Ranks past R read rank 0: their result columns are not stored.
-    if constexpr (!TRANS) {
-#pragma unroll
-        for (int jb = 0; jb < W; ++jb) {
-            const int j = jb * 16 + col;
-            out[jb] = *reinterpret_cast<const u32x4 *>(w + (j < R ? j : 0) * C + k);
-        }
-    } else {
-        uint32_t t[8][(W + 1) / 2];
-        const int j = col * W < R ? col * W : 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint16_t *p = w + (k + i) * R + j;
-            if constexpr (W == 1) {
-                t[i][0] = *p;
-            } else if constexpr (W == 2) {
-                t[i][0] = *reinterpret_cast<const uint32_t *>(p);
-            } else if constexpr (W == 4) {
-                const u32x2 v = *reinterpret_cast<const u32x2 *>(p);
-                t[i][0] = v.x;
-                t[i][1] = v.y;
-            } else {
-                const u32x4 v = *reinterpret_cast<const u32x4 *>(p);
-#pragma unroll
-                for (int d = 0; d < 4; ++d) t[i][d] = v[d];
-            }
-        }
-#pragma unroll
-        for (int jb = 0; jb < W; ++jb)
-#pragma unroll
-            for (int d = 0; d < 4; ++d)
-                out[jb][d] = (jb & 1) ? high_halves(t[2 * d][jb >> 1], t[2 * d + 1][jb >> 1])
-                                      : low_halves(t[2 * d][jb >> 1], t[2 * d + 1][jb >> 1]);
-    }
+__device__ __forceinline__ uint16_t *row_at(uint16_t *p, int row, uint32_t ld_bytes) {
+    return const_cast<uint16_t *>(row_at(const_cast<const uint16_t *>(p), row, ld_bytes));
 }
-
-__device__ __forceinline__ u32x4 keep_chunk(u32x4 v, const DropoutKey &key, uint64_t e,
-                                            uint32_t threshold) {
-    uint32_t w[4];
-    dropout_words(key, e, w);
-#pragma unroll
-    for (int d = 0; d < 4; ++d) v[d] &= dropout_keep2(w[d], threshold);
-    return v;
-}
-
-// Grid: (tiles, K parts); part y sums columns [y * kpart, (y + 1) * kpart) and
-// writes sums[y][row][0 .. R).
-template <int RP, bool TRANS, bool DROP>
-__global__ __launch_bounds__(THREADS) void adapter_shrink_kernel(
-    PlanView plan, const uint16_t *__restrict__ src, int64_t ld, int64_t C,
-    const uint16_t *__restrict__ weights, const float *__restrict__ alpha, int R,
-    float *__restrict__ sums, int64_t part_stride, int64_t kpart, DropoutArgs drop) {
-    __shared__ float red[WAVES][16 * RP];
-    __shared__ int rows[TILE];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, g = lane >> 4;
-    // All of the plan's words for this tile in one round trip.
-    const bool built = plan.built();
-    const int tile = blockIdx.x, a = plan.tile_adapter[tile];
-    int my_row[2];
-#pragma unroll
-    for (int mb = 0; mb < 2; ++mb) my_row[mb] = plan.tile_row[(int64_t)tile * TILE + 16 * mb + col];
-    if (!built || a < 0) return;
-    if (tid < 16) {
-        rows[tid] = my_row[0];
-        rows[16 + tid] = my_row[1];
-    }
-    const uint16_t *w = weights + (int64_t)a * R * C;
-
-    int64_t kw = ((kpart + WAVES - 1) / WAVES + 31) / 32 * 32;   // a wave's columns
-    const int64_t k0 = blockIdx.y * kpart + wave * kw;
-    const int64_t k1 = min(min(k0 + kw, (int64_t)(blockIdx.y + 1) * kpart), C);
-
-    const uint16_t *px[2];
-    int64_t row[2];
-#pragma unroll
-    for (int mb = 0; mb < 2; ++mb) {
-        row[mb] = max(my_row[mb], 0);        // a position without a row reads row 0, unstored
-        px[mb] = src + row[mb] * ld;
-    }
-    f32x4 acc[2][RP / 16];
-#pragma unroll
-    for (int mb = 0; mb < 2; ++mb)
-#pragma unroll
-        for (int jb = 0; jb < RP / 16; ++jb) acc[mb][jb] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-    constexpr int U = RP >= 128 ? 2 : 4;
-    for (int64_t kk = k0; kk < k1; kk += 32 * U) {
-        // Past the end both operands read the part's first columns, and x
-        // counts as zero there.
-        u32x4 xs[U][2], ws[U][RP / 16];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t k = kk + 32 * u + 8 * g, kc = k < k1 ? k : k0;
-#pragma unroll
-            for (int mb = 0; mb < 2; ++mb) xs[u][mb] = *reinterpret_cast<const u32x4 *>(px[mb] + kc);
-            load_shrink_weights<RP, TRANS>(w, C, R, kc, col, ws[u]);
-        }
-        if (kk + 32 * U > k1) {
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int mb = 0; mb < 2; ++mb)
-#pragma unroll
-                    for (int d = 0; d < 4; ++d)
-                        xs[u][mb][d] = kk + 32 * u + 8 * g < k1 ? xs[u][mb][d] : 0u;
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if constexpr (DROP) {
-                const DropoutKey key(drop.rng);
-                const int64_t k = kk + 32 * u + 8 * g;
-#pragma unroll
-                for (int mb = 0; mb < 2; ++mb)
-                    xs[u][mb] = keep_chunk(xs[u][mb], key, (uint64_t)(row[mb] * (C >> 3) + (k >> 3)),
-                                           drop.threshold);
-            }
-#pragma unroll
-            for (int mb = 0; mb < 2; ++mb)
-#pragma unroll
-                for (int jb = 0; jb < RP / 16; ++jb)
-                    acc[mb][jb] = mfma(xs[u][mb], ws[u][jb], acc[mb][jb]);
-        }
-    }
-    const float scale = alpha[a] * drop.factor;
-#pragma unroll
-    for (int mb = 0; mb < 2; ++mb) {
-        if (mb) __syncthreads();
-#pragma unroll
-        for (int jb = 0; jb < RP / 16; ++jb)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                red[wave][(4 * g + i) * RP + shrink_rank<RP, TRANS>(jb, col)] = acc[mb][jb][i];
-        __syncthreads();
-        for (int e = tid; e < 16 * RP; e += THREADS) {
-            const int r = rows[16 * mb + e / RP], j = e % RP;
-            if (j < R && r >= 0)
-                sums[blockIdx.y * part_stride + (int64_t)r * R + j] =
-                    scale * (((red[0][e] + red[1][e]) + red[2][e]) + red[3][e]);
-        }
-    }
-}
-
-// ---- expand: out = base + f keep (h W) ---------------------------------------
 
 // L bf16 columns, as loaded and stored.
 template <int L>
@@ -383,13 +235,17 @@ struct Cols {
             const u32x4 v = *reinterpret_cast<const u32x4 *>(p);
 #pragma unroll
             for (int i = 0; i < 4; ++i) d[i] = v[i];
-        } else {
+        } else if constexpr (L == 4) {
             const u32x2 v = *reinterpret_cast<const u32x2 *>(p);
             d[0] = v.x;
             d[1] = v.y;
+        } else {
+            static_assert(L == 2, "2, 4 or 8 columns");
+            d[0] = *reinterpret_cast<const uint32_t *>(p);
         }
     }
     __device__ __forceinline__ void store(uint16_t *p) const {
+        static_assert(L >= 4, "4 or 8 columns");
         if constexpr (L == 8)
             *reinterpret_cast<u32x4 *>(p) = u32x4{d[0], d[1], d[2], d[3]};
         else
@@ -400,6 +256,216 @@ struct Cols {
         for (int i = 0; i < L / 2; ++i) d[i] = ok ? d[i] : 0u;
     }
 };
+
+__device__ __forceinline__ u32x4 keep_chunk(u32x4 v, const DropoutKey &key, uint64_t e,
+                                            uint32_t threshold) {
+    uint32_t w[4];
+    dropout_words(key, e, w);
+#pragma unroll
+    for (int d = 0; d < 4; ++d) v[d] &= dropout_keep2(w[d], threshold);
+    return v;
+}
+
+// The shrink's shape for a padded rank: its waves split the columns, each in
+// steps through LDS of its own.  From rank 64 on four waves, so that two
+// workgroups and more fit a CU: with one, a few more tiles than CUs take a
+// second round.
+constexpr int shrink_waves(int rp) { return rp >= 64 ? 4 : 8; }
+constexpr int shrink_threads(int rp) { return 64 * shrink_waves(rp); }
+constexpr int shrink_step(int rp) { return rp >= 128 ? 32 : 64; }
+// Tiles of a workgroup: rank 128's weights are four times a tile's x, so two
+// tiles of an adapter share them.
+constexpr int shrink_tiles(int rp) { return rp >= 128 ? 2 : 1; }
+// 16-byte pieces of LDS a wave stages: x (two row blocks a tile) and W (rp / 16).
+constexpr int shrink_wave_pieces(int rp) {
+    return shrink_step(rp) / 32 * (2 * shrink_tiles(rp) + rp / 16) * 64;
+}
+constexpr int shrink_lds_bytes(int rp) { return shrink_waves(rp) * shrink_wave_pieces(rp) * 16; }
+static_assert(shrink_wave_pieces(128) * 16 >= 16 * 128 * 4 &&
+                  shrink_wave_pieces(64) * 16 >= 16 * 64 * 4 &&
+                  shrink_wave_pieces(16) * 16 >= 16 * 16 * 4,
+              "the sums of 16 rows meet in the same LDS");
+
+// Grid: (groups of T tiles, K parts); part y sums columns [y * kpart, (y + 1) * kpart) and
+// writes sums[y][row][0 .. R).
+//
+// A lane of an MFMA operand holds one row's 8 columns, so sixteen neighbouring
+// lanes want sixteen rows: read from memory that way, a 16-byte load costs the
+// L1 an access per lane.  Here lanes read runs of 64 or 128 bytes of a row, and
+// a wave turns them into operands in LDS that only it uses (no barrier in the
+// loop); the next step's loads are in flight meanwhile.  Octet k of row r sits
+// at lane 16 (k % 4) + (r ^ 2 k ^ r / 16) % 16 of its block of 16 rows: writes of
+// a row's octets, or of every fourth row, and reads of a block's rows all spread
+// over the banks.
+//   TRANS false, W [R, C] (A in the forward): staged as x is.
+//   TRANS true, W [C, R] (B in the backward): a lane reads V ranks of 8 columns
+//   and turns them in registers.
+template <int RP, bool TRANS, bool DROP>
+__global__ __launch_bounds__(shrink_threads(RP), 2) void adapter_shrink_kernel(
+    PlanView plan, int tiles_max, const uint16_t *__restrict__ src, uint32_t ld, int64_t C,
+    const uint16_t *__restrict__ weights, const float *__restrict__ alpha, int R,
+    float *__restrict__ sums, int64_t part_stride, int64_t kpart, DropoutArgs drop) {
+    constexpr int STEP = shrink_step(RP), OCTS = STEP / 8, U = STEP / 32, J = RP / 16;
+    constexpr int NW = shrink_waves(RP), T = shrink_tiles(RP), MB = 2 * T;
+    constexpr int XI = T * TILE * OCTS / 64;             // 16-byte loads of x a lane and step
+    constexpr int V = RP >= 64 ? 4 : 2;                  // ranks of a TRANS load
+    constexpr int WI = TRANS ? RP / V * OCTS / 64 : RP * OCTS / 64;
+    extern __shared__ u32x4 lds[];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, g = lane >> 4;
+    u32x4 *lx = lds + wave * shrink_wave_pieces(RP), *lw = lx + U * MB * 64;
+    // All of the plan's words for these tiles in one round trip.
+    const bool built = plan.built();
+    const int tile0 = blockIdx.x * T;
+    const int32_t *tile_row = plan.tile_row + (int64_t)tile0 * TILE;
+    int adapter[T], x_row[XI];
+#pragma unroll
+    for (int t = 0; t < T; ++t)
+        adapter[t] = tile0 + t < tiles_max ? plan.tile_adapter[tile0 + t] : -2;
+#pragma unroll
+    for (int i = 0; i < XI; ++i) {
+        const int at = lane / OCTS + i * (64 / OCTS);
+        // (a tile that there is not: its row is never stored)
+        x_row[i] = tile_row[tile0 + at / TILE < tiles_max ? at : 0];
+    }
+    if (!built) return;
+
+    const int64_t kw = ((kpart + NW - 1) / NW + STEP - 1) / STEP * STEP;
+    const int64_t k0 = blockIdx.y * kpart + wave * kw;
+    const int64_t k1 = min(min(k0 + kw, (int64_t)(blockIdx.y + 1) * kpart), C);
+    const int oct = lane % OCTS;
+    const DropoutKey key(DROP ? drop.rng : nullptr, DROP);
+    const uint16_t *px[XI];
+#pragma unroll
+    for (int i = 0; i < XI; ++i) {
+        x_row[i] = (uint32_t)x_row[i] < (uint32_t)plan.rows ? x_row[i] : 0;   // unstored
+        px[i] = row_at(src, x_row[i], ld);
+    }
+
+    const uint16_t *w = weights;
+    u32x4 xr[XI];
+    u32x4 wr[TRANS ? 1 : WI];                // TRANS false: as loaded
+    Cols<V> tr[TRANS ? WI : 1][8];           // TRANS true: V ranks of 8 columns
+    // Past the end both operands read the part's first columns, and x counts as
+    // zero there; ranks past R read the first ranks, unstored.
+    auto load = [&](int64_t kk) {
+        const int64_t k = kk + 8 * oct, kc = k < k1 ? k : k0;
+#pragma unroll
+        for (int i = 0; i < XI; ++i) xr[i] = *reinterpret_cast<const u32x4 *>(px[i] + kc);
+        if constexpr (!TRANS) {
+#pragma unroll
+            for (int i = 0; i < WI; ++i) {
+                const int j = lane / OCTS + i * (64 / OCTS);
+                wr[i] = *reinterpret_cast<const u32x4 *>(w + (j < R ? j : 0) * C + kc);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < WI; ++i) {
+                const int item = lane + 64 * i, j = item % (RP / V) * V;
+                const int64_t n = kk + 8 * (item / (RP / V)), nc = n < k1 ? n : k0;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) tr[i][e].load(w + (nc + e) * R + (j < R ? j : 0));
+            }
+        }
+    };
+    auto slot = [](int o, int r) { return 16 * (o & 3) + ((r ^ (2 * o) ^ (r >> 4)) & 15); };
+    auto stage = [&](int64_t kk) {
+        const int64_t k = kk + 8 * oct;
+#pragma unroll
+        for (int i = 0; i < XI; ++i) {
+            const int r = lane / OCTS + i * (64 / OCTS);
+            u32x4 v = xr[i];
+            if constexpr (DROP)
+                v = keep_chunk(v, key, (uint64_t)(x_row[i] * (C >> 3) + (k >> 3)), drop.threshold);
+#pragma unroll
+            for (int d = 0; d < 4; ++d) v[d] = k < k1 ? v[d] : 0u;
+            lx[((oct >> 2) * MB + (r >> 4)) * 64 + slot(oct, r)] = v;
+        }
+        if constexpr (!TRANS) {
+#pragma unroll
+            for (int i = 0; i < WI; ++i) {
+                const int j = lane / OCTS + i * (64 / OCTS);
+                lw[((oct >> 2) * J + (j >> 4)) * 64 + slot(oct, j)] = wr[i];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < WI; ++i) {
+                const int item = lane + 64 * i, j0 = item % (RP / V) * V, o = item / (RP / V);
+#pragma unroll
+                for (int t = 0; t < V; ++t) {
+                    u32x4 v;
+#pragma unroll
+                    for (int d = 0; d < 4; ++d)
+                        v[d] = (t & 1) ? high_halves(tr[i][2 * d].d[t >> 1], tr[i][2 * d + 1].d[t >> 1])
+                                       : low_halves(tr[i][2 * d].d[t >> 1], tr[i][2 * d + 1].d[t >> 1]);
+                    lw[((o >> 2) * J + ((j0 + t) >> 4)) * 64 + slot(o, j0 + t)] = v;
+                }
+            }
+        }
+    };
+
+    // Tiles of different adapters (an adapter's last tile beside the next one's
+    // first) take a pass each.
+#pragma unroll
+    for (int pass = 0; pass < T; ++pass) {
+        const int a = adapter[pass];
+        if (a < 0 || (pass > 0 && a == adapter[0])) continue;
+        w = weights + (int64_t)a * R * C;
+        f32x4 acc[MB][J];
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+            for (int jb = 0; jb < J; ++jb) acc[mb][jb] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (pass > 0) __syncthreads();       // the pass before has read its sums
+        if (k0 < k1) load(k0);
+        for (int64_t kk = k0; kk < k1; kk += STEP) {
+            stage(kk);
+            if (kk + STEP < k1) load(kk + STEP);
+            // A wave's LDS operations complete in issue order, so its reads see
+            // every lane's writes and the next writes come after them; the
+            // fences keep the compiler from moving them across.
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+            __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                u32x4 xs[MB];
+#pragma unroll
+                for (int mb = 0; mb < MB; ++mb)
+                    xs[mb] = lx[(u * MB + mb) * 64 + slot(4 * u + g, 16 * mb + col)];
+#pragma unroll
+                for (int jb = 0; jb < J; ++jb) {
+                    const u32x4 b = lw[(u * J + jb) * 64 + slot(4 * u + g, 16 * jb + col)];
+#pragma unroll
+                    for (int mb = 0; mb < MB; ++mb) acc[mb][jb] = mfma(xs[mb], b, acc[mb][jb]);
+                }
+            }
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        }
+        // The waves' sums of 16 rows at a time, added in wave order.
+        float *red = reinterpret_cast<float *>(lds);
+        const float scale = alpha[a] * drop.factor;
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb) {
+            if (adapter[mb / 2] != a) continue;
+            __syncthreads();
+#pragma unroll
+            for (int jb = 0; jb < J; ++jb)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    red[wave * 16 * RP + (4 * g + i) * RP + jb * 16 + col] = acc[mb][jb][i];
+            __syncthreads();
+            for (int e = tid; e < 16 * RP; e += 64 * NW) {
+                const int r = tile_row[16 * mb + e / RP], j = e % RP;
+                float sum = red[e];
+#pragma unroll
+                for (int n = 1; n < NW; ++n) sum += red[n * 16 * RP + e];
+                if (j < R && r >= 0)
+                    sums[blockIdx.y * part_stride + (int64_t)r * R + j] = scale * sum;
+            }
+        }
+    }
+}
+
+// ---- expand: out = base + f keep (h W) ---------------------------------------
 
 // The dropout's numbers of L columns c .. (c a multiple of L).
 template <int L>
@@ -520,8 +586,8 @@ struct PackArgs {
 template <int RP, bool TRANS, bool DROP>
 __global__ __launch_bounds__(expand_threads(RP), 2) void adapter_expand_kernel(
     PlanView plan, int tiles_max, int chunk, const float *h, int parts, int64_t part_stride,
-    const uint16_t *__restrict__ weights, int R, int64_t C, const uint16_t *base, int32_t ldbase,
-    uint16_t *out, int32_t ldo, float *h_out, PackArgs pack, DropoutArgs drop) {
+    const uint16_t *__restrict__ weights, int R, int64_t C, const uint16_t *base, uint32_t ldbase,
+    uint16_t *out, uint32_t ldo, float *h_out, PackArgs pack, DropoutArgs drop) {
     // RP = 16: one contraction step, ranks 0 .. 15 of h's high part in its
     // first half and of the low part in its second.
     constexpr int S = RP == 16 ? 1 : RP / 32;
@@ -575,7 +641,8 @@ __global__ __launch_bounds__(expand_threads(RP), 2) void adapter_expand_kernel(
             d.rows[mb] = *reinterpret_cast<const int4 *>(p + 16 * mb + 4 * g);
         return d;
     };
-    Ids next = load_ids(tile0);
+    Ids next = load_ids(tile0), after{};
+    if (AHEAD && tile0 + 1 < tile1) after = load_ids(tile0 + 1);
     if (!plan.built()) return;
     const bool in_place = base == out && ldbase == ldo;
     const DropoutKey key(DROP ? drop.rng : nullptr, DROP);
@@ -620,7 +687,7 @@ __global__ __launch_bounds__(expand_threads(RP), 2) void adapter_expand_kernel(
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 if (read_base)
-                    ahead[mb][i].load(base + (int64_t)max(rows[i], 0) * ldbase + c);
+                    ahead[mb][i].load(row_at(base + c, max(rows[i], 0), ldbase));
                 else
                     ahead[mb][i].clear_unless(false);
             }
@@ -634,7 +701,9 @@ __global__ __launch_bounds__(expand_threads(RP), 2) void adapter_expand_kernel(
         const Ids now = next;
         const int a = now.a;
         if (a == -2) return;
-        if (AHEAD && tile + 1 < tile1) next = load_ids(tile + 1);
+        // The plan's words two tiles ahead, the data one.
+        next = after;
+        if (AHEAD && tile + 2 < tile1) after = load_ids(tile + 2);
         if (a >= 0 && a != a_held) {
             load_expand_weights<RP, TRANS, S, L>(weights + (int64_t)a * R * C, C, R, c, g, ws);
             a_held = a;
@@ -681,7 +750,7 @@ __global__ __launch_bounds__(expand_threads(RP), 2) void adapter_expand_kernel(
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         if (rows[mb][i] >= 0)
-                            bases[mb][i].store(out + (int64_t)rows[mb][i] * ldo + c);
+                            bases[mb][i].store(row_at(out + c, rows[mb][i], ldo));
             }
             if constexpr (!AHEAD) return;
             continue;
@@ -720,7 +789,7 @@ __global__ __launch_bounds__(expand_threads(RP), 2) void adapter_expand_kernel(
                     hi += __uint_as_float(bases[mb][i].d[d] & 0xFFFF0000u);
                     o.d[d] = pack_bf16(lo, hi);
                 }
-                o.store(out + (int64_t)row * ldo + c);
+                o.store(row_at(out + c, row, ldo));
             }
         }
         if constexpr (!AHEAD) return;        // its only tile
@@ -730,6 +799,19 @@ __global__ __launch_bounds__(expand_threads(RP), 2) void adapter_expand_kernel(
 
 // ---- few rows: shrink and expand in one launch ----------------------------------
 
+// A of an adapter [R, K] as the MFMA's columns, read straight from memory (few
+// rows): 8 contraction indices are 16 bytes.  Ranks past R read rank 0: their
+// result columns are not used.
+template <int RP>
+__device__ __forceinline__ void load_small_weights(const uint16_t *w, int64_t K, int R, int64_t k,
+                                                   int col, u32x4 (&out)[RP / 16]) {
+#pragma unroll
+    for (int jb = 0; jb < RP / 16; ++jb) {
+        const int j = jb * 16 + col;
+        out[jb] = *reinterpret_cast<const u32x4 *>(w + (j < R ? j : 0) * K + k);
+    }
+}
+
 // A decode step's batch is bound by the launches and by the chain of loads, not
 // by the bytes.  Here every column block of a tile computes the tile's whole h
 // by itself (the adapter's A comes from the L2) and goes on to its columns of
@@ -737,10 +819,10 @@ __global__ __launch_bounds__(expand_threads(RP), 2) void adapter_expand_kernel(
 // Grid: (blocks of 512 columns, tiles).  Lane layouts as in the two kernels.
 template <int RP, bool DROP>
 __global__ __launch_bounds__(THREADS, 2) void adapter_small_kernel(
-    PlanView plan, const uint16_t *__restrict__ x, int32_t ldx, int64_t K,
+    PlanView plan, const uint16_t *__restrict__ x, uint32_t ldx, int64_t K,
     const uint16_t *__restrict__ wa, const uint16_t *__restrict__ wb,
-    const float *__restrict__ alpha, int R, int64_t C, const uint16_t *base, int32_t ldbase,
-    uint16_t *out, int32_t ldo, float *h_out, DropoutArgs drop) {
+    const float *__restrict__ alpha, int R, int64_t C, const uint16_t *base, uint32_t ldbase,
+    uint16_t *out, uint32_t ldo, float *h_out, DropoutArgs drop) {
     constexpr int S = RP == 16 ? 1 : RP / 32, P = RP == 16 ? 1 : 2, L = 8, OCTS = RP / 8;
     __shared__ float red[WAVES][TILE * RP];
     __shared__ u32x4 hs[2][S][P][64];
@@ -770,7 +852,7 @@ __global__ __launch_bounds__(THREADS, 2) void adapter_small_kernel(
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if (read_base && (mb == 0 || two))
-                bases[mb][i].load(base + (int64_t)max(rows[mb][i], 0) * ldbase + c);
+                bases[mb][i].load(row_at(base + c, max(rows[mb][i], 0), ldbase));
             else
                 bases[mb][i].clear_unless(false);
         }
@@ -792,7 +874,7 @@ __global__ __launch_bounds__(THREADS, 2) void adapter_small_kernel(
         for (int mb = 0; mb < 2; ++mb)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (rows[mb][i] >= 0) bases[mb][i].store(out + (int64_t)rows[mb][i] * ldo + c);
+                if (rows[mb][i] >= 0) bases[mb][i].store(row_at(out + c, rows[mb][i], ldo));
         return;
     }
     u32x4 ws[L][S];
@@ -806,7 +888,7 @@ __global__ __launch_bounds__(THREADS, 2) void adapter_small_kernel(
 #pragma unroll
     for (int mb = 0; mb < 2; ++mb) {
         h_row[mb] = max(h_row[mb], 0);
-        px[mb] = x + (int64_t)h_row[mb] * ldx;
+        px[mb] = row_at(x, h_row[mb], ldx);
     }
     f32x4 acc[2][RP / 16];
 #pragma unroll
@@ -822,7 +904,7 @@ __global__ __launch_bounds__(THREADS, 2) void adapter_small_kernel(
 #pragma unroll
             for (int mb = 0; mb < 2; ++mb)
                 if (mb == 0 || two) xs[u][mb] = *reinterpret_cast<const u32x4 *>(px[mb] + kc);
-            load_shrink_weights<RP, false>(w, K, R, kc, col, as[u]);
+            load_small_weights<RP>(w, K, R, kc, col, as[u]);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -893,7 +975,7 @@ __global__ __launch_bounds__(THREADS, 2) void adapter_small_kernel(
                 o.d[d] = pack_bf16(sum[2 * d][i] + __uint_as_float(bases[mb][i].d[d] << 16),
                                    sum[2 * d + 1][i] +
                                        __uint_as_float(bases[mb][i].d[d] & 0xFFFF0000u));
-            o.store(out + (int64_t)rows[mb][i] * ldo + c);
+            o.store(row_at(out + c, rows[mb][i], ldo));
         }
     }
 }
@@ -904,7 +986,7 @@ __global__ __launch_bounds__(THREADS, 2) void adapter_small_kernel(
 // partial [slot][R][C] = sum over a chunk's rows of short[row, j] * src[row, c].
 struct WgradSide {
     const uint16_t *src;
-    int32_t ld;
+    uint32_t ld;                // bytes
     int64_t C;
     const u32x4 *packed;        // the short operand (pack_tile)
     float *partial;
@@ -946,19 +1028,27 @@ __global__ __launch_bounds__(wgrad_threads(RP), 2) void adapter_wgrad_kernel(
     const int tile_end = min(tile + chunk, live);
     const DropoutKey key(DROP ? drop.rng : nullptr, DROP);
 
-    int rows[8];
+    // A lane's rows are read two tiles ahead, the operands one.
+    struct Rows {
+        int4 lo, hi;
+        __device__ __forceinline__ int operator[](int i) const {
+            const int r[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+            return r[i];
+        }
+    };
+    auto rows_of = [&](int t) {
+        const int4 *p = reinterpret_cast<const int4 *>(plan.tile_row + (int64_t)t * TILE + 8 * g);
+        return Rows{p[0], p[1]};
+    };
+    Rows rows, rows_next, rows_after;
     Cols<L> in[8], in_next[8];
     u32x4 h_next[ITEMS];
-    auto load_tile = [&](int t) {
-        const int4 *p = reinterpret_cast<const int4 *>(plan.tile_row + (int64_t)t * TILE + 8 * g);
-        const int4 lo = p[0], hi = p[1];
+    auto load_tile = [&](int t, const Rows &r) {
 #pragma unroll
         for (int it = 0; it < ITEMS; ++it)
             h_next[it] = side.packed[(int64_t)t * PIECES + min(tid + it * NT, PIECES - 1)];
-        rows[0] = lo.x, rows[1] = lo.y, rows[2] = lo.z, rows[3] = lo.w;
-        rows[4] = hi.x, rows[5] = hi.y, rows[6] = hi.z, rows[7] = hi.w;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) in_next[i].load(src + (int64_t)max(rows[i], 0) * side.ld);
+        for (int i = 0; i < 8; ++i) in_next[i].load(row_at(src, max(r[i], 0), side.ld));
     };
     auto stage_short = [&](int buf) {
 #pragma unroll
@@ -974,12 +1064,17 @@ __global__ __launch_bounds__(wgrad_threads(RP), 2) void adapter_wgrad_kernel(
         for (int t = 0; t < L; ++t)
 #pragma unroll
             for (int jb = 0; jb < J; ++jb) acc[t][jb] = f32x4{0.f, 0.f, 0.f, 0.f};
-        load_tile(tile);
+        rows_next = rows_of(tile);
+        rows_after = rows_of(min(tile + 1, stop - 1));
+        load_tile(tile, rows_next);
         int buf = 0;
         __syncthreads();                     // the run before has read both buffers
         stage_short(0);
         __syncthreads();
         for (; tile < stop; ++tile, buf ^= 1) {
+            rows = rows_next;
+            rows_next = rows_after;
+            if (tile + 2 < stop) rows_after = rows_of(tile + 2);
             // A position without a row: its short operand is zero, and its
             // long one may not be an infinity.
 #pragma unroll
@@ -1000,7 +1095,7 @@ __global__ __launch_bounds__(wgrad_threads(RP), 2) void adapter_wgrad_kernel(
                 }
             }
             const bool more = tile + 1 < stop;
-            if (more) load_tile(tile + 1);
+            if (more) load_tile(tile + 1, rows_next);
             u32x4 xs[L];
 #pragma unroll
             for (int t = 0; t < L; ++t)
@@ -1009,14 +1104,22 @@ __global__ __launch_bounds__(wgrad_threads(RP), 2) void adapter_wgrad_kernel(
                     xs[t][d] = (t & 1)
                                    ? high_halves(in[2 * d].d[t >> 1], in[2 * d + 1].d[t >> 1])
                                    : low_halves(in[2 * d].d[t >> 1], in[2 * d + 1].d[t >> 1]);
+            // The next rank block's operands are read while this one's are used.
+            u32x4 b[2][PARTS];
 #pragma unroll
-            for (int p = 0; p < PARTS; ++p)
+            for (int p = 0; p < PARTS; ++p) b[0][p] = hs[buf][p * J * 64 + lane];
 #pragma unroll
-                for (int jb = 0; jb < J; ++jb) {
-                    const u32x4 b = hs[buf][(p * J + jb) * 64 + lane];
+            for (int jb = 0; jb < J; ++jb) {
+                if (jb + 1 < J)
 #pragma unroll
-                    for (int t = 0; t < L; ++t) acc[t][jb] = mfma(xs[t], b, acc[t][jb]);
-                }
+                    for (int p = 0; p < PARTS; ++p)
+                        b[(jb + 1) & 1][p] = hs[buf][(p * J + jb + 1) * 64 + lane];
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int p = 0; p < PARTS; ++p)
+#pragma unroll
+                    for (int t = 0; t < L; ++t) acc[t][jb] = mfma(xs[t], b[jb & 1][p], acc[t][jb]);
+            }
             if (more) stage_short(buf ^ 1);
             __syncthreads();
         }
@@ -1117,6 +1220,8 @@ __global__ __launch_bounds__(THREADS) void adapter_clear_kernel(u32x4 *__restric
 
 // ---- launches -----------------------------------------------------------------
 
+uint32_t row_bytes(int64_t ld) { return (uint32_t)(2 * ld); }
+
 template <typename F>
 hipError_t by_rank(int rank, F f) {
     if (rank <= 16) f(std::integral_constant<int, 16>{});
@@ -1130,32 +1235,37 @@ hipError_t by_rank(int rank, F f) {
 // weigh more against a tile's base and output (128 bytes a column), while
 // enough workgroups are left.
 int64_t expand_chunk(int64_t tiles, int64_t blocks, int64_t rank) {
-    return rank <= 32 ? 1 : std::max<int64_t>(1, std::min(rank / 16, tiles * blocks / 1024));
+    return rank <= 32 ? 1 : std::max<int64_t>(1, std::min(rank / 12, (tiles * blocks + 1023) / 1024));
 }
 
 constexpr int64_t SMALL_TILE_BYTES = 256 << 10, SMALL_ALL_BYTES = 64 << 20;
 
-int64_t part_columns(int64_t C, int parts) { return ((C + parts - 1) / parts + 31) / 32 * 32; }
+int64_t part_columns(int64_t C, int parts) { return ((C + parts - 1) / parts + 63) / 64 * 64; }
 
 template <bool TRANS>
 hipError_t launch_shrink(const AdapterArgs &w, const AdapterPlanShape &shape, const int32_t *plan,
                          const DropoutArgs &drop, const uint16_t *src, int64_t ld, int64_t C,
                          float *sums, int parts, hipStream_t stream) {
     const PlanView v = view_of(shape, plan);
-    const dim3 grid((unsigned)shape.tiles_max, (unsigned)parts);
-    return by_rank(w.rank, [&](auto rp) {
+    hipError_t enabled = hipSuccess;
+    const hipError_t e = by_rank(w.rank, [&](auto rp) {
+        constexpr int RP = decltype(rp)::value, bytes = shrink_lds_bytes(RP), T = shrink_tiles(RP);
+        const dim3 grid((unsigned)((shape.tiles_max + T - 1) / T), (unsigned)parts);
         auto go = [&](auto dropped) {
-            hipLaunchKernelGGL((adapter_shrink_kernel<decltype(rp)::value, TRANS,
-                                                      decltype(dropped)::value>),
-                               grid, dim3(THREADS), 0, stream, v, src, ld, C, TRANS ? w.b : w.a,
-                               w.alpha, w.rank, sums, shape.rows * w.rank, part_columns(C, parts),
-                               drop);
+            const auto kernel = adapter_shrink_kernel<RP, TRANS, decltype(dropped)::value>;
+            static std::atomic<uint64_t> done{0};
+            enabled = enable_dynamic_lds(reinterpret_cast<const void *>(kernel), bytes, done);
+            if (enabled) return;
+            hipLaunchKernelGGL(kernel, grid, dim3(shrink_threads(RP)), bytes, stream, v,
+                               (int)shape.tiles_max, src, row_bytes(ld), C, TRANS ? w.b : w.a, w.alpha, w.rank, sums,
+                               shape.rows * w.rank, part_columns(C, parts), drop);
         };
         if constexpr (!TRANS) {
             if (drop.rng) return go(std::true_type{});
         }
         go(std::false_type{});
     });
+    return enabled ? enabled : e;
 }
 
 template <bool TRANS>
@@ -1177,8 +1287,7 @@ hipError_t launch_expand(const AdapterArgs &w, const AdapterPlanShape &shape, co
                                                       decltype(dropped)::value>),
                                grid, dim3(expand_threads(decltype(rp)::value)), 0, stream, v, (int)shape.tiles_max, (int)chunk,
                                h, parts, shape.rows * w.rank, TRANS ? w.a : w.b, w.rank, C, base,
-                               (int32_t)ldbase,
-                               out, (int32_t)ldo, h_out, packing, drop);
+                               row_bytes(ldbase), out, row_bytes(ldo), h_out, packing, drop);
         };
         if constexpr (TRANS) {
             if (drop.rng) return go(std::true_type{});
@@ -1205,8 +1314,9 @@ hipError_t launch_small(const AdapterArgs &w, const AdapterPlanShape &shape, con
     const dim3 grid = grid_of((w.out + kAdapterCols - 1) / kAdapterCols, shape.tiles_max);
     auto go = [&](auto rp, auto dropped) {
         hipLaunchKernelGGL((adapter_small_kernel<decltype(rp)::value, decltype(dropped)::value>),
-                           grid, dim3(THREADS), 0, stream, v, x, (int32_t)ldx, w.in, w.a, w.b,
-                           w.alpha, w.rank, w.out, base, (int32_t)ldbase, y, (int32_t)ldy, h, drop);
+                           grid, dim3(THREADS), 0, stream, v, x, row_bytes(ldx), w.in, w.a, w.b,
+                           w.alpha, w.rank, w.out, base, row_bytes(ldbase), y, row_bytes(ldy), h,
+                           drop);
     };
     auto by_drop = [&](auto rp) {
         if (drop.rng) go(rp, std::true_type{});
@@ -1254,7 +1364,7 @@ hipError_t launch_adapter_fwd(const AdapterArgs &w, const AdapterPlanShape &shap
                               int64_t ldx, const uint16_t *base, int64_t ldbase, uint16_t *y,
                               int64_t ldy, float *h, void *ws, hipStream_t stream) {
     if (one_launch(w, shape)) return launch_small(w, shape, plan, drop, x, ldx, base, ldbase, y, ldy, h, stream);
-    const int parts = adapter_parts(shape.tiles_max, w.in);
+    const int parts = adapter_parts(shape.tiles_max, w.in, w.rank);
     float *sums = parts == 1 && h ? h : static_cast<float *>(ws);
     if (hipError_t e = launch_shrink<false>(w, shape, plan, drop, x, ldx, w.in, sums, parts, stream))
         return e;
@@ -1270,7 +1380,7 @@ hipError_t launch_adapter_backward(const AdapterArgs &w, const AdapterPlanShape 
                                    int64_t ldbase, uint16_t *dx, int64_t lddx, void *da, void *db,
                                    int out_dtype, void *ws, hipStream_t stream) {
     const AdapterWorkspace layout(shape, w.rank, w.in, w.out);
-    const int parts = adapter_parts(shape.tiles_max, w.out);
+    const int parts = adapter_parts(shape.tiles_max, w.out, w.rank);
     float *g = static_cast<float *>(ws);
     const DropoutArgs none = {nullptr, 0, 1.0f};
     if (hipError_t e = launch_shrink<true>(w, shape, plan, none, dy, lddy, w.out, g, parts, stream))
@@ -1294,8 +1404,8 @@ hipError_t launch_adapter_backward(const AdapterArgs &w, const AdapterPlanShape 
     const int64_t slots = adapter_slots(shape, chunk);
     float *part_a = reinterpret_cast<float *>(at + layout.packed);
     float *part_b = part_a + slots * w.rank * w.in;
-    const WgradSide left = {x, (int32_t)ldx, w.in, pack.g.packed, part_a, 1};
-    const WgradSide right = {dy, (int32_t)lddy, w.out, pack.h.packed, part_b, 0};
+    const WgradSide left = {x, row_bytes(ldx), w.in, pack.g.packed, part_a, 1};
+    const WgradSide right = {dy, row_bytes(lddy), w.out, pack.h.packed, part_b, 0};
     const int left_blocks = (int)((w.in + kAdapterCols - 1) / kAdapterCols);
     const int right_blocks = (int)((w.out + kAdapterCols - 1) / kAdapterCols);
     const dim3 grid = grid_of(left_blocks + right_blocks, chunks);

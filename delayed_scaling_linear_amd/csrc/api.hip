@@ -113,9 +113,10 @@ int check_adapter(const fp8_adapters_t *w, const void *plan, int64_t plan_bytes,
     return FP8_OK;
 }
 
-// A row stride of a [rows, cols] bf16 tensor (the kernels hold it in 32 bits).
+// A row stride of a [rows, cols] bf16 tensor (the kernels hold its bytes in 32
+// bits).
 bool bad_stride(int64_t ld, int64_t cols) {
-    return ld < cols || (ld % 8) != 0 || ld > INT32_MAX;
+    return ld < cols || (ld % 8) != 0 || ld >= ((int64_t)1 << 30);
 }
 
 AdapterArgs adapter_args(const fp8_adapters_t *w) {

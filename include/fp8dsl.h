@@ -723,7 +723,7 @@ int64_t fp8_adapter_workspace_bytes(int64_t rows, int32_t adapters, int32_t rank
  * workspace device, 16-byte aligned, at least fp8_adapter_workspace_bytes;
  *           its contents on entry do not matter and on return are
  *           unspecified; calls that overlap on one workspace race.
- * Strides are multiples of 8, at least the row's length and below 2^31;
+ * Strides are multiples of 8, at least the row's length and below 2^30;
  * tensors 16-byte aligned.  rows 0: no work.
  * Errors: FP8_ERR_NULL, FP8_ERR_SHAPE (sizes, strides, plan_bytes,
  * workspace_bytes), FP8_ERR_ALIGN, FP8_ERR_ARG (p), FP8_ERR_LAUNCH /
