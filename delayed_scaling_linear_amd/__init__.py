@@ -24,7 +24,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from dataclasses import dataclass
+from dataclasses import dataclass, field
 from typing import Optional
 
 import torch
@@ -215,7 +215,7 @@ def _need_shape(t: Optional[torch.Tensor], shape, what: str) -> None:
     """The C ABI trusts the sizes it is given: a tensor smaller than the call
     assumes would be read or written out of bounds on the device, so every
     extent is checked here before the call."""
-    if t is not None and tuple(t.shape) != tuple(shape):
+    if t is not None and t.shape != shape and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
@@ -544,7 +544,7 @@ def fp8_produce_modulate_backward(op: int, dy: torch.Tensor, x: torch.Tensor, a:
         dy.shape[1], _stream(stream)), "fp8_produce_modulate_backward")
 
 
-@dataclass
+@dataclass(frozen=True)
 class Dropout:
     """A dropout: probability p and rng, a device int64 tensor {seed, offset}
     (a row of a [sites, 2] tensor is fine).  The mask follows from them and an
@@ -552,11 +552,18 @@ class Dropout:
     device when they run."""
     p: float
     rng: torch.Tensor
+    _desc: Optional[_DropoutDesc] = field(default=None, init=False, repr=False, compare=False)
 
     def desc(self) -> _DropoutDesc:
-        if self.rng is None or self.rng.numel() != 2:
-            raise ValueError("Dropout.rng must hold two elements (seed, offset)")
-        return _DropoutDesc(_ptr(self.rng, torch.int64, "Dropout.rng"), self.p, 0)
+        """The C descriptor, built at the first call and again if the tensor's
+        memory has moved since."""
+        d = self._desc
+        if d is None or d.rng != self.rng.data_ptr():
+            if self.rng is None or self.rng.numel() != 2:
+                raise ValueError("Dropout.rng must hold two elements (seed, offset)")
+            d = _DropoutDesc(_ptr(self.rng, torch.int64, "Dropout.rng"), self.p, 0)
+            object.__setattr__(self, "_desc", d)
+        return d
 
 
 def _on_current_device(*tensors) -> None:
@@ -672,16 +679,23 @@ def fp8_dropout_cast_transpose_amax(x: torch.Tensor, drop: Dropout, scale: torch
         "fp8_dropout_cast_transpose_amax")
 
 
-@dataclass
+@dataclass(frozen=True)
 class Adapters:
     """Low-rank adapters of one linear: a [count, rank, in] and b [count, out,
     rank] (bf16) and each adapter's factor alpha [count] (fp32)."""
     a: torch.Tensor
     b: torch.Tensor
     alpha: torch.Tensor
+    _desc: Optional[_AdaptersDesc] = field(default=None, init=False, repr=False, compare=False)
 
     def desc(self) -> _AdaptersDesc:
+        """The C descriptor, built at the first call and again if a tensor's
+        memory has moved since."""
         a, b, alpha = self.a, self.b, self.alpha
+        d = self._desc
+        if d is not None and d.a == a.data_ptr() and d.b == b.data_ptr() \
+                and d.alpha == alpha.data_ptr():
+            return d
         if a.dim() != 3 or b.dim() != 3:
             raise ValueError("Adapters.a and Adapters.b must be 3-D")
         count, rank, n_in = a.shape
@@ -690,9 +704,11 @@ class Adapters:
             _need_shape(b, (count, n_out, rank), "Adapters.b")
         if alpha.shape != (count,):
             _need_shape(alpha, (count,), "Adapters.alpha")
-        return _AdaptersDesc(_ptr(a, torch.bfloat16, "Adapters.a"),
-                             _ptr(b, torch.bfloat16, "Adapters.b"),
-                             _ptr(alpha, torch.float32, "Adapters.alpha"), count, rank, n_in, n_out)
+        d = _AdaptersDesc(_ptr(a, torch.bfloat16, "Adapters.a"),
+                          _ptr(b, torch.bfloat16, "Adapters.b"),
+                          _ptr(alpha, torch.float32, "Adapters.alpha"), count, rank, n_in, n_out)
+        object.__setattr__(self, "_desc", d)
+        return d
 
 
 @dataclass
@@ -737,13 +753,12 @@ def fp8_adapter_plan(row_adapter: torch.Tensor, plan: AdapterPlan, stream=None) 
     plan.built = True
 
 
-def _adapter_call(w: Adapters, plan: AdapterPlan, rows: int, workspace, drop):
+def _adapter_call(w: Adapters, plan: AdapterPlan, workspace, drop):
     """The arguments that both adapter calls begin with, and the workspace's."""
     if not plan.built:
         raise ValueError("the plan has not been built (fp8_adapter_plan)")
-    if plan.rows != rows or plan.adapters != w.a.shape[0]:
-        raise ValueError(f"the plan is for {plan.rows} rows and {plan.adapters} adapters, the call "
-                         f"has {rows} and {w.a.shape[0]}")
+    if plan.adapters != w.a.shape[0]:
+        raise ValueError(f"the plan is for {plan.adapters} adapters, the call has {w.a.shape[0]}")
     if workspace is None:
         raise ValueError("workspace is required (fp8_adapter_workspace_bytes)")
     head = (ctypes.byref(w.desc()), *_ws(plan.buf),
@@ -765,7 +780,7 @@ def fp8_adapter_fwd(w: Adapters, plan: AdapterPlan, x: torch.Tensor,
     bm = _NONE if base is None else _matrix(base, rows, n_out, torch.bfloat16, "base")
     if h is not None:
         _need_shape(h, (rows, rank), "h")
-    head, ws = _adapter_call(w, plan, rows, workspace, drop)
+    head, ws = _adapter_call(w, plan, workspace, drop)
     _on_current_device(w.a, w.b, w.alpha, plan.buf, x, y, base, h, workspace,
                        None if drop is None else drop.rng)
     _need_apart(ym, bm, rows, n_out, n_out, 2, "y", same=True)
@@ -803,7 +818,7 @@ def fp8_adapter_backward(w: Adapters, plan: AdapterPlan, x: Optional[torch.Tenso
         if da.dtype != db.dtype or da.dtype not in (torch.float32, bf16):
             raise TypeError("da and db must both be fp32 or both bf16")
         dtype = DTYPE_FP32 if da.dtype == torch.float32 else DTYPE_BF16
-    head, ws = _adapter_call(w, plan, rows, workspace, drop)
+    head, ws = _adapter_call(w, plan, workspace, drop)
     _on_current_device(w.a, w.b, w.alpha, plan.buf, x, dy, h, dx, dx_base, da, db, workspace,
                        None if drop is None else drop.rng)
     if dx is not None:
@@ -857,9 +872,11 @@ def _ws(workspace: Optional[torch.Tensor]):
     """(pointer, bytes) of an optional uint8 device workspace."""
     if workspace is None:
         return None, 0
-    if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+    if workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 device tensor")
-    return _ptr(workspace, torch.uint8, "workspace"), workspace.numel()
+    if not workspace.is_cuda:
+        raise ValueError("workspace must be a device tensor")
+    return workspace.data_ptr(), workspace.numel()
 
 
 def fp8_linear_fwd(x: Float8Tensor, w: Float8Tensor, bias: Optional[torch.Tensor],

@@ -219,7 +219,7 @@ __global__ __launch_bounds__(THREADS) void adapter_plan_rows_kernel(
 // Element 0 of row `row` (not negative) of a bf16 matrix: one 32 x 32 + 64 bit
 // multiply-add with the stride in bytes.
 __device__ __forceinline__ const uint16_t *row_at(const uint16_t *p, int row, uint32_t ld_bytes) {
-    return reinterpret_cast<const uint16_t *>(reinterpret_cast<uintptr_t>(p) +
+    return reinterpret_cast<const uint16_t *>(reinterpret_cast<const char *>(p) +
                                               (uint64_t)(uint32_t)row * ld_bytes);
 }
 __device__ __forceinline__ uint16_t *row_at(uint16_t *p, int row, uint32_t ld_bytes) {
@@ -647,50 +647,30 @@ __global__ __launch_bounds__(expand_threads(RP), 2) void adapter_expand_kernel(
     const bool in_place = base == out && ldbase == ldo;
     const DropoutKey key(DROP ? drop.rng : nullptr, DROP);
 
-    // The tile ahead: its values of h (K parts still apart are added here) and
-    // its base.
-    float v[ITEMS][8];
+    // The tile ahead: its values of h (the first K part) and its base, as loaded:
+    // nothing is done to them before their tile's turn, so nothing waits.  (A
+    // position without a row reads row 0, an output without a base itself.)
+    f32x4 h_ahead[ITEMS][2];
     Cols<L> ahead[2][4];
+    const uint16_t *bases_at = base ? base : out;
+    const uint32_t ld_bases = base ? ldbase : ldo;
+    auto h_at = [&](int row, int it) {
+        const int j = 8 * ((tid + it * NT) % OCTS);
+        return h + (int64_t)max(row, 0) * R + (j < R ? j : 0);
+    };
     auto load_data = [&](const Ids &d) {
 #pragma unroll
         for (int it = 0; it < ITEMS; ++it) {
-            const int item = tid + it * NT, j = 8 * (item % OCTS);
-            const bool ok = d.a >= 0 && item < TILE * OCTS && d.h[it] >= 0 && j < R;
-            const float *p = h + (ok ? (int64_t)d.h[it] * R + j : 0);
-            const f32x4 lo = *reinterpret_cast<const f32x4 *>(p);
-            const f32x4 hi = *reinterpret_cast<const f32x4 *>(p + 4);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                v[it][i] = ok ? lo[i] : 0.0f;
-                v[it][4 + i] = ok ? hi[i] : 0.0f;
-            }
-            // Few rows: the other parts, three in flight at a time.
-            for (int s0 = 1; s0 < parts; s0 += 3) {
-                f32x4 q[3][2];
-#pragma unroll
-                for (int s = 0; s < 3; ++s) {
-                    const float *at = p + min(s0 + s, parts - 1) * part_stride;
-                    q[s][0] = *reinterpret_cast<const f32x4 *>(at);
-                    q[s][1] = *reinterpret_cast<const f32x4 *>(at + 4);
-                }
-#pragma unroll
-                for (int s = 0; s < 3; ++s)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        v[it][i] += ok && s0 + s < parts ? q[s][i >> 2][i & 3] : 0.0f;
-            }
+            const float *p = h_at(d.h[it], it);
+            h_ahead[it][0] = *reinterpret_cast<const f32x4 *>(p);
+            h_ahead[it][1] = *reinterpret_cast<const f32x4 *>(p + 4);
         }
-        const bool read_base = base != nullptr && !(in_place && d.a < 0);
 #pragma unroll
         for (int mb = 0; mb < 2; ++mb) {
             const int rows[4] = {d.rows[mb].x, d.rows[mb].y, d.rows[mb].z, d.rows[mb].w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (read_base)
-                    ahead[mb][i].load(row_at(base + c, max(rows[i], 0), ldbase));
-                else
-                    ahead[mb][i].clear_unless(false);
-            }
+            for (int i = 0; i < 4; ++i)
+                ahead[mb][i].load(row_at(bases_at + c, max(rows[i], 0), ld_bases));
         }
     };
 
@@ -711,14 +691,34 @@ __global__ __launch_bounds__(expand_threads(RP), 2) void adapter_expand_kernel(
 #pragma unroll
         for (int it = 0; it < ITEMS; ++it) {
             const int item = tid + it * NT, p = item / OCTS, o = item % OCTS;
+            const bool ok = a >= 0 && now.h[it] >= 0 && 8 * o < R;
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = ok ? h_ahead[it][i >> 2][i & 3] : 0.0f;
+            // Few rows: the other parts, three in flight at a time.
+            for (int s0 = 1; s0 < parts; s0 += 3) {
+                const float *first = h_at(now.h[it], it);
+                f32x4 q[3][2];
+#pragma unroll
+                for (int s = 0; s < 3; ++s) {
+                    const float *at = first + min(s0 + s, parts - 1) * part_stride;
+                    q[s][0] = *reinterpret_cast<const f32x4 *>(at);
+                    q[s][1] = *reinterpret_cast<const f32x4 *>(at + 4);
+                }
+#pragma unroll
+                for (int s = 0; s < 3; ++s)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        v[i] += ok && s0 + s < parts ? q[s][i >> 2][i & 3] : 0.0f;
+            }
             if (h_out != nullptr && (a < 0 || parts > 1) && blockIdx.x == 0 &&
                 item < TILE * OCTS && now.h[it] >= 0 && 8 * o < R) {
                 float *to = h_out + (int64_t)now.h[it] * R + 8 * o;
-                *reinterpret_cast<f32x4 *>(to) = f32x4{v[it][0], v[it][1], v[it][2], v[it][3]};
-                *reinterpret_cast<f32x4 *>(to + 4) = f32x4{v[it][4], v[it][5], v[it][6], v[it][7]};
+                *reinterpret_cast<f32x4 *>(to) = f32x4{v[0], v[1], v[2], v[3]};
+                *reinterpret_cast<f32x4 *>(to + 4) = f32x4{v[4], v[5], v[6], v[7]};
             }
             u32x4 part[2];
-            split8<2>(v[it], part);
+            split8<2>(v, part);
             if (a >= 0 && item < TILE * OCTS) {
                 if constexpr (RP == 16) {
                     hs[buf][p >> 4][0][0][16 * o + (p & 15)] = part[0];
@@ -734,6 +734,12 @@ __global__ __launch_bounds__(expand_threads(RP), 2) void adapter_expand_kernel(
         for (int mb = 0; mb < 2; ++mb)
 #pragma unroll
             for (int i = 0; i < 4; ++i) bases[mb][i] = ahead[mb][i];
+        if (base == nullptr) {
+#pragma unroll
+            for (int mb = 0; mb < 2; ++mb)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) bases[mb][i].clear_unless(false);
+        }
         // Before this tile's stores: a load that follows a store waits for it.
         if (AHEAD && tile + 1 < tile1 && next.a != -2) load_data(next);
         int rows[2][4];
@@ -763,14 +769,23 @@ __global__ __launch_bounds__(expand_threads(RP), 2) void adapter_expand_kernel(
             f32x4 acc[L];
 #pragma unroll
             for (int t = 0; t < L; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+            // The next step's operands are read while this one's are used.
+            u32x4 operand[2][P];
 #pragma unroll
-            for (int s = 0; s < S; ++s)
+            for (int p = 0; p < P; ++p) operand[0][p] = hs[buf][mb][0][p][lane];
 #pragma unroll
-                for (int p = 0; p < P; ++p) {
-                    const u32x4 operand = hs[buf][mb][s][p][lane];
+            for (int s = 0; s < S; ++s) {
+                if (s + 1 < S)
 #pragma unroll
-                    for (int t = 0; t < L; ++t) acc[t] = mfma(operand, ws[t][s], acc[t]);
-                }
+                    for (int p = 0; p < P; ++p)
+                        operand[(s + 1) & 1][p] = hs[buf][mb][s + 1][p][lane];
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int p = 0; p < P; ++p)
+#pragma unroll
+                    for (int t = 0; t < L; ++t)
+                        acc[t] = mfma(operand[s & 1][p], ws[t][s], acc[t]);
+            }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int row = rows[mb][i];

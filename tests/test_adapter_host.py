@@ -152,15 +152,17 @@ def test_binding_refusals():
     with pytest.raises(ValueError, match="row_adapter"):
         dsl.fp8_adapter_plan(torch.zeros(7, dtype=torch.int32), plan)
     with pytest.raises(ValueError, match="not been built"):
-        dsl._adapter_call(w, plan, 8, None, None)
+        dsl._adapter_call(w, plan, None, None)
     plan.built = True
-    with pytest.raises(ValueError, match="8 rows and 2 adapters"):
-        dsl._adapter_call(w, plan, 9, None, None)
-    with pytest.raises(ValueError, match="8 rows and 2 adapters"):
-        dsl._adapter_call(dsl.Adapters(bf(3, 16, 64), bf(3, 128, 16), torch.ones(3)), plan, 8, None,
+    with pytest.raises(ValueError, match="2 adapters, the call has 3"):
+        dsl._adapter_call(dsl.Adapters(bf(3, 16, 64), bf(3, 128, 16), torch.ones(3)), plan, None,
                           None)
     with pytest.raises(ValueError, match="workspace is required"):
-        dsl._adapter_call(w, plan, 8, None, None)
+        dsl._adapter_call(w, plan, None, None)
+    with pytest.raises(ValueError, match="x must have shape"):          # the plan's rows
+        dsl.fp8_adapter_fwd(w, plan, bf(9, 64), None, bf(9, 128))
+    with pytest.raises(Exception, match="cannot assign"):               # handles do not change
+        w.a = bf(2, 16, 64)
     with pytest.raises(ValueError, match="device tensor"):
         dsl.fp8_adapter_fwd(w, plan, bf(8, 64), None, bf(8, 128))
     with pytest.raises(ValueError, match="x must have shape"):
