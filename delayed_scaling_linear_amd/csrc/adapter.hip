@@ -345,8 +345,8 @@ __global__ __launch_bounds__(shrink_threads(RP), 2) void adapter_shrink_kernel(
     u32x4 xr[XI];
     u32x4 wr[TRANS ? 1 : WI];                // TRANS false: as loaded
     Cols<V> tr[TRANS ? WI : 1][8];           // TRANS true: V ranks of 8 columns
-    // Past the end both operands read the part's first columns, and x counts as
-    // zero there; ranks past R read the first ranks, unstored.
+    // Past the end both operands read the part's first columns and count as zero;
+    // ranks past R read the first ranks, unstored.
     auto load = [&](int64_t kk) {
         const int64_t k = kk + 8 * oct, kc = k < k1 ? k : k0;
 #pragma unroll
@@ -370,21 +370,27 @@ __global__ __launch_bounds__(shrink_threads(RP), 2) void adapter_shrink_kernel(
     auto slot = [](int o, int r) { return 16 * (o & 3) + ((r ^ (2 * o) ^ (r >> 4)) & 15); };
     auto stage = [&](int64_t kk) {
         const int64_t k = kk + 8 * oct;
+        const bool tail = kk + STEP > k1;
 #pragma unroll
         for (int i = 0; i < XI; ++i) {
             const int r = lane / OCTS + i * (64 / OCTS);
             u32x4 v = xr[i];
             if constexpr (DROP)
                 v = keep_chunk(v, key, (uint64_t)(x_row[i] * (C >> 3) + (k >> 3)), drop.threshold);
+            if (tail)
 #pragma unroll
-            for (int d = 0; d < 4; ++d) v[d] = k < k1 ? v[d] : 0u;
+                for (int d = 0; d < 4; ++d) v[d] = k < k1 ? v[d] : 0u;
             lx[((oct >> 2) * MB + (r >> 4)) * 64 + slot(oct, r)] = v;
         }
         if constexpr (!TRANS) {
 #pragma unroll
             for (int i = 0; i < WI; ++i) {
                 const int j = lane / OCTS + i * (64 / OCTS);
-                lw[((oct >> 2) * J + (j >> 4)) * 64 + slot(oct, j)] = wr[i];
+                u32x4 v = wr[i];
+                if (tail)
+#pragma unroll
+                    for (int d = 0; d < 4; ++d) v[d] = k < k1 ? v[d] : 0u;
+                lw[((oct >> 2) * J + (j >> 4)) * 64 + slot(oct, j)] = v;
             }
         } else {
 #pragma unroll
@@ -397,6 +403,9 @@ __global__ __launch_bounds__(shrink_threads(RP), 2) void adapter_shrink_kernel(
                     for (int d = 0; d < 4; ++d)
                         v[d] = (t & 1) ? high_halves(tr[i][2 * d].d[t >> 1], tr[i][2 * d + 1].d[t >> 1])
                                        : low_halves(tr[i][2 * d].d[t >> 1], tr[i][2 * d + 1].d[t >> 1]);
+                    if (tail)
+#pragma unroll
+                        for (int d = 0; d < 4; ++d) v[d] = kk + 8 * o < k1 ? v[d] : 0u;
                     lw[((o >> 2) * J + ((j0 + t) >> 4)) * 64 + slot(o, j0 + t)] = v;
                 }
             }
@@ -924,6 +933,12 @@ __global__ __launch_bounds__(THREADS, 2) void adapter_small_kernel(
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t k = kk + 32 * u + 8 * g;
+            if (kk + 32 * U > k1) {
+#pragma unroll
+                for (int jb = 0; jb < RP / 16; ++jb)
+#pragma unroll
+                    for (int d = 0; d < 4; ++d) as[u][jb][d] = k < k1 ? as[u][jb][d] : 0u;
+            }
 #pragma unroll
             for (int mb = 0; mb < 2; ++mb) {
                 if (mb == 1 && !two) continue;
@@ -1253,8 +1268,6 @@ int64_t expand_chunk(int64_t tiles, int64_t blocks, int64_t rank) {
     return rank <= 32 ? 1 : std::max<int64_t>(1, std::min(rank / 12, (tiles * blocks + 1023) / 1024));
 }
 
-constexpr int64_t SMALL_TILE_BYTES = 256 << 10, SMALL_ALL_BYTES = 64 << 20;
-
 int64_t part_columns(int64_t C, int parts) { return ((C + parts - 1) / parts + 63) / 64 * 64; }
 
 template <bool TRANS>
@@ -1311,14 +1324,19 @@ hipError_t launch_expand(const AdapterArgs &w, const AdapterPlanShape &shape, co
     });
 }
 
-// Whether the forward runs in one launch (adapter_small_kernel): its column
-// blocks read each tile's A and x again, which pays while a block's read and
-// all of them together stay small against the launch that is saved.
+// Whether the forward runs in one launch (adapter_small_kernel).  Its column
+// blocks read each tile's A again, 16 rows at a time.  Measured against the two
+// launches (in a graph, us): A of 32 or 64 KiB 5.2 against 7.0 (one token), 7.0
+// against 8.2 (64 tokens over 32 adapters, 8 MiB of A read in all), 10.7 against
+// 9.7 (33 MiB, where the launch saved, 3 us of the host's time, still makes an
+// ungraphed call faster); A of 128 KiB level up to 17 MiB, of 256 KiB a third
+// slower; 64 rows an adapter a third slower from 128 KiB on.
 bool one_launch(const AdapterArgs &w, const AdapterPlanShape &shape) {
     const int64_t blocks = (w.out + kAdapterCols - 1) / kAdapterCols;
     const int64_t a_bytes = adapter_padded_rank(w.rank) * w.in * 2;
-    return w.rank <= 64 && a_bytes <= SMALL_TILE_BYTES &&
-           shape.tiles_max * blocks * a_bytes <= SMALL_ALL_BYTES;
+    const int64_t most = a_bytes > (64 << 10) ? 17 << 20 : 34 << 20;
+    return w.rank <= 64 && shape.rows <= 16 * shape.adapters && a_bytes <= (128 << 10) &&
+           shape.tiles_max * blocks * a_bytes <= most;
 }
 
 hipError_t launch_small(const AdapterArgs &w, const AdapterPlanShape &shape, const int32_t *plan,
@@ -1378,7 +1396,8 @@ hipError_t launch_adapter_fwd(const AdapterArgs &w, const AdapterPlanShape &shap
                               const int32_t *plan, const DropoutArgs &drop, const uint16_t *x,
                               int64_t ldx, const uint16_t *base, int64_t ldbase, uint16_t *y,
                               int64_t ldy, float *h, void *ws, hipStream_t stream) {
-    if (one_launch(w, shape)) return launch_small(w, shape, plan, drop, x, ldx, base, ldbase, y, ldy, h, stream);
+    if (one_launch(w, shape))
+        return launch_small(w, shape, plan, drop, x, ldx, base, ldbase, y, ldy, h, stream);
     const int parts = adapter_parts(shape.tiles_max, w.in, w.rank);
     float *sums = parts == 1 && h ? h : static_cast<float *>(ws);
     if (hipError_t e = launch_shrink<false>(w, shape, plan, drop, x, ldx, w.in, sums, parts, stream))

@@ -83,7 +83,7 @@ int dropout_args(const fp8_dropout_t *drop, DropoutArgs *out) {
 // Sizes of an adapter call.
 int check_adapter_sizes(int64_t rows, int32_t adapters, int32_t rank, int64_t in, int64_t out) {
     constexpr int64_t kMost = (int64_t)1 << 22;
-    if (rows < 0 || rows > ((int64_t)1 << 28) || adapters < 1 || adapters > kAdapterMaxCount)
+    if (rows < 0 || rows > ((int64_t)1 << 26) || adapters < 1 || adapters > kAdapterMaxCount)
         return FP8_ERR_SHAPE;
     if (rank < 8 || rank > kAdapterMaxRank || (rank % 8) != 0) return FP8_ERR_SHAPE;
     if (in < 8 || in > kMost || (in % 8) != 0 || out < 8 || out > kMost || (out % 8) != 0)

@@ -693,7 +693,7 @@ typedef struct fp8_adapters {
  * plan         device, 16-byte aligned, fp8_adapter_plan_bytes(rows,
  *              adapters) bytes, owned by the caller; read by the calls below
  *              until it is built again.
- * 0 <= rows <= 2^28, 1 <= adapters <= FP8DSL_ADAPTERS_MAX.  rows 0: no work.
+ * 0 <= rows <= 2^26, 1 <= adapters <= FP8DSL_ADAPTERS_MAX.  rows 0: no work.
  * fp8_adapter_plan_bytes returns a negative status for sizes out of range.
  * Errors: FP8_ERR_SHAPE (sizes, plan_bytes), FP8_ERR_NULL, FP8_ERR_ALIGN,
  * FP8_ERR_LAUNCH / FP8_ERR_DEVICE.

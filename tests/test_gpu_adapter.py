@@ -374,3 +374,80 @@ def test_binding_refuses_what_the_kernels_cannot_see():
         dsl.fp8_adapter_fwd(c.w, c.plan, x, wide[:, 8:136], wide[:, :128], workspace=c.ws)
     with pytest.raises(ValueError, match="not been built"):
         dsl.fp8_adapter_fwd(c.w, dsl.AdapterPlan.empty(16, 4), x, None, y, workspace=c.ws)
+
+
+@pytest.mark.parametrize("rank, k", [(16, 72), (24, 136), (40, 200), (128, 40), (16, 1048), (64, 2056)])
+@pytest.mark.parametrize("rows", [3, 40])
+def test_infinite_weights_stay_in_their_rank(rank, k, rows):
+    """An infinite weight meets its own column of x only: h is infinite in its
+    rank (x is positive) and finite elsewhere, whatever the padding of the
+    contraction does; the same for g, whose padded rows are B's."""
+    c = Case(rows, k, k, rank, 1, [0] * rows)
+    c.x.fill_(1.0)
+    c.dy.fill_(1.0)
+    c.alpha.fill_(1.0)
+    c.h.zero_()
+    for at in (0, k - 8, k - 1):
+        a, b = torch.ones_like(c.a), torch.ones_like(c.b)
+        a[0, 3, at] = b[0, at, 3] = float("inf")
+        c.w = dsl.Adapters(a.to(DEV), b.to(DEV), c.dev(c.alpha))
+        _, h = c.forward()
+        want = torch.full((rows, rank), float(k), device=DEV)
+        want[:, 3] = float("inf")
+        assert torch.equal(h, want)
+        _, da, _ = c.backward()                       # dA = g^T x, g = the same sums
+        want = torch.full_like(da, float(k * rows))
+        want[:, 3] = float("inf")
+        assert torch.equal(da, want)
+
+
+def test_byte_offsets_past_32_bits():
+    """Rows 2 MiB apart: the last ones lie 4.4 GB behind the first."""
+    rows, ld = 2100, 1 << 20
+    c = Case(rows, 72, 88, 16, 3, _ids(rows, 3))
+    big = torch.empty(rows * ld, dtype=torch.bfloat16, device=DEV)
+    view = lambda at, n: torch.as_strided(big, (rows, n), (ld, 1), at)
+    x, base, y, dy, dx = view(0, 72), view(96, 88), view(192, 88), view(288, 88), view(384, 72)
+    x.copy_(c.x)
+    base.copy_(c.base)
+    dy.copy_(c.dy)
+    dx.copy_(c.dx_base)
+    dsl.fp8_adapter_fwd(c.w, c.plan, x, base, y, workspace=c.ws)
+    _same_bf16(y, c.want_forward()[0])
+    da, db = torch.empty(c.a.shape, device=DEV), torch.empty(c.b.shape, device=DEV)
+    dsl.fp8_adapter_backward(c.w, c.plan, x, dy, c.dev(c.h), dx_base=dx, dx=dx, da=da, db=db,
+                             workspace=c.ws)
+    wdx, wda, wdb, _ = c.want_backward()
+    _same_bf16(dx, wdx)
+    np.testing.assert_array_equal(f32(da), wda)
+    np.testing.assert_array_equal(f32(db), wdb)
+
+
+@pytest.mark.parametrize("rows, count, k, n", [(16, 1, 4096, 1032), (17, 1, 4096, 1032),
+                                               (64, 32, 2048, 8192), (64, 32, 2056, 8200),
+                                               (8, 8, 4096, 512), (8, 8, 4104, 512)])
+def test_both_sides_of_the_one_launch_rule(rows, count, k, n):
+    """Batches just inside and just outside of the rule that puts the forward
+    into one launch, with and without h."""
+    c = Case(rows, k, n, 16, count, _ids(rows, count, none=0.1))
+    y, h = c.forward()
+    wy, wh = c.want_forward()
+    np.testing.assert_array_equal(f32(h), wh)
+    _same_bf16(y, wy)
+    assert torch.equal(c.forward(keep_h=False)[0], y)
+
+
+def test_a_plan_that_was_never_built_writes_nothing():
+    """Through the C ABI a buffer without a plan of these sizes: no work."""
+    import ctypes
+    c = Case(40, 72, 88, 16, 3, _ids(40, 3))
+    x, base = c.dev(c.x), c.dev(c.base)
+    y = torch.full((40, 88), -7.0, dtype=torch.bfloat16, device=DEV)
+    for buf in (torch.full_like(c.plan.buf, 0xA5), torch.zeros_like(c.plan.buf)):
+        rc = dsl.lib().fp8_adapter_fwd(ctypes.byref(c.w.desc()), buf.data_ptr(), buf.numel(), None,
+                                       x.data_ptr(), 72, base.data_ptr(), 88, y.data_ptr(), 88, 40,
+                                       None, c.ws.data_ptr(), c.ws.numel(),
+                                       torch.cuda.current_stream().cuda_stream)
+        assert rc == 0
+        torch.cuda.synchronize()
+        assert (y == -7.0).all()
