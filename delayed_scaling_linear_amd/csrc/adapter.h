@@ -48,14 +48,21 @@ inline int64_t adapter_padded_rank(int64_t rank) {
     return rank <= 16 ? 16 : rank <= 32 ? 32 : rank <= 64 ? 64 : 128;
 }
 
-// K parts of the contraction over C columns (workgroups per tile, or per two
-// tiles of rank 128, of the shrink kernel): a workgroup per CU, each at least 256
-// columns, at most 16.  (More of them than CUs measured no faster at 257 and 265
-// tiles, and every part is one more read of the sums for the kernels behind.)
+// K parts of the contraction over C columns: workgroups per tile (per two tiles
+// of rank 128) of the shrink kernel.
+//   Fewer tiles than CUs: a workgroup per CU, each at least 256 columns, at most
+//   16.
+//   Else as many as are resident at once, if each keeps 2048 columns: over 8192
+//   columns of dy, 257 tiles, 3 parts take 55 us against 68 at rank 64 and 2
+//   take 41 against 49 at rank 32; rank 16 is bound by dy itself (35 us either
+//   way).  Over 2048 columns parts measured no faster, and each is one more
+//   read of the sums for the kernels behind (expand at rank 64: 61 us with one
+//   part, 67 with three).
 inline int adapter_parts(int64_t tiles, int64_t C, int64_t rank) {
-    const int64_t groups = rank > 64 ? (tiles + 1) / 2 : tiles;
-    const int64_t want = 256 / std::max<int64_t>(groups, 1);
-    return (int)std::max<int64_t>(1, std::min<int64_t>({want, C / 256, 16}));
+    const int64_t groups = std::max<int64_t>(1, rank > 64 ? (tiles + 1) / 2 : tiles);
+    const int64_t resident = rank <= 16 ? 256 : rank <= 32 || rank > 64 ? 520 : 800;
+    const int64_t fill = std::min<int64_t>({256 / groups, C / 256, 16});
+    return (int)std::max<int64_t>({1, fill, std::min(resident / groups, C / 2048)});
 }
 
 // Tiles of one weight-gradient workgroup: a partial sum of R fp32 per column
