@@ -170,7 +170,8 @@ def lib() -> ctypes.CDLL:
         L.fp8_adapter_backward.argtypes = [ap, vp, i64, pp, vp, i64, vp, i64, vp, vp, i64, vp, i64,
                                            i64, vp, vp, i32, vp, i64, vp]
         for f in (L.fp8_adapter_plan, L.fp8_adapter_fwd, L.fp8_adapter_backward, L.fp8_dropout,
-                  L.fp8_dropout_cast_transpose_amax, L.fp8_scale_update, L.fp8_cast_transpose_amax, L.fp8_cast_transpose_amax_dbias,
+                  L.fp8_dropout_cast_transpose_amax, L.fp8_scale_update, L.fp8_cast_transpose_amax,
+                  L.fp8_cast_transpose_amax_dbias,
                   L.fp8_cast_transpose_amax_dbias_noalloc, L.fp8_cast_transpose_amax_cached,
                   L.fp8_reference_copy,
                   L.fp8_produce_cast_transpose_amax, L.fp8_cast_transpose_dynamic,
@@ -603,7 +604,9 @@ def _need_apart(y, t, rows: int, y_cols: int, t_cols: int, size: int, what: str,
         return
     if same and yp == tp and yld == tld:
         return
-    if yp >= tp + ((rows - 1) * tld + t_cols) * size or tp >= yp + ((rows - 1) * yld + y_cols) * size:
+    if yp >= tp + ((rows - 1) * tld + t_cols) * size:
+        return
+    if tp >= yp + ((rows - 1) * yld + y_cols) * size:
         return
     gap = (tp - yp) // size % yld
     if yld != tld or gap < y_cols or gap + t_cols > yld:

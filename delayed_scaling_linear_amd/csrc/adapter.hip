@@ -20,10 +20,16 @@
 //            bits on every run).
 //
 // h and g are held in fp32.  Where they feed a matrix core they are split
-// into bf16 parts that add up to them: two (the error is 2^-17 of h) where
+// into bf16 parts that add up to them: two (the error is 2^-16 of h) where
 // the result is rounded to bf16, three (2^-24) where it is stored in fp32.
 // Dropout multiplies by the mask on the operand (exact) and by f in fp32 on
 // the sums.
+//
+// Measured on MI355X, where a large copy moves 5.1 TB/s (us of a whole call,
+// and in brackets its bytes at that rate): 8192 rows of 2048 -> 6144, rank 64,
+// nine requests 65 (47); 2048 -> 8192, rank 16 with dropout, forward 64 (59),
+// backward 92 (46, reading dy once; it is read twice); 16384 rows of 8192 ->
+// 2048, rank 128, backward 350 (178).
 #include "adapter.h"
 
 #include "fp8dsl_internal.h"
@@ -244,6 +250,19 @@ struct Cols {
             d[0] = *reinterpret_cast<const uint32_t *>(p);
         }
     }
+    // What is read once: past the last-level cache.
+    __device__ __forceinline__ void load_once(const uint16_t *p) {
+        static_assert(L >= 4, "4 or 8 columns");
+        if constexpr (L == 8) {
+            const u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) d[i] = v[i];
+        } else {
+            const u32x2 v = __builtin_nontemporal_load(reinterpret_cast<const u32x2 *>(p));
+            d[0] = v.x;
+            d[1] = v.y;
+        }
+    }
     __device__ __forceinline__ void store(uint16_t *p) const {
         static_assert(L >= 4, "4 or 8 columns");
         if constexpr (L == 8)
@@ -286,8 +305,8 @@ static_assert(shrink_wave_pieces(128) * 16 >= 16 * 128 * 4 &&
                   shrink_wave_pieces(16) * 16 >= 16 * 16 * 4,
               "the sums of 16 rows meet in the same LDS");
 
-// Grid: (groups of T tiles, K parts); part y sums columns [y * kpart, (y + 1) * kpart) and
-// writes sums[y][row][0 .. R).
+// Grid: (groups of T tiles, K parts); part y sums columns [y * kpart,
+// (y + 1) * kpart) and writes sums[y][row][0 .. R).
 //
 // A lane of an MFMA operand holds one row's 8 columns, so sixteen neighbouring
 // lanes want sixteen rows: read from memory that way, a 16-byte load costs the
@@ -300,6 +319,10 @@ static_assert(shrink_wave_pieces(128) * 16 >= 16 * 128 * 4 &&
 //   TRANS false, W [R, C] (A in the forward): staged as x is.
 //   TRANS true, W [C, R] (B in the backward): a lane reads V ranks of 8 columns
 //   and turns them in registers.
+// Bound by reading x at low rank: dy [8192, 8192] at rank 16 30 to 35 us (134 MB,
+// 3.8 to 4.5 TB/s; a library maximum over as much reads 3.0).  From rank 32 on the
+// weights, read again by each tile, and the latency of a wave's steps count: 41
+// us at rank 32, 55 at 64; x [8192, 2048] at rank 64 17 us.
 template <int RP, bool TRANS, bool DROP>
 __global__ __launch_bounds__(shrink_threads(RP), 2) void adapter_shrink_kernel(
     PlanView plan, int tiles_max, const uint16_t *__restrict__ src, uint32_t ld, int64_t C,
@@ -400,9 +423,10 @@ __global__ __launch_bounds__(shrink_threads(RP), 2) void adapter_shrink_kernel(
                 for (int t = 0; t < V; ++t) {
                     u32x4 v;
 #pragma unroll
-                    for (int d = 0; d < 4; ++d)
-                        v[d] = (t & 1) ? high_halves(tr[i][2 * d].d[t >> 1], tr[i][2 * d + 1].d[t >> 1])
-                                       : low_halves(tr[i][2 * d].d[t >> 1], tr[i][2 * d + 1].d[t >> 1]);
+                    for (int d = 0; d < 4; ++d) {
+                        const uint32_t a = tr[i][2 * d].d[t >> 1], b = tr[i][2 * d + 1].d[t >> 1];
+                        v[d] = (t & 1) ? high_halves(a, b) : low_halves(a, b);
+                    }
                     if (tail)
 #pragma unroll
                         for (int d = 0; d < 4; ++d) v[d] = kk + 8 * o < k1 ? v[d] : 0u;
@@ -487,8 +511,8 @@ __device__ __forceinline__ void numbers_of(const DropoutKey &key, int64_t row, i
 }
 
 // Columns of an expand lane and threads of a workgroup of 512 columns.  Rank 128
-// takes half the columns a lane, so that its weights leave registers for three
-// waves on a SIMD.
+// takes half the columns a lane, so that its weights and the tile ahead fit two
+// waves' registers on a SIMD.
 constexpr int expand_lane_cols(int rp) { return rp >= 128 ? 4 : 8; }
 constexpr int expand_threads(int rp) { return kAdapterCols / expand_lane_cols(rp) * 4; }
 
@@ -553,8 +577,8 @@ struct PackSide {
 };
 
 template <int PARTS>
-__device__ __forceinline__ void pack_tile(const PackSide &side, const int32_t *tile_row, int64_t tile,
-                                          int R, int64_t part_stride, int blocks) {
+__device__ __forceinline__ void pack_tile(const PackSide &side, const int32_t *tile_row,
+                                          int64_t tile, int R, int64_t part_stride, int blocks) {
     for (int item = threadIdx.x; item < blocks * 64; item += blockDim.x) {
         const int jb = item >> 6, l = item & 63, j = 16 * jb + (l & 15);
         const int4 *q = reinterpret_cast<const int4 *>(tile_row + tile * TILE + 8 * (l >> 4));
@@ -584,14 +608,19 @@ struct PackArgs {
 };
 
 // Grid: (blocks of 512 columns, chunks of tiles); in the backward rows of
-// workgroups before them pack both short operands of the weight gradients.  h is the MFMA's row operand
-// and a lane's 8 adjacent columns are 8 column blocks, so a lane holds 8
-// adjacent columns of rows 4 g .. 4 g + 3 of the result and the sixteen lanes of
-// a row load the base and store the output in one run of 256 bytes.  The
-// workgroup sums h's parts, splits h and lays it out in LDS as MFMA operands
-// once for its four waves (each wave reading it from memory by itself made the
-// L1 the bound: 2.3 GB through it for 200 MB of base and output).  A wave keeps
-// the weights of its columns while its tiles' adapter stays the same.
+// workgroups before them pack both short operands of the weight gradients.
+// h is the MFMA's row operand and a lane's L adjacent columns are L column
+// blocks, so a lane holds L adjacent columns of rows 4 g .. 4 g + 3 of the result
+// and the sixteen lanes of a row load the base and store the output in one run of
+// 256 (rank 128: 128) bytes.  The workgroup sums h's parts, splits h and lays it
+// out in LDS as MFMA operands once for its waves (each wave reading it from
+// memory by itself made the L1 the bound: 2.3 GB through it for 200 MB of base
+// and output).  A wave keeps the weights of its columns while its tiles' adapter
+// stays the same.
+// Bound by base and output: [8192, 8192] at rank 16 49 us (268 MB, 5.5 TB/s),
+// [8192, 6144] at rank 64 48 (201 MB, 4.2 TB/s).  [16384, 8192] at rank 128 135
+// (537 MB, 4.0 TB/s): there the two bf16 parts' 69 GFLOP take a fifth of the
+// cycles and the vector work of a tile (h's split, addresses, sums) a third.
 template <int RP, bool TRANS, bool DROP>
 __global__ __launch_bounds__(expand_threads(RP), 2) void adapter_expand_kernel(
     PlanView plan, int tiles_max, int chunk, const float *h, int parts, int64_t part_stride,
@@ -613,7 +642,7 @@ __global__ __launch_bounds__(expand_threads(RP), 2) void adapter_expand_kernel(
     const int64_t c = c_ok ? c_lane : 0;     // lanes past the end compute column 0, unstored
     int64_t part = chunk_of_block();
     if constexpr (TRANS) {
-        // The first pack_rows rows of the grid pack a tile each (they start
+        // The first pack.rows rows of the grid pack a tile each (they start
         // first: a late one would be the kernel's tail).
         if (part < pack.rows) {
             const int64_t tile = part * gridDim.x + blockIdx.x;
@@ -679,7 +708,7 @@ __global__ __launch_bounds__(expand_threads(RP), 2) void adapter_expand_kernel(
             const int rows[4] = {d.rows[mb].x, d.rows[mb].y, d.rows[mb].z, d.rows[mb].w};
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                ahead[mb][i].load(row_at(bases_at + c, max(rows[i], 0), ld_bases));
+                ahead[mb][i].load_once(row_at(bases_at + c, max(rows[i], 0), ld_bases));
         }
     };
 
@@ -1034,6 +1063,9 @@ constexpr int wgrad_threads(int rp) { return kAdapterCols / wgrad_lane_cols(rp) 
 // wave's 16 L); the short operand comes through LDS, once for the workgroup.
 // The next tile's loads of both are in flight while the current one is
 // multiplied.
+// Bound by x and dy at low rank: [8192, 2048 + 8192] at rank 16 39 us (168 MB,
+// 4.3 TB/s).  At rank 128, [16384, 2048 + 8192], 146 us: three bf16 parts make 129
+// GFLOP of 43, 0.88 PFLOP/s where a large library product reaches 1.24.
 template <int RP, int PARTS, bool DROP>
 __global__ __launch_bounds__(wgrad_threads(RP), 2) void adapter_wgrad_kernel(
     PlanView plan, WgradSide left, WgradSide right, int left_blocks, int R, int chunk,
@@ -1078,7 +1110,7 @@ __global__ __launch_bounds__(wgrad_threads(RP), 2) void adapter_wgrad_kernel(
         for (int it = 0; it < ITEMS; ++it)
             h_next[it] = side.packed[(int64_t)t * PIECES + min(tid + it * NT, PIECES - 1)];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) in_next[i].load(row_at(src, max(r[i], 0), side.ld));
+        for (int i = 0; i < 8; ++i) in_next[i].load_once(row_at(src, max(r[i], 0), side.ld));
     };
     auto stage_short = [&](int buf) {
 #pragma unroll
@@ -1265,7 +1297,8 @@ hipError_t by_rank(int rank, F f) {
 // weigh more against a tile's base and output (128 bytes a column), while
 // enough workgroups are left.
 int64_t expand_chunk(int64_t tiles, int64_t blocks, int64_t rank) {
-    return rank <= 32 ? 1 : std::max<int64_t>(1, std::min(rank / 12, (tiles * blocks + 1023) / 1024));
+    if (rank <= 32) return 1;
+    return std::max<int64_t>(1, std::min(rank / 12, (tiles * blocks + 1023) / 1024));
 }
 
 int64_t part_columns(int64_t C, int parts) { return ((C + parts - 1) / parts + 63) / 64 * 64; }
@@ -1285,8 +1318,8 @@ hipError_t launch_shrink(const AdapterArgs &w, const AdapterPlanShape &shape, co
             enabled = enable_dynamic_lds(reinterpret_cast<const void *>(kernel), bytes, done);
             if (enabled) return;
             hipLaunchKernelGGL(kernel, grid, dim3(shrink_threads(RP)), bytes, stream, v,
-                               (int)shape.tiles_max, src, row_bytes(ld), C, TRANS ? w.b : w.a, w.alpha, w.rank, sums,
-                               shape.rows * w.rank, part_columns(C, parts), drop);
+                               (int)shape.tiles_max, src, row_bytes(ld), C, TRANS ? w.b : w.a, w.alpha,
+                               w.rank, sums, shape.rows * w.rank, part_columns(C, parts), drop);
         };
         if constexpr (!TRANS) {
             if (drop.rng) return go(std::true_type{});
@@ -1313,8 +1346,8 @@ hipError_t launch_expand(const AdapterArgs &w, const AdapterPlanShape &shape, co
         auto go = [&](auto dropped) {
             hipLaunchKernelGGL((adapter_expand_kernel<decltype(rp)::value, TRANS,
                                                       decltype(dropped)::value>),
-                               grid, dim3(expand_threads(decltype(rp)::value)), 0, stream, v, (int)shape.tiles_max, (int)chunk,
-                               h, parts, shape.rows * w.rank, TRANS ? w.a : w.b, w.rank, C, base,
+                               grid, dim3(expand_threads(decltype(rp)::value)), 0, stream, v,
+                               (int)shape.tiles_max, (int)chunk, h, parts, shape.rows * w.rank, TRANS ? w.a : w.b, w.rank, C, base,
                                row_bytes(ldbase), out, row_bytes(ldo), h_out, packing, drop);
         };
         if constexpr (TRANS) {
@@ -1335,8 +1368,8 @@ bool one_launch(const AdapterArgs &w, const AdapterPlanShape &shape) {
     const int64_t blocks = (w.out + kAdapterCols - 1) / kAdapterCols;
     const int64_t a_bytes = adapter_padded_rank(w.rank) * w.in * 2;
     const int64_t most = a_bytes > (64 << 10) ? 17 << 20 : 34 << 20;
-    return w.rank <= 64 && shape.rows <= 16 * shape.adapters && a_bytes <= (128 << 10) &&
-           shape.tiles_max * blocks * a_bytes <= most;
+    return w.rank <= 64 && shape.rows <= 16 * shape.adapters && shape.tiles_max <= GRID_Y &&
+           a_bytes <= (128 << 10) && shape.tiles_max * blocks * a_bytes <= most;
 }
 
 hipError_t launch_small(const AdapterArgs &w, const AdapterPlanShape &shape, const int32_t *plan,
@@ -1400,7 +1433,8 @@ hipError_t launch_adapter_fwd(const AdapterArgs &w, const AdapterPlanShape &shap
         return launch_small(w, shape, plan, drop, x, ldx, base, ldbase, y, ldy, h, stream);
     const int parts = adapter_parts(shape.tiles_max, w.in, w.rank);
     float *sums = parts == 1 && h ? h : static_cast<float *>(ws);
-    if (hipError_t e = launch_shrink<false>(w, shape, plan, drop, x, ldx, w.in, sums, parts, stream))
+    if (hipError_t e =
+            launch_shrink<false>(w, shape, plan, drop, x, ldx, w.in, sums, parts, stream))
         return e;
     const DropoutArgs none = {nullptr, 0, 1.0f};
     return launch_expand<false>(w, shape, plan, none, sums, parts, w.out, base, ldbase, y, ldy, h,

