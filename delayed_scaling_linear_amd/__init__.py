@@ -556,10 +556,11 @@ class Dropout:
     _desc: Optional[_DropoutDesc] = field(default=None, init=False, repr=False, compare=False)
 
     def desc(self) -> _DropoutDesc:
-        """The C descriptor, built at the first call and again if the tensor's
-        memory has moved since."""
+        """The C descriptor, built at the first call and again if the tensor
+        has been moved or reshaped in place since."""
         d = self._desc
-        if d is None or d.rng != self.rng.data_ptr():
+        if d is None or d.rng != self.rng.data_ptr() or self.rng.numel() != 2 \
+                or not self.rng.is_contiguous():
             if self.rng is None or self.rng.numel() != 2:
                 raise ValueError("Dropout.rng must hold two elements (seed, offset)")
             d = _DropoutDesc(_ptr(self.rng, torch.int64, "Dropout.rng"), self.p, 0)
@@ -692,12 +693,14 @@ class Adapters:
     _desc: Optional[_AdaptersDesc] = field(default=None, init=False, repr=False, compare=False)
 
     def desc(self) -> _AdaptersDesc:
-        """The C descriptor, built at the first call and again if a tensor's
-        memory has moved since."""
+        """The C descriptor, built at the first call and again if a tensor has
+        been moved or reshaped in place since."""
         a, b, alpha = self.a, self.b, self.alpha
         d = self._desc
         if d is not None and d.a == a.data_ptr() and d.b == b.data_ptr() \
-                and d.alpha == alpha.data_ptr():
+                and d.alpha == alpha.data_ptr() and a.shape == (d.count, d.rank, d.in_) \
+                and b.shape == (d.count, d.out, d.rank) and alpha.shape == (d.count,) \
+                and a.is_contiguous() and b.is_contiguous() and alpha.is_contiguous():
             return d
         if a.dim() != 3 or b.dim() != 3:
             raise ValueError("Adapters.a and Adapters.b must be 3-D")

@@ -687,11 +687,12 @@ __global__ __launch_bounds__(expand_threads(RP), 2) void adapter_expand_kernel(
 
     // The tile ahead: its values of h (the first K part) and its base, as loaded:
     // nothing is done to them before their tile's turn, so nothing waits.  (A
-    // position without a row reads row 0, an output without a base itself.)
+    // position without a row reads row 0; without a base all read the output's
+    // row 0, which stays in the caches.)
     f32x4 h_ahead[ITEMS][2];
     Cols<L> ahead[2][4];
     const uint16_t *bases_at = base ? base : out;
-    const uint32_t ld_bases = base ? ldbase : ldo;
+    const uint32_t ld_bases = base ? ldbase : 0u;
     auto h_at = [&](int row, int it) {
         const int j = 8 * ((tid + it * NT) % OCTS);
         return h + (int64_t)max(row, 0) * R + (j < R ? j : 0);
@@ -1166,21 +1167,19 @@ __global__ __launch_bounds__(wgrad_threads(RP), 2) void adapter_wgrad_kernel(
                     xs[t][d] = (t & 1)
                                    ? high_halves(in[2 * d].d[t >> 1], in[2 * d + 1].d[t >> 1])
                                    : low_halves(in[2 * d].d[t >> 1], in[2 * d + 1].d[t >> 1]);
-            // The next rank block's operands are read while this one's are used.
-            u32x4 b[2][PARTS];
+            // The operands are read two steps ahead of their use.
+            constexpr int STEPS = J * PARTS, RING = 3;
+            auto operand = [&](int q) { return hs[buf][(q % PARTS * J + q / PARTS) * 64 + lane]; };
+            u32x4 b[RING];
 #pragma unroll
-            for (int p = 0; p < PARTS; ++p) b[0][p] = hs[buf][p * J * 64 + lane];
+            for (int q = 0; q < min(RING - 1, STEPS); ++q) b[q] = operand(q);
 #pragma unroll
-            for (int jb = 0; jb < J; ++jb) {
-                if (jb + 1 < J)
-#pragma unroll
-                    for (int p = 0; p < PARTS; ++p)
-                        b[(jb + 1) & 1][p] = hs[buf][(p * J + jb + 1) * 64 + lane];
+            for (int q = 0; q < STEPS; ++q) {
+                if (q + RING - 1 < STEPS) b[(q + RING - 1) % RING] = operand(q + RING - 1);
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int p = 0; p < PARTS; ++p)
-#pragma unroll
-                    for (int t = 0; t < L; ++t) acc[t][jb] = mfma(xs[t], b[jb & 1][p], acc[t][jb]);
+                for (int t = 0; t < L; ++t)
+                    acc[t][q / PARTS] = mfma(xs[t], b[q % RING], acc[t][q / PARTS]);
             }
             if (more) stage_short(buf ^ 1);
             __syncthreads();

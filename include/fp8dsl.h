@@ -447,7 +447,7 @@ int fp8_dropout(const fp8_dropout_t *drop, const void *x, int64_t ldx, const voi
  *         (>= cols, multiples of 8; 16-byte aligned).
  * y       device bf16 [rows, cols], row stride ldy (as ldx), or NULL: only the
  *         codes are wanted.  May be x or residual (same pointer and stride),
- *         else must not overlap them.
+ *         else must not overlap them.  A set noop_flag leaves it unwritten too.
  * dbias   NULL, or as fp8_cast_transpose_amax_dbias, with its workspace of
  *         fp8_cast_dbias_workspace_bytes(rows, cols) bytes (workspace and
  *         workspace_bytes are not read without dbias).
@@ -666,7 +666,9 @@ int fp8_linear_wgrad_ws(const fp8_tensor_t *dy, const fp8_tensor_t *x, void *dw,
  * Products and sums are taken in fp32; the products over `rank` see h and g as
  * sums of bf16 parts, within 2^-16 of each value (2^-23 where the result is
  * stored in fp32).  Each row's result depends on that row and its adapter
- * alone.  Repeated calls give identical bits.
+ * alone, but for the order of its sums, which follows from the call's sizes.
+ * Repeated calls give identical bits.  An infinity that meets h or g in a
+ * product over `rank` or over the rows gives an infinity or a NaN.
  */
 typedef struct fp8_adapters {
     const uint16_t *a;      /* device bf16 [count, rank, in], 16-byte aligned  */

@@ -451,3 +451,23 @@ def test_a_plan_that_was_never_built_writes_nothing():
         assert rc == 0
         torch.cuda.synchronize()
         assert (y == -7.0).all()
+
+
+def test_handles_reshaped_in_place():
+    """The descriptors that Adapters and Dropout keep follow their tensors."""
+    wide = Case(40, 64, 48, 16, 3, [r % 4 - 1 for r in range(40)], seed=5)
+    _same_bf16(wide.forward()[0], wide.want_forward()[0])
+    narrow = Case(40, 64, 48, 8, 3, wide.ids.tolist(), seed=6)
+    # the same memory, now of rank 8
+    w = wide.w
+    w.a.resize_(3, 8, 64).copy_(narrow.a)
+    w.b.resize_(3, 48, 8).copy_(narrow.b)
+    w.alpha.copy_(narrow.alpha)
+    narrow.w = w
+    _same_bf16(narrow.forward()[0], narrow.want_forward()[0])
+    drop = dsl.Dropout(0.5, torch.tensor([1, 2], device=DEV))
+    x = torch.ones(8, 16, device=DEV)
+    dsl.fp8_dropout(x, drop, torch.empty_like(x))
+    drop.rng.resize_(1)
+    with pytest.raises(ValueError):
+        dsl.fp8_dropout(x, drop, torch.empty_like(x))
