@@ -355,6 +355,12 @@ __global__ __launch_bounds__(shrink_threads(RP), 2) void adapter_shrink_kernel(
     const int64_t kw = ((kpart + NW - 1) / NW + STEP - 1) / STEP * STEP;
     const int64_t k0 = blockIdx.y * kpart + wave * kw;
     const int64_t k1 = min(min(k0 + kw, (int64_t)(blockIdx.y + 1) * kpart), C);
+    // Rows are often a multiple of 4 KiB apart: workgroups that all began at
+    // their first column would ask a part of the memory channels for it.  So where
+    // x's bytes count they begin at different steps, also those of one XCD.
+    const int steps = k0 < k1 ? (int)((k1 - k0 + STEP - 1) / STEP) : 0;
+    const int first =
+        RP <= 32 && steps > 0 ? (int)((blockIdx.x + blockIdx.x / 8) % (unsigned)steps) : 0;
     const int oct = lane % OCTS;
     const DropoutKey key(DROP ? drop.rng : nullptr, DROP);
     const uint16_t *px[XI];
@@ -449,10 +455,12 @@ __global__ __launch_bounds__(shrink_threads(RP), 2) void adapter_shrink_kernel(
 #pragma unroll
             for (int jb = 0; jb < J; ++jb) acc[mb][jb] = f32x4{0.f, 0.f, 0.f, 0.f};
         if (pass > 0) __syncthreads();       // the pass before has read its sums
-        if (k0 < k1) load(k0);
-        for (int64_t kk = k0; kk < k1; kk += STEP) {
-            stage(kk);
-            if (kk + STEP < k1) load(kk + STEP);
+        if (steps > 0) load(k0 + first * STEP);
+        for (int s = 0, at = first; s < steps; ++s) {
+            const int ahead = at + 1 == steps ? 0 : at + 1;
+            stage(k0 + (int64_t)at * STEP);
+            if (s + 1 < steps) load(k0 + (int64_t)ahead * STEP);
+            at = ahead;
             // A wave's LDS operations complete in issue order, so its reads see
             // every lane's writes and the next writes come after them; the
             // fences keep the compiler from moving them across.
@@ -473,9 +481,19 @@ __global__ __launch_bounds__(shrink_threads(RP), 2) void adapter_shrink_kernel(
             }
             __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
         }
-        // The waves' sums of 16 rows at a time, added in wave order.
+        // The waves' sums of 16 rows at a time, added in wave order, four ranks a
+        // thread.
         float *red = reinterpret_cast<float *>(lds);
         const float scale = alpha[a] * drop.factor;
+        constexpr int OUTS = (4 * RP + 64 * NW - 1) / (64 * NW);
+        int out_row[MB][OUTS];
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+            for (int i = 0; i < OUTS; ++i)
+                out_row[mb][i] =
+                    adapter[mb / 2] == a
+                        ? tile_row[16 * mb + min((tid + 64 * NW * i) / (RP / 4), 15)] : -1;
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb) {
             if (adapter[mb / 2] != a) continue;
@@ -486,13 +504,17 @@ __global__ __launch_bounds__(shrink_threads(RP), 2) void adapter_shrink_kernel(
                 for (int i = 0; i < 4; ++i)
                     red[wave * 16 * RP + (4 * g + i) * RP + jb * 16 + col] = acc[mb][jb][i];
             __syncthreads();
-            for (int e = tid; e < 16 * RP; e += 64 * NW) {
-                const int r = tile_row[16 * mb + e / RP], j = e % RP;
-                float sum = red[e];
 #pragma unroll
-                for (int n = 1; n < NW; ++n) sum += red[n * 16 * RP + e];
-                if (j < R && r >= 0)
-                    sums[blockIdx.y * part_stride + (int64_t)r * R + j] = scale * sum;
+            for (int i = 0; i < OUTS; ++i) {
+                const int e = 4 * (tid + 64 * NW * i), j = e % RP;
+                if (e >= 16 * RP) continue;
+                f32x4 sum = *reinterpret_cast<const f32x4 *>(red + e);
+#pragma unroll
+                for (int n = 1; n < NW; ++n)
+                    sum += *reinterpret_cast<const f32x4 *>(red + n * 16 * RP + e);
+                if (j < R && out_row[mb][i] >= 0)
+                    *reinterpret_cast<f32x4 *>(sums + blockIdx.y * part_stride +
+                                               (int64_t)out_row[mb][i] * R + j) = scale * sum;
             }
         }
     }
