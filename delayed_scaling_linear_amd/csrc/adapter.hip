@@ -293,7 +293,10 @@ constexpr int shrink_waves(int rp) { return rp >= 64 ? 4 : 8; }
 constexpr int shrink_threads(int rp) { return 64 * shrink_waves(rp); }
 constexpr int shrink_step(int rp) { return rp >= 128 ? 32 : 64; }
 // Tiles of a workgroup: rank 128's weights are four times a tile's x, so two
-// tiles of an adapter share them.
+// tiles of an adapter share them.  A pair of two adapters' tiles is split: its
+// second tile goes to one of the workgroups, one for each adapter, behind those of the
+// pairs (a second pass over the weights instead made such a workgroup the kernel's
+// tail).
 constexpr int shrink_tiles(int rp) { return rp >= 128 ? 2 : 1; }
 // 16-byte pieces of LDS a wave stages: x (two row blocks a tile) and W (rp / 16).
 constexpr int shrink_wave_pieces(int rp) {
@@ -305,7 +308,7 @@ static_assert(shrink_wave_pieces(128) * 16 >= 16 * 128 * 4 &&
                   shrink_wave_pieces(16) * 16 >= 16 * 16 * 4,
               "the sums of 16 rows meet in the same LDS");
 
-// Grid: (groups of T tiles, K parts); part y sums columns [y * kpart,
+// Grid: (groups of T tiles, and for T = 2 the adapters; K parts); part y sums columns [y * kpart,
 // (y + 1) * kpart) and writes sums[y][row][0 .. R).
 //
 // A lane of an MFMA operand holds one row's 8 columns, so sixteen neighbouring
@@ -338,19 +341,33 @@ __global__ __launch_bounds__(shrink_threads(RP), 2) void adapter_shrink_kernel(
     u32x4 *lx = lds + wave * shrink_wave_pieces(RP), *lw = lx + U * MB * 64;
     // All of the plan's words for these tiles in one round trip.
     const bool built = plan.built();
-    const int tile0 = blockIdx.x * T;
+    int tile0 = blockIdx.x * T;
+    bool alone = false;
+    if constexpr (T > 1) {
+        const int pairs = (tiles_max + 1) / 2;
+        if ((int)blockIdx.x >= pairs) {
+            // An adapter whose first tile is the second of its pair.
+            if (!built) return;
+            const int a = blockIdx.x - pairs;
+            tile0 = plan.group_tile0[a];
+            alone = true;
+            if ((tile0 & 1) == 0 || plan.group_tile0[a + 1] == tile0) return;
+        }
+    }
     const int32_t *tile_row = plan.tile_row + (int64_t)tile0 * TILE;
     int adapter[T], x_row[XI];
 #pragma unroll
     for (int t = 0; t < T; ++t)
-        adapter[t] = tile0 + t < tiles_max ? plan.tile_adapter[tile0 + t] : -2;
+        adapter[t] = tile0 + t < tiles_max && (t == 0 || !alone)
+                         ? plan.tile_adapter[tile0 + t] : -2;
 #pragma unroll
     for (int i = 0; i < XI; ++i) {
         const int at = lane / OCTS + i * (64 / OCTS);
         // (a tile that there is not: its row is never stored)
         x_row[i] = tile_row[tile0 + at / TILE < tiles_max ? at : 0];
     }
-    if (!built) return;
+    const int a = adapter[0];
+    if (!built || a < 0) return;
 
     const int64_t kw = ((kpart + NW - 1) / NW + STEP - 1) / STEP * STEP;
     const int64_t k0 = blockIdx.y * kpart + wave * kw;
@@ -370,7 +387,7 @@ __global__ __launch_bounds__(shrink_threads(RP), 2) void adapter_shrink_kernel(
         px[i] = row_at(src, x_row[i], ld);
     }
 
-    const uint16_t *w = weights;
+    const uint16_t *w = weights + (int64_t)a * R * C;
     u32x4 xr[XI];
     u32x4 wr[TRANS ? 1 : WI];                // TRANS false: as loaded
     Cols<V> tr[TRANS ? WI : 1][8];           // TRANS true: V ranks of 8 columns
@@ -442,80 +459,71 @@ __global__ __launch_bounds__(shrink_threads(RP), 2) void adapter_shrink_kernel(
         }
     };
 
-    // Tiles of different adapters (an adapter's last tile beside the next one's
-    // first) take a pass each.
+    f32x4 acc[MB][J];
 #pragma unroll
-    for (int pass = 0; pass < T; ++pass) {
-        const int a = adapter[pass];
-        if (a < 0 || (pass > 0 && a == adapter[0])) continue;
-        w = weights + (int64_t)a * R * C;
-        f32x4 acc[MB][J];
+    for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
-        for (int mb = 0; mb < MB; ++mb)
+        for (int jb = 0; jb < J; ++jb) acc[mb][jb] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (steps > 0) load(k0 + first * STEP);
+    for (int s = 0, at = first; s < steps; ++s) {
+        const int ahead = at + 1 == steps ? 0 : at + 1;
+        stage(k0 + (int64_t)at * STEP);
+        if (s + 1 < steps) load(k0 + (int64_t)ahead * STEP);
+        at = ahead;
+        // A wave's LDS operations complete in issue order, so its reads see
+        // every lane's writes and the next writes come after them; the
+        // fences keep the compiler from moving them across.
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 #pragma unroll
-            for (int jb = 0; jb < J; ++jb) acc[mb][jb] = f32x4{0.f, 0.f, 0.f, 0.f};
-        if (pass > 0) __syncthreads();       // the pass before has read its sums
-        if (steps > 0) load(k0 + first * STEP);
-        for (int s = 0, at = first; s < steps; ++s) {
-            const int ahead = at + 1 == steps ? 0 : at + 1;
-            stage(k0 + (int64_t)at * STEP);
-            if (s + 1 < steps) load(k0 + (int64_t)ahead * STEP);
-            at = ahead;
-            // A wave's LDS operations complete in issue order, so its reads see
-            // every lane's writes and the next writes come after them; the
-            // fences keep the compiler from moving them across.
-            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-            __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        for (int u = 0; u < U; ++u) {
+            u32x4 xs[MB];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                u32x4 xs[MB];
+            for (int mb = 0; mb < MB; ++mb)
+                xs[mb] = lx[(u * MB + mb) * 64 + slot(4 * u + g, 16 * mb + col)];
 #pragma unroll
-                for (int mb = 0; mb < MB; ++mb)
-                    xs[mb] = lx[(u * MB + mb) * 64 + slot(4 * u + g, 16 * mb + col)];
+            for (int jb = 0; jb < J; ++jb) {
+                const u32x4 b = lw[(u * J + jb) * 64 + slot(4 * u + g, 16 * jb + col)];
 #pragma unroll
-                for (int jb = 0; jb < J; ++jb) {
-                    const u32x4 b = lw[(u * J + jb) * 64 + slot(4 * u + g, 16 * jb + col)];
-#pragma unroll
-                    for (int mb = 0; mb < MB; ++mb) acc[mb][jb] = mfma(xs[mb], b, acc[mb][jb]);
-                }
+                for (int mb = 0; mb < MB; ++mb) acc[mb][jb] = mfma(xs[mb], b, acc[mb][jb]);
             }
-            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
         }
-        // The waves' sums of 16 rows at a time, added in wave order, four ranks a
-        // thread.
-        float *red = reinterpret_cast<float *>(lds);
-        const float scale = alpha[a] * drop.factor;
-        constexpr int OUTS = (4 * RP + 64 * NW - 1) / (64 * NW);
-        int out_row[MB][OUTS];
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    }
+    // The waves' sums of 16 rows at a time, added in wave order, four ranks a
+    // thread.
+    float *red = reinterpret_cast<float *>(lds);
+    const float scale = alpha[a] * drop.factor;
+    constexpr int OUTS = (4 * RP + 64 * NW - 1) / (64 * NW);
+    int out_row[MB][OUTS];
 #pragma unroll
-        for (int mb = 0; mb < MB; ++mb)
+    for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
-            for (int i = 0; i < OUTS; ++i)
-                out_row[mb][i] =
-                    adapter[mb / 2] == a
-                        ? tile_row[16 * mb + min((tid + 64 * NW * i) / (RP / 4), 15)] : -1;
+        for (int i = 0; i < OUTS; ++i)
+            out_row[mb][i] =
+                adapter[mb / 2] == a
+                    ? tile_row[16 * mb + min((tid + 64 * NW * i) / (RP / 4), 15)] : -1;
 #pragma unroll
-        for (int mb = 0; mb < MB; ++mb) {
-            if (adapter[mb / 2] != a) continue;
-            __syncthreads();
+    for (int mb = 0; mb < MB; ++mb) {
+        if (adapter[mb / 2] != a) continue;
+        __syncthreads();
 #pragma unroll
-            for (int jb = 0; jb < J; ++jb)
+        for (int jb = 0; jb < J; ++jb)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    red[wave * 16 * RP + (4 * g + i) * RP + jb * 16 + col] = acc[mb][jb][i];
-            __syncthreads();
+            for (int i = 0; i < 4; ++i)
+                red[wave * 16 * RP + (4 * g + i) * RP + jb * 16 + col] = acc[mb][jb][i];
+        __syncthreads();
 #pragma unroll
-            for (int i = 0; i < OUTS; ++i) {
-                const int e = 4 * (tid + 64 * NW * i), j = e % RP;
-                if (e >= 16 * RP) continue;
-                f32x4 sum = *reinterpret_cast<const f32x4 *>(red + e);
+        for (int i = 0; i < OUTS; ++i) {
+            const int e = 4 * (tid + 64 * NW * i), j = e % RP;
+            if (e >= 16 * RP) continue;
+            f32x4 sum = *reinterpret_cast<const f32x4 *>(red + e);
 #pragma unroll
-                for (int n = 1; n < NW; ++n)
-                    sum += *reinterpret_cast<const f32x4 *>(red + n * 16 * RP + e);
-                if (j < R && out_row[mb][i] >= 0)
-                    *reinterpret_cast<f32x4 *>(sums + blockIdx.y * part_stride +
-                                               (int64_t)out_row[mb][i] * R + j) = scale * sum;
-            }
+            for (int n = 1; n < NW; ++n)
+                sum += *reinterpret_cast<const f32x4 *>(red + n * 16 * RP + e);
+            if (j < R && out_row[mb][i] >= 0)
+                *reinterpret_cast<f32x4 *>(sums + blockIdx.y * part_stride +
+                                           (int64_t)out_row[mb][i] * R + j) = scale * sum;
         }
     }
 }
@@ -1332,7 +1340,8 @@ hipError_t launch_shrink(const AdapterArgs &w, const AdapterPlanShape &shape, co
     hipError_t enabled = hipSuccess;
     const hipError_t e = by_rank(w.rank, [&](auto rp) {
         constexpr int RP = decltype(rp)::value, bytes = shrink_lds_bytes(RP), T = shrink_tiles(RP);
-        const dim3 grid((unsigned)((shape.tiles_max + T - 1) / T), (unsigned)parts);
+        const dim3 grid((unsigned)(T > 1 ? (shape.tiles_max + 1) / 2 + shape.adapters
+                                         : shape.tiles_max), (unsigned)parts);
         auto go = [&](auto dropped) {
             const auto kernel = adapter_shrink_kernel<RP, TRANS, decltype(dropped)::value>;
             static std::atomic<uint64_t> done{0};

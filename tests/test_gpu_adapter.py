@@ -471,3 +471,11 @@ def test_handles_reshaped_in_place():
     drop.rng.resize_(1)
     with pytest.raises(ValueError):
         dsl.fp8_dropout(x, drop, torch.empty_like(x))
+
+
+@pytest.mark.parametrize("tiles", [[1, 1, 1], [1, 2, 0, 1], [0, 3, 2, 3], [2, 2], [1, 0, 0, 1], [3]])
+@pytest.mark.parametrize("rank", [72, 128])
+def test_pairs_of_tiles(rank, tiles):
+    """Adapters that begin in the second tile of a pair, with and without rows."""
+    ids = [a for a, t in enumerate(tiles) for _ in range(32 * t - 5 if t else 0)] + [-1] * 40
+    _exact(Case(len(ids), 72, 264, rank, len(tiles), ids, seed=sum(tiles)))
