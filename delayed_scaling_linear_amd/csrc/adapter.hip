@@ -28,8 +28,8 @@
 // Measured on MI355X, where a large copy moves 5.1 TB/s (us of a whole call,
 // and in brackets its bytes at that rate): 8192 rows of 2048 -> 6144, rank 64,
 // nine requests 65 (47); 2048 -> 8192, rank 16 with dropout, forward 64 (59),
-// backward 92 (46, reading dy once; it is read twice); 16384 rows of 8192 ->
-// 2048, rank 128, backward 350 (178).
+// backward 90 (46, reading dy once; it is read twice); 16384 rows of 8192 ->
+// 2048, rank 128, backward 320 (178).
 #include "adapter.h"
 
 #include "fp8dsl_internal.h"
@@ -322,10 +322,11 @@ static_assert(shrink_wave_pieces(128) * 16 >= 16 * 128 * 4 &&
 //   TRANS false, W [R, C] (A in the forward): staged as x is.
 //   TRANS true, W [C, R] (B in the backward): a lane reads V ranks of 8 columns
 //   and turns them in registers.
-// Bound by reading x at low rank: dy [8192, 8192] at rank 16 30 to 35 us (134 MB,
-// 3.8 to 4.5 TB/s; a library maximum over as much reads 3.0).  From rank 32 on the
-// weights, read again by each tile, and the latency of a wave's steps count: 41
-// us at rank 32, 55 at 64; x [8192, 2048] at rank 64 17 us.
+// Bound by reading x at low rank: dy [8192, 8192] at rank 16 28 us (134 MB, 4.8
+// TB/s; a library maximum over as much reads 3.0).  From rank 32 on the weights,
+// read again by each tile, and the latency of a wave's steps count: 39 us at rank
+// 32, 54 at 64; x [8192, 2048] at rank 64 17 us; [16384, 2048] at rank 128 52 (as
+// long with one tile a workgroup or steps of 64 columns).
 template <int RP, bool TRANS, bool DROP>
 __global__ __launch_bounds__(shrink_threads(RP), 2) void adapter_shrink_kernel(
     PlanView plan, int tiles_max, const uint16_t *__restrict__ src, uint32_t ld, int64_t C,
@@ -1095,7 +1096,7 @@ constexpr int wgrad_threads(int rp) { return kAdapterCols / wgrad_lane_cols(rp) 
 // The next tile's loads of both are in flight while the current one is
 // multiplied.
 // Bound by x and dy at low rank: [8192, 2048 + 8192] at rank 16 39 us (168 MB,
-// 4.3 TB/s).  At rank 128, [16384, 2048 + 8192], 146 us: three bf16 parts make 129
+// 4.3 TB/s); at rank 64 and in fp32 70, in bf16 64.  At rank 128, [16384, 2048 + 8192], 146 us: three bf16 parts make 129
 // GFLOP of 43, 0.88 PFLOP/s where a large library product reaches 1.24.
 template <int RP, int PARTS, bool DROP>
 __global__ __launch_bounds__(wgrad_threads(RP), 2) void adapter_wgrad_kernel(
@@ -1197,7 +1198,8 @@ __global__ __launch_bounds__(wgrad_threads(RP), 2) void adapter_wgrad_kernel(
                     xs[t][d] = (t & 1)
                                    ? high_halves(in[2 * d].d[t >> 1], in[2 * d + 1].d[t >> 1])
                                    : low_halves(in[2 * d].d[t >> 1], in[2 * d + 1].d[t >> 1]);
-            // The operands are read two steps ahead of their use.
+            // The operands are read two steps ahead of their use (a rank block ahead
+            // takes twice the registers: at rank 64 and in fp32 84 us against 70).
             constexpr int STEPS = J * PARTS, RING = 3;
             auto operand = [&](int q) { return hs[buf][(q % PARTS * J + q / PARTS) * 64 + lane]; };
             u32x4 b[RING];
