@@ -17,6 +17,9 @@ constexpr int kAdapterMaxRank = 128;
 constexpr int kAdapterMaxCount = 4096;
 // Columns of one workgroup of the expand and of the weight-gradient kernel.
 constexpr int kAdapterCols = 512;
+// bf16 parts of a short operand of the weight gradients: together all 24 bits of
+// an fp32 value.
+constexpr int kAdapterGradParts = 3;
 
 // Device layout of a plan (int32 words): the batch's rows sorted by adapter,
 // every adapter's rows starting a new tile.
@@ -82,14 +85,15 @@ inline int64_t adapter_slots(const AdapterPlanShape &p, int64_t chunk) {
 }
 
 // Workspace: K-part sums of h or g, both short operands of the weight
-// gradients as up to three bf16 parts, and the gradients' partial sums.
+// gradients as bf16 parts, and the gradients' partial sums.
 struct AdapterWorkspace {
     int64_t sums, packed, grads, bytes;
     AdapterWorkspace(const AdapterPlanShape &p, int64_t rank, int64_t in, int64_t out) {
         const int64_t parts = std::max(adapter_parts(p.tiles_max, in, rank),
                                        adapter_parts(p.tiles_max, out, rank));
         sums = (parts * p.rows * rank * 4 + 255) / 256 * 256;
-        packed = 2 * p.tiles_max * kAdapterTile * adapter_padded_rank(rank) * 3 * 2;
+        packed = 2 * p.tiles_max * kAdapterTile * adapter_padded_rank(rank) *
+                 kAdapterGradParts * 2;
         grads = adapter_slots(p, adapter_chunk(p.tiles_max, rank, in, out)) * rank * (in + out) * 4;
         bytes = sums + packed + grads;
     }

@@ -20,8 +20,10 @@
 //            bits on every run).
 //
 // h and g are held in fp32.  Where they feed a matrix core they are split
-// into bf16 parts that add up to them: two (the error is 2^-16 of h) where
-// the result is rounded to bf16, three (2^-24) where it is stored in fp32.
+// into bf16 parts that add up to them: two (the error is 2^-16 of h) for y and
+// dx, bf16 results beside a base, three (all of an fp32 value's 24 bits) for dA
+// and dB, which bf16 takes as the fp32 result rounded once: with two parts one
+// in 200 of its values went to the other neighbour.
 // Dropout multiplies by the mask on the operand (exact) and by f in fp32 on
 // the sums.
 //
@@ -607,7 +609,6 @@ struct PackSide {
     u32x4 *packed;
 };
 
-template <int PARTS>
 __device__ __forceinline__ void pack_tile(const PackSide &side, const int32_t *tile_row,
                                           int64_t tile, int R, int64_t part_stride, int blocks) {
     for (int item = threadIdx.x; item < blocks * 64; item += blockDim.x) {
@@ -624,17 +625,16 @@ __device__ __forceinline__ void pack_tile(const PackSide &side, const int32_t *t
             for (int i = 0; i < 8; ++i) v[i] += p[(int64_t)max(r[i], 0) * R];
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = r[i] >= 0 && j < R ? v[i] : 0.0f;
-        u32x4 part[PARTS];
-        split8<PARTS>(v, part);
+        u32x4 part[kAdapterGradParts];
+        split8(v, part);
 #pragma unroll
-        for (int n = 0; n < PARTS; ++n)
-            side.packed[((tile * PARTS + n) * blocks + jb) * 64 + l] = part[n];
+        for (int n = 0; n < kAdapterGradParts; ++n)
+            side.packed[((tile * kAdapterGradParts + n) * blocks + jb) * 64 + l] = part[n];
     }
 }
 
 struct PackArgs {
     PackSide g, h;
-    int split;                  // bf16 parts: 2 or 3
     int64_t rows;               // rows of the expand's grid that pack; 0: nothing to pack
 };
 
@@ -678,13 +678,8 @@ __global__ __launch_bounds__(expand_threads(RP), 2) void adapter_expand_kernel(
         if (part < pack.rows) {
             const int64_t tile = part * gridDim.x + blockIdx.x;
             if (tile >= tiles_max || !plan.built() || plan.tile_adapter[tile] < 0) return;
-            if (pack.split == 3) {
-                pack_tile<3>(pack.g, plan.tile_row, tile, R, part_stride, RP / 16);
-                pack_tile<3>(pack.h, plan.tile_row, tile, R, 0, RP / 16);
-            } else {
-                pack_tile<2>(pack.g, plan.tile_row, tile, R, part_stride, RP / 16);
-                pack_tile<2>(pack.h, plan.tile_row, tile, R, 0, RP / 16);
-            }
+            pack_tile(pack.g, plan.tile_row, tile, R, part_stride, RP / 16);
+            pack_tile(pack.h, plan.tile_row, tile, R, 0, RP / 16);
             return;
         }
         part -= pack.rows;
@@ -1096,14 +1091,14 @@ constexpr int wgrad_threads(int rp) { return kAdapterCols / wgrad_lane_cols(rp) 
 // The next tile's loads of both are in flight while the current one is
 // multiplied.
 // Bound by x and dy at low rank: [8192, 2048 + 8192] at rank 16 39 us (168 MB,
-// 4.3 TB/s); at rank 64 and in fp32 70, in bf16 64.  At rank 128, [16384, 2048 + 8192], 146 us: three bf16 parts make 129
-// GFLOP of 43, 0.88 PFLOP/s where a large library product reaches 1.24.
-template <int RP, int PARTS, bool DROP>
+// 4.3 TB/s); at rank 64 70, bf16 results alike.  At rank 128, [16384, 2048 + 8192], 146 us: three bf16 parts
+// make 129 GFLOP of 43, 0.88 PFLOP/s where a large library product reaches 1.24.
+template <int RP, bool DROP>
 __global__ __launch_bounds__(wgrad_threads(RP), 2) void adapter_wgrad_kernel(
     PlanView plan, WgradSide left, WgradSide right, int left_blocks, int R, int chunk,
     DropoutArgs drop) {
     constexpr int L = wgrad_lane_cols(RP), NT = wgrad_threads(RP);
-    constexpr int J = RP / 16, PIECES = PARTS * J * 64;
+    constexpr int PARTS = kAdapterGradParts, J = RP / 16, PIECES = PARTS * J * 64;
     constexpr int ITEMS = (PIECES + NT - 1) / NT;
     __shared__ u32x4 hs[2][PIECES];
     if (!plan.built()) return;
@@ -1199,7 +1194,7 @@ __global__ __launch_bounds__(wgrad_threads(RP), 2) void adapter_wgrad_kernel(
                                    ? high_halves(in[2 * d].d[t >> 1], in[2 * d + 1].d[t >> 1])
                                    : low_halves(in[2 * d].d[t >> 1], in[2 * d + 1].d[t >> 1]);
             // The operands are read two steps ahead of their use (a rank block ahead
-            // takes twice the registers: at rank 64 and in fp32 84 us against 70).
+            // takes twice the registers: at rank 64 84 us against 70).
             constexpr int STEPS = J * PARTS, RING = 3;
             auto operand = [&](int q) { return hs[buf][(q % PARTS * J + q / PARTS) * 64 + lane]; };
             u32x4 b[RING];
@@ -1485,14 +1480,12 @@ hipError_t launch_adapter_backward(const AdapterArgs &w, const AdapterPlanShape 
     const DropoutArgs none = {nullptr, 0, 1.0f};
     if (hipError_t e = launch_shrink<true>(w, shape, plan, none, dy, lddy, w.out, g, parts, stream))
         return e;
-    const int split = out_dtype == FP8_DTYPE_FP32 ? 3 : 2;
     const int64_t packed = layout.packed / 2;
     char *at = static_cast<char *>(ws) + layout.sums;
     PackArgs pack{};
     if (da) {
         pack.g = {g, parts, reinterpret_cast<u32x4 *>(at)};
         pack.h = {h, 1, reinterpret_cast<u32x4 *>(at + packed)};
-        pack.split = split;
     }
     if (hipError_t e = launch_expand<true>(w, shape, plan, drop, g, parts, w.in, base, ldbase, dx,
                                            lddx, nullptr, pack, stream))
@@ -1510,20 +1503,13 @@ hipError_t launch_adapter_backward(const AdapterArgs &w, const AdapterPlanShape 
     const int right_blocks = (int)((w.out + kAdapterCols - 1) / kAdapterCols);
     const dim3 grid = grid_of(left_blocks + right_blocks, chunks);
     hipError_t e = by_rank(w.rank, [&](auto rp) {
-        auto go = [&](auto parts_, auto dropped) {
-            hipLaunchKernelGGL((adapter_wgrad_kernel<decltype(rp)::value, decltype(parts_)::value,
-                                                     decltype(dropped)::value>),
+        auto go = [&](auto dropped) {
+            hipLaunchKernelGGL((adapter_wgrad_kernel<decltype(rp)::value, decltype(dropped)::value>),
                                grid, dim3(wgrad_threads(decltype(rp)::value)), 0, stream, v, left,
                                right, left_blocks, w.rank, (int)chunk, drop);
         };
-        using Two = std::integral_constant<int, 2>;
-        using Three = std::integral_constant<int, 3>;
-        auto by_drop = [&](auto parts_) {
-            if (drop.rng) go(parts_, std::true_type{});
-            else go(parts_, std::false_type{});
-        };
-        if (split == 3) by_drop(Three{});
-        else by_drop(Two{});
+        if (drop.rng) go(std::true_type{});
+        else go(std::false_type{});
     });
     if (e) return e;
     const int64_t a_blocks = (w.rank * w.in / 4 + THREADS - 1) / THREADS;

@@ -663,9 +663,10 @@ int fp8_linear_wgrad_ws(const fp8_tensor_t *dy, const fp8_tensor_t *x, void *dw,
  *              dB_a  = sum over the adapter's rows of dy[r]^T h[r]
  *
  * base is what the shared projection wrote (fp8_linear_fwd, fp8_linear_dgrad).
- * Products and sums are taken in fp32; the products over `rank` see h and g as
- * sums of bf16 parts, within 2^-16 of each value (2^-23 where the result is
- * stored in fp32).  Each row's result depends on that row and its adapter
+ * Products and sums are taken in fp32.  y and dx see h and g as sums of two
+ * bf16 parts, within 2^-16 of each value; dA and dB see all 24 bits of them
+ * (of values from 2^-110 on), and in bf16 they are the fp32 result rounded
+ * once.  Each row's result depends on that row and its adapter
  * alone, but for the order of its sums, which follows from the call's sizes.
  * Repeated calls give identical bits.  An infinity that meets h or g in a
  * product over `rank` or over the rows gives an infinity or a NaN.
