@@ -375,12 +375,9 @@ __global__ __launch_bounds__(shrink_threads(RP), 2) void adapter_shrink_kernel(
     const int64_t kw = ((kpart + NW - 1) / NW + STEP - 1) / STEP * STEP;
     const int64_t k0 = blockIdx.y * kpart + wave * kw;
     const int64_t k1 = min(min(k0 + kw, (int64_t)(blockIdx.y + 1) * kpart), C);
-    // Rows are often a multiple of 4 KiB apart: workgroups that all began at
-    // their first column would ask a part of the memory channels for it.  So where
-    // x's bytes count they begin at different steps, also those of one XCD.
+    // Every workgroup takes its columns in one order, so that a row's sums do not
+    // depend on the tile that it is in.
     const int steps = k0 < k1 ? (int)((k1 - k0 + STEP - 1) / STEP) : 0;
-    const int first =
-        RP <= 32 && steps > 0 ? (int)((blockIdx.x + blockIdx.x / 8) % (unsigned)steps) : 0;
     const int oct = lane % OCTS;
     const DropoutKey key(DROP ? drop.rng : nullptr, DROP);
     const uint16_t *px[XI];
@@ -467,12 +464,10 @@ __global__ __launch_bounds__(shrink_threads(RP), 2) void adapter_shrink_kernel(
     for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
         for (int jb = 0; jb < J; ++jb) acc[mb][jb] = f32x4{0.f, 0.f, 0.f, 0.f};
-    if (steps > 0) load(k0 + first * STEP);
-    for (int s = 0, at = first; s < steps; ++s) {
-        const int ahead = at + 1 == steps ? 0 : at + 1;
-        stage(k0 + (int64_t)at * STEP);
-        if (s + 1 < steps) load(k0 + (int64_t)ahead * STEP);
-        at = ahead;
+    if (steps > 0) load(k0);
+    for (int s = 0; s < steps; ++s) {
+        stage(k0 + (int64_t)s * STEP);
+        if (s + 1 < steps) load(k0 + (int64_t)(s + 1) * STEP);
         // A wave's LDS operations complete in issue order, so its reads see
         // every lane's writes and the next writes come after them; the
         // fences keep the compiler from moving them across.

@@ -666,10 +666,11 @@ int fp8_linear_wgrad_ws(const fp8_tensor_t *dy, const fp8_tensor_t *x, void *dw,
  * Products and sums are taken in fp32.  y and dx see h and g as sums of two
  * bf16 parts, within 2^-16 of each value; dA and dB see all 24 bits of them
  * (of values from 2^-110 on), and in bf16 they are the fp32 result rounded
- * once.  Each row's result depends on that row and its adapter
- * alone, but for the order of its sums, which follows from the call's sizes.
- * Repeated calls give identical bits.  An infinity that meets h or g in a
- * product over `rank` or over the rows gives an infinity or a NaN.
+ * once.  A row's h, y and dx depend on that row, its adapter and the call's
+ * sizes alone, to the last bit: their sums run in an order that follows from
+ * the sizes, whatever the other rows ask for.  Repeated calls give identical
+ * bits.  An infinity that meets h or g in a product over `rank` or over the
+ * rows gives an infinity or a NaN.
  */
 typedef struct fp8_adapters {
     const uint16_t *a;      /* device bf16 [count, rank, in], 16-byte aligned  */

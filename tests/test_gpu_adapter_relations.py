@@ -3,6 +3,7 @@ values, where the order of sums and every rounding show."""
 import pytest
 import torch
 
+import delayed_scaling_linear_amd as dsl
 from tests.gpu_util import bits16
 from tests.test_gpu_adapter import Case, _ids
 
@@ -18,3 +19,22 @@ def test_bf16_gradients_are_the_fp32_ones_rounded_once(rows, k, n, rank, p):
     assert torch.equal(dx16, dx)
     for got, exact in ((da16, da), (db16, db)):
         assert (bits16(got) == bits16(exact.to(torch.bfloat16))).all()
+
+
+@pytest.mark.parametrize("rows, k, n, rank, p", [(4200, 2048, 1048, 16, 0.0), (4200, 1048, 2048, 8, 0.1),
+                                                 (4200, 2056, 2048, 32, 0.5), (2100, 1032, 2056, 64, 0.0),
+                                                 (2100, 2048, 2048, 128, 0.0), (48, 1048, 776, 16, 0.1)])
+def test_a_rows_results_do_not_depend_on_the_other_rows(rows, k, n, rank, p):
+    """Batches of one size that share their last rows: those rows' h, y and dx
+    have the same bits wherever the plan puts them."""
+    same, count = 30, 3
+    c = Case(rows, k, n, rank, count, _ids(rows, count), p=p, ints=False)
+    first = None
+    for seed in range(4):
+        ids = _ids(rows, count, seed=seed, none=0.3 * seed)
+        ids[-same:] = [r % (count + 1) - 1 for r in range(same)]
+        dsl.fp8_adapter_plan(c.dev(torch.as_tensor(ids, dtype=torch.int32)), c.plan)
+        got = [t[-same:] for t in (*c.forward(), c.backward()[0])]
+        first = first or got
+        for a, b in zip(first, got):
+            assert torch.equal(a, b)
