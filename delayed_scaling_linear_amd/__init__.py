@@ -557,10 +557,10 @@ class Dropout:
 
     def desc(self) -> _DropoutDesc:
         """The C descriptor, built at the first call and again if the tensor
-        has been moved or reshaped in place since."""
+        has been moved, reshaped or given another type in place since."""
         d = self._desc
         if d is None or d.rng != self.rng.data_ptr() or self.rng.numel() != 2 \
-                or not self.rng.is_contiguous():
+                or self.rng.dtype is not torch.int64 or not self.rng.is_contiguous():
             if self.rng is None or self.rng.numel() != 2:
                 raise ValueError("Dropout.rng must hold two elements (seed, offset)")
             d = _DropoutDesc(_ptr(self.rng, torch.int64, "Dropout.rng"), self.p, 0)
@@ -694,12 +694,14 @@ class Adapters:
 
     def desc(self) -> _AdaptersDesc:
         """The C descriptor, built at the first call and again if a tensor has
-        been moved or reshaped in place since."""
+        been moved, reshaped or given another type in place since."""
         a, b, alpha = self.a, self.b, self.alpha
         d = self._desc
         if d is not None and d.a == a.data_ptr() and d.b == b.data_ptr() \
                 and d.alpha == alpha.data_ptr() and a.shape == (d.count, d.rank, d.in_) \
                 and b.shape == (d.count, d.out, d.rank) and alpha.shape == (d.count,) \
+                and a.dtype is torch.bfloat16 and b.dtype is torch.bfloat16 \
+                and alpha.dtype is torch.float32 \
                 and a.is_contiguous() and b.is_contiguous() and alpha.is_contiguous():
             return d
         if a.dim() != 3 or b.dim() != 3:

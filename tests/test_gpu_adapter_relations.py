@@ -38,3 +38,18 @@ def test_a_rows_results_do_not_depend_on_the_other_rows(rows, k, n, rank, p):
         first = first or got
         for a, b in zip(first, got):
             assert torch.equal(a, b)
+
+
+def test_handles_refuse_a_type_changed_in_place():
+    """Memory that now holds another type at the same address and in the same
+    shape (a module converted after its first call) is not read as the old one."""
+    c = Case(40, 72, 88, 16, 3, _ids(40, 3), p=0.5)
+    c.forward()
+    for t, other in ((c.w.a, torch.float16), (c.w.b, torch.float16), (c.w.alpha, torch.int32),
+                     (c.drop.rng, torch.float64)):
+        was = t.dtype
+        t.data = t.data.view(other)
+        with pytest.raises(TypeError, match=str(was)):
+            c.forward()
+        t.data = t.data.view(was)
+    c.forward()
