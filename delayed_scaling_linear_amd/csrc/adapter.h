@@ -67,14 +67,20 @@ inline int adapter_parts(int64_t tiles, int64_t C, int64_t rank) {
     const int64_t fill = std::min<int64_t>({256 / groups, C / 256, 16});
     return (int)std::max<int64_t>({1, fill, std::min(resident / groups, C / 2048)});
 }
+// Rows of the sums of all parts where there is more than one: workgroups (256, or
+// `resident`) times rows of one, at most 520 * 64.
+constexpr int64_t kAdapterSumRows = 520 * 64;
 
 // Tiles of one weight-gradient workgroup: a partial sum of R fp32 per column
 // is written and read per workgroup, so as few of them as fill the chip (two
 // workgroups per CU; one of rank 128, which has twice the threads).
-inline int64_t adapter_chunk(int64_t tiles, int64_t rank, int64_t in, int64_t out) {
+inline int64_t adapter_chunks(int64_t rank, int64_t in, int64_t out) {
     const int64_t blocks = (in + kAdapterCols - 1) / kAdapterCols +
                            (out + kAdapterCols - 1) / kAdapterCols;
-    const int64_t chunks = std::max<int64_t>(1, (rank > 64 ? 256 : 512) / blocks);
+    return std::max<int64_t>(1, (rank > 64 ? 256 : 512) / blocks);
+}
+inline int64_t adapter_chunk(int64_t tiles, int64_t rank, int64_t in, int64_t out) {
+    const int64_t chunks = adapter_chunks(rank, in, out);
     return std::max<int64_t>(1, (tiles + chunks - 1) / chunks);
 }
 
@@ -86,16 +92,36 @@ inline int64_t adapter_slots(const AdapterPlanShape &p, int64_t chunk) {
 
 // Workspace: K-part sums of h or g, both short operands of the weight
 // gradients as bf16 parts, and the gradients' partial sums.
+// Each is sized by a bound that does not fall when rows, adapters or rank
+// rise, so that the workspace of a program's largest batch serves all of its
+// batches.  (The splits themselves do not rise: fewer tiles run in more K
+// parts, and 300 rows of one adapter need more sums than 2000.)
 struct AdapterWorkspace {
     int64_t sums, packed, grads, bytes;
     AdapterWorkspace(const AdapterPlanShape &p, int64_t rank, int64_t in, int64_t out) {
-        const int64_t parts = std::max(adapter_parts(p.tiles_max, in, rank),
-                                       adapter_parts(p.tiles_max, out, rank));
-        sums = (parts * p.rows * rank * 4 + 255) / 256 * 256;
+        sums = (sum_rows(p.rows, in, out) * rank * 4 + 255) / 256 * 256;
         packed = 2 * p.tiles_max * kAdapterTile * adapter_padded_rank(rank) *
                  kAdapterGradParts * 2;
-        grads = adapter_slots(p, adapter_chunk(p.tiles_max, rank, in, out)) * rank * (in + out) * 4;
+        grads = grad_bytes(p, rank, in, out);
+        if (rank > 64) grads = std::max(grads, grad_bytes(p, 64, in, out));
         bytes = sums + packed + grads;
+    }
+
+private:
+    // Rows of sums, over all K parts: at most 16 parts or 2048 columns a part, and
+    // either one part or no more workgroups than adapter_parts aims at, of 32 rows
+    // (64 at rank 128).
+    static int64_t sum_rows(int64_t rows, int64_t in, int64_t out) {
+        const int64_t C = std::max(in, out);
+        const int64_t parts = std::max<int64_t>({1, std::min<int64_t>(C / 256, 16), C / 2048});
+        return std::max(rows, std::min(rows * parts, kAdapterSumRows));
+    }
+    // As adapter_slots: ceil(tiles / chunk) is at most the chunks aimed at, and
+    // at most the tiles.
+    static int64_t grad_bytes(const AdapterPlanShape &p, int64_t rank, int64_t in, int64_t out) {
+        const int64_t slots = std::min(p.tiles_max, adapter_chunks(rank, in, out)) +
+                              std::min(p.adapters, p.rows);
+        return slots * rank * (in + out) * 4;
     }
 };
 

@@ -707,7 +707,8 @@ int fp8_adapter_plan(const int32_t *row_adapter, int64_t rows, int32_t adapters,
                      int64_t plan_bytes, fp8_stream_t stream);
 
 /* Device workspace (bytes) of either call below; a negative status for sizes
- * out of range. */
+ * out of range.  More rows, adapters or ranks never ask for less, so the
+ * workspace of a program's largest batch serves all of its batches. */
 int64_t fp8_adapter_workspace_bytes(int64_t rows, int32_t adapters, int32_t rank, int64_t in,
                                     int64_t out);
 

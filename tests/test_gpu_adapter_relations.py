@@ -5,7 +5,7 @@ import torch
 
 import delayed_scaling_linear_amd as dsl
 from tests.gpu_util import bits16
-from tests.test_gpu_adapter import Case, _ids
+from tests.test_gpu_adapter import Case, _exact, _ids
 
 pytestmark = pytest.mark.gpu
 
@@ -53,3 +53,13 @@ def test_handles_refuse_a_type_changed_in_place():
             c.forward()
         t.data = t.data.view(was)
     c.forward()
+
+
+@pytest.mark.parametrize("rank, n", [(16, 264), (64, 2056), (128, 520)])
+def test_the_largest_batchs_workspace_serves_every_smaller_one(rank, n):
+    """Rows that the plan of K parts treats differently: one part, a few, many."""
+    whole = Case(2050, 1048, n, rank, 3, _ids(2050, 3))
+    for rows in (2018, 994, 482, 129, 33, 1):
+        c = Case(rows, 1048, n, rank, 3, _ids(rows, 3))
+        c.ws = whole.ws
+        _exact(c)
