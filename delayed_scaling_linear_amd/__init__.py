@@ -42,7 +42,8 @@ __all__ = [
     "fp8_gemm_workspace_bytes", "fp8_cast_transpose_amax_group", "CAST_GROUP_MAX",
     "Dropout", "fp8_dropout", "fp8_dropout_cast_transpose_amax",
     "Adapters", "AdapterPlan", "fp8_adapter_plan", "fp8_adapter_plan_bytes",
-    "fp8_adapter_workspace_bytes", "fp8_adapter_fwd", "fp8_adapter_backward",
+    "fp8_adapter_workspace_bytes", "fp8_adapter_fwd_workspace_bytes", "fp8_adapter_fwd",
+    "fp8_adapter_backward",
     "library_path", "lib",
 ]
 
@@ -162,8 +163,9 @@ def lib() -> ctypes.CDLL:
         ap = ctypes.POINTER(_AdaptersDesc)
         L.fp8_adapter_plan_bytes.argtypes = [i64, i32]
         L.fp8_adapter_plan_bytes.restype = i64
-        L.fp8_adapter_workspace_bytes.argtypes = [i64, i32, i32, i64, i64]
-        L.fp8_adapter_workspace_bytes.restype = i64
+        for f in (L.fp8_adapter_workspace_bytes, L.fp8_adapter_fwd_workspace_bytes):
+            f.argtypes = [i64, i32, i32, i64, i64]
+            f.restype = i64
         L.fp8_adapter_plan.argtypes = [vp, i64, i32, vp, i64, vp]
         L.fp8_adapter_fwd.argtypes = [ap, vp, i64, pp, vp, i64, vp, i64, vp, i64, i64, vp, vp, i64,
                                       vp]
@@ -743,10 +745,21 @@ def fp8_adapter_plan_bytes(rows: int, adapters: int) -> int:
 
 
 def fp8_adapter_workspace_bytes(rows: int, adapters: int, rank: int, n_in: int, n_out: int) -> int:
-    """Device workspace bytes of fp8_adapter_fwd and fp8_adapter_backward."""
+    """Device workspace bytes of fp8_adapter_fwd and fp8_adapter_backward; those
+    of a program's largest batch serve all of its batches."""
     n = lib().fp8_adapter_workspace_bytes(rows, adapters, rank, n_in, n_out)
     if n < 0:
         raise Fp8Error(n, "fp8_adapter_workspace_bytes")
+    return n
+
+
+def fp8_adapter_fwd_workspace_bytes(rows: int, adapters: int, rank: int, n_in: int,
+                                    n_out: int) -> int:
+    """What fp8_adapter_fwd, and fp8_adapter_backward without da and db, need of
+    it: all that a program keeps which does not train the adapters."""
+    n = lib().fp8_adapter_fwd_workspace_bytes(rows, adapters, rank, n_in, n_out)
+    if n < 0:
+        raise Fp8Error(n, "fp8_adapter_fwd_workspace_bytes")
     return n
 
 

@@ -98,6 +98,9 @@ inline int64_t adapter_slots(const AdapterPlanShape &p, int64_t chunk) {
 // parts, and 300 rows of one adapter need more sums than 2000.)
 struct AdapterWorkspace {
     int64_t sums, packed, grads, bytes;
+    // What a call without weight gradients is asked for: the sums alone, where the
+    // rest counts (1 MiB and more: small workspaces are one size for all calls).
+    int64_t no_grads;
     AdapterWorkspace(const AdapterPlanShape &p, int64_t rank, int64_t in, int64_t out) {
         sums = (sum_rows(p.rows, in, out) * rank * 4 + 255) / 256 * 256;
         packed = 2 * p.tiles_max * kAdapterTile * adapter_padded_rank(rank) *
@@ -105,6 +108,7 @@ struct AdapterWorkspace {
         grads = grad_bytes(p, rank, in, out);
         if (rank > 64) grads = std::max(grads, grad_bytes(p, 64, in, out));
         bytes = sums + packed + grads;
+        no_grads = std::min(bytes, std::max<int64_t>(sums, 1 << 20));
     }
 
 private:

@@ -91,11 +91,11 @@ int check_adapter_sizes(int64_t rows, int32_t adapters, int32_t rank, int64_t in
     return FP8_OK;
 }
 
-// What the two adapter calls share: the adapters, the plan, the workspace and
-// the dropout (rng null where there is none).
+// What the two adapter calls share: the adapters, the plan, the workspace (grads:
+// with weight gradients) and the dropout (rng null where there is none).
 int check_adapter(const fp8_adapters_t *w, const void *plan, int64_t plan_bytes,
                   const fp8_dropout_t *drop, int64_t rows, const void *workspace,
-                  int64_t workspace_bytes, DropoutArgs *args) {
+                  int64_t workspace_bytes, bool grads, DropoutArgs *args) {
     if (w == nullptr) return FP8_ERR_NULL;
     if (int e = check_adapter_sizes(rows, w->count, w->rank, w->in, w->out)) return e;
     *args = {nullptr, 0, 1.0f};
@@ -107,8 +107,9 @@ int check_adapter(const fp8_adapters_t *w, const void *plan, int64_t plan_bytes,
     if (!aligned16(w->a) || !aligned16(w->b) || (reinterpret_cast<uintptr_t>(w->alpha) & 3) != 0 ||
         !aligned16(plan) || !aligned16(workspace))
         return FP8_ERR_ALIGN;
+    const AdapterWorkspace need(AdapterPlanShape(rows, w->count), w->rank, w->in, w->out);
     if (plan_bytes < fp8_adapter_plan_bytes(rows, w->count) ||
-        workspace_bytes < fp8_adapter_workspace_bytes(rows, w->count, w->rank, w->in, w->out))
+        workspace_bytes < (grads ? need.bytes : need.no_grads))
         return FP8_ERR_SHAPE;
     return FP8_OK;
 }
@@ -517,12 +518,19 @@ int64_t fp8_adapter_workspace_bytes(int64_t rows, int32_t adapters, int32_t rank
     return AdapterWorkspace(AdapterPlanShape(rows, adapters), rank, in, out).bytes;
 }
 
+int64_t fp8_adapter_fwd_workspace_bytes(int64_t rows, int32_t adapters, int32_t rank, int64_t in,
+                                        int64_t out) {
+    if (int e = check_adapter_sizes(rows, adapters, rank, in, out)) return e;
+    return AdapterWorkspace(AdapterPlanShape(rows, adapters), rank, in, out).no_grads;
+}
+
 int fp8_adapter_fwd(const fp8_adapters_t *w, const void *plan, int64_t plan_bytes,
                     const fp8_dropout_t *drop, const uint16_t *x, int64_t ldx,
                     const uint16_t *base, int64_t ldbase, uint16_t *y, int64_t ldy, int64_t rows,
                     float *h, void *workspace, int64_t workspace_bytes, fp8_stream_t stream) {
     DropoutArgs args;
-    if (int e = check_adapter(w, plan, plan_bytes, drop, rows, workspace, workspace_bytes, &args))
+    if (int e = check_adapter(w, plan, plan_bytes, drop, rows, workspace, workspace_bytes, false,
+                              &args))
         return e;
     if (bad_stride(ldx, w->in) || bad_stride(ldy, w->out) ||
         (base && bad_stride(ldbase, w->out)))
@@ -543,7 +551,8 @@ int fp8_adapter_backward(const fp8_adapters_t *w, const void *plan, int64_t plan
                          int64_t rows, void *da, void *db, int32_t out_dtype, void *workspace,
                          int64_t workspace_bytes, fp8_stream_t stream) {
     DropoutArgs args;
-    if (int e = check_adapter(w, plan, plan_bytes, drop, rows, workspace, workspace_bytes, &args))
+    if (int e = check_adapter(w, plan, plan_bytes, drop, rows, workspace, workspace_bytes,
+                              da != nullptr || db != nullptr, &args))
         return e;
     if (out_dtype != FP8_DTYPE_FP32 && out_dtype != FP8_DTYPE_BF16) return FP8_ERR_ARG;
     if ((da == nullptr) != (db == nullptr)) return FP8_ERR_ARG;

@@ -708,9 +708,15 @@ int fp8_adapter_plan(const int32_t *row_adapter, int64_t rows, int32_t adapters,
 
 /* Device workspace (bytes) of either call below; a negative status for sizes
  * out of range.  More rows, adapters or ranks never ask for less, so the
- * workspace of a program's largest batch serves all of its batches. */
+ * workspace of a program's largest batch serves all of its batches.
+ *
+ * The second is what fp8_adapter_fwd, and fp8_adapter_backward without weight
+ * gradients (da and db NULL), need of it: a program that does not train the
+ * adapters, serving them or passing a gradient through them, keeps no more. */
 int64_t fp8_adapter_workspace_bytes(int64_t rows, int32_t adapters, int32_t rank, int64_t in,
                                     int64_t out);
+int64_t fp8_adapter_fwd_workspace_bytes(int64_t rows, int32_t adapters, int32_t rank, int64_t in,
+                                        int64_t out);
 
 /*
  * fp8_adapter_fwd -- y = base + the adapters' forward.
@@ -725,7 +731,7 @@ int64_t fp8_adapter_workspace_bytes(int64_t rows, int32_t adapters, int32_t rank
  *           Rows without an adapter: y = base.
  * h         device fp32 [rows, rank], 16-byte aligned, for the backward, or
  *           NULL.  Rows without an adapter: 0.
- * workspace device, 16-byte aligned, at least fp8_adapter_workspace_bytes;
+ * workspace device, 16-byte aligned, at least fp8_adapter_fwd_workspace_bytes;
  *           its contents on entry do not matter and on return are
  *           unspecified; calls that overlap on one workspace race.
  * Strides are multiples of 8, at least the row's length and below 2^30;
@@ -752,7 +758,8 @@ int fp8_adapter_fwd(const fp8_adapters_t *w, const void *plan, int64_t plan_byte
  *           (FP8_DTYPE_FP32 or FP8_DTYPE_BF16), 16-byte aligned, overwritten;
  *           an adapter without rows gets zeros.  Both NULL: no weight
  *           gradients (x and h are not read).
- * workspace as the forward's.  rows 0: da and db are cleared.
+ * workspace as the forward's; with da and db at least
+ *           fp8_adapter_workspace_bytes.  rows 0: da and db are cleared.
  * Errors: those of fp8_adapter_fwd; FP8_ERR_ARG also for another out_dtype and
  * for one of da, db alone.
  */

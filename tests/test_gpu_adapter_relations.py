@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import delayed_scaling_linear_amd as dsl
-from tests.gpu_util import bits16
+from tests.gpu_util import DEV, bits16
 from tests.test_gpu_adapter import Case, _exact, _ids
 
 pytestmark = pytest.mark.gpu
@@ -63,3 +63,27 @@ def test_the_largest_batchs_workspace_serves_every_smaller_one(rank, n):
         c = Case(rows, 1048, n, rank, 3, _ids(rows, 3))
         c.ws = whole.ws
         _exact(c)
+
+
+@pytest.mark.parametrize("rows, count, rank, k, n", [(512, 512, 64, 1048, 1032), (300, 3, 128, 2056, 264),
+                                                     (2050, 4, 40, 136, 2048), (20, 2, 8, 4096, 72)])
+def test_the_forwards_own_workspace_is_all_that_it_writes(rows, count, rank, k, n):
+    """Forward and data gradient in their own workspace, its surroundings watched."""
+    c = Case(rows, k, n, rank, count, _ids(rows, count), p=0.5)
+    y, h = c.forward()
+    dx = c.backward()[0]
+    size = dsl.fp8_adapter_fwd_workspace_bytes(rows, count, rank, k, n)
+    room = torch.full((size + 8192,), 0xFF, dtype=torch.uint8, device=DEV)
+    ws = room[4096:4096 + size]
+    y2, y3, h2, dx2 = (torch.empty_like(t) for t in (y, y, h, dx))
+    x, base, dy, dx_base = (c.dev(t) for t in (c.x, c.base, c.dy, c.dx_base))
+    dsl.fp8_adapter_fwd(c.w, c.plan, x, base, y2, h=h2, drop=c.drop, workspace=ws)
+    dsl.fp8_adapter_fwd(c.w, c.plan, x, base, y3, drop=c.drop, workspace=ws)
+    dsl.fp8_adapter_backward(c.w, c.plan, None, dy, dx_base=dx_base, dx=dx2, drop=c.drop, workspace=ws)
+    for got, want in ((y2, y), (y3, y), (h2, h), (dx2, dx)):
+        assert torch.equal(got, want)
+    assert (room[:4096] == 0xFF).all() and (room[4096 + size:] == 0xFF).all()
+    da, db = torch.empty(c.a.shape, device=DEV), torch.empty(c.b.shape, device=DEV)
+    if size < dsl.fp8_adapter_workspace_bytes(rows, count, rank, k, n):
+        with pytest.raises(dsl.Fp8Error):
+            dsl.fp8_adapter_backward(c.w, c.plan, x, dy, h, da=da, db=db, drop=c.drop, workspace=ws)
