@@ -84,6 +84,15 @@ inline int64_t adapter_chunk(int64_t tiles, int64_t rank, int64_t in, int64_t ou
     return std::max<int64_t>(1, (tiles + chunks - 1) / chunks);
 }
 
+// Tiles of one expand workgroup: more where its weights (2 rank bytes a column)
+// weigh more against a tile's base and output (128 bytes a column), while
+// enough workgroups are left.
+inline int64_t adapter_expand_chunk(int64_t tiles, int64_t C, int64_t rank) {
+    if (rank <= 32) return 1;
+    const int64_t blocks = (C + kAdapterCols - 1) / kAdapterCols;
+    return std::max<int64_t>(1, std::min(rank / 12, (tiles * blocks + 1023) / 1024));
+}
+
 // Partial sums of the weight gradients: one per (chunk of tiles, adapter
 // with rows in it); chunk + rank of the adapter is distinct for each.
 inline int64_t adapter_slots(const AdapterPlanShape &p, int64_t chunk) {

@@ -1314,14 +1314,6 @@ hipError_t by_rank(int rank, F f) {
     return hipGetLastError();
 }
 
-// Tiles of one expand workgroup: more where its weights (2 rank bytes a column)
-// weigh more against a tile's base and output (128 bytes a column), while
-// enough workgroups are left.
-int64_t expand_chunk(int64_t tiles, int64_t blocks, int64_t rank) {
-    if (rank <= 32) return 1;
-    return std::max<int64_t>(1, std::min(rank / 12, (tiles * blocks + 1023) / 1024));
-}
-
 int64_t part_columns(int64_t C, int parts) { return ((C + parts - 1) / parts + 63) / 64 * 64; }
 
 template <bool TRANS>
@@ -1359,7 +1351,7 @@ hipError_t launch_expand(const AdapterArgs &w, const AdapterPlanShape &shape, co
     const PlanView v = view_of(shape, plan);
     return by_rank(w.rank, [&](auto rp) {
         const int64_t blocks = (C + kAdapterCols - 1) / kAdapterCols;
-        const int64_t chunk = expand_chunk(shape.tiles_max, blocks, w.rank);
+        const int64_t chunk = adapter_expand_chunk(shape.tiles_max, C, w.rank);
         PackArgs packing = pack;
         packing.rows = pack.g.packed ? (shape.tiles_max + blocks - 1) / blocks : 0;
         // Without an output only the packing is done.
