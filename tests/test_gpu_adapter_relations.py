@@ -87,3 +87,16 @@ def test_the_forwards_own_workspace_is_all_that_it_writes(rows, count, rank, k, 
     if size < dsl.fp8_adapter_workspace_bytes(rows, count, rank, k, n):
         with pytest.raises(dsl.Fp8Error):
             dsl.fp8_adapter_backward(c.w, c.plan, x, dy, h, da=da, db=db, drop=c.drop, workspace=ws)
+
+
+@pytest.mark.parametrize("rows, rank", [(40, 16), (200, 40)])
+def test_an_infinite_row_is_infinite_or_nan_everywhere_and_alone(rows, rank):
+    """One launch and two: x = inf meets weights of -1, 0 and 1, so every h and
+    y of its row is lost, and no other row's."""
+    c = Case(rows, 72, 88, rank, 2, [0, 1] * (rows // 2))
+    y, h = c.forward()
+    c.x[5] = float("inf")
+    yi, hi = c.forward()
+    assert not torch.isfinite(hi[5]).any() and not torch.isfinite(yi[5]).any()
+    others = [r for r in range(rows) if r != 5]
+    assert torch.equal(hi[others], h[others]) and torch.equal(yi[others], y[others])
