@@ -688,7 +688,9 @@ def fp8_dropout_cast_transpose_amax(x: torch.Tensor, drop: Dropout, scale: torch
 @dataclass(frozen=True)
 class Adapters:
     """Low-rank adapters of one linear: a [count, rank, in] and b [count, out,
-    rank] (bf16) and each adapter's factor alpha [count] (fp32)."""
+    rank] (bf16) and each adapter's factor alpha [count] (fp32).  rank is 8, 16
+    .. 128; adapters of lower ranks are padded with zeros in a's rows and b's
+    columns, whose gradients are zero."""
     a: torch.Tensor
     b: torch.Tensor
     alpha: torch.Tensor

@@ -671,6 +671,12 @@ int fp8_linear_wgrad_ws(const fp8_tensor_t *dy, const fp8_tensor_t *x, void *dw,
  * the sizes, whatever the other rows ask for.  Repeated calls give identical
  * bits.  An infinity that meets h or g in a product over `rank` or over the
  * rows gives an infinity or a NaN.
+ *
+ * All adapters of a call have one rank, a multiple of 8.  Lower ranks are padded
+ * with zeros, in the rows of A_a and the columns of B_a: finite results do not
+ * change, and the padding's gradients are zero, so it stays zero in training.
+ * A rank above FP8DSL_ADAPTER_RANK_MAX is taken in pieces, one call each, every
+ * call's base (dx_base) being the call before's y (dx), rounded to bf16.
  */
 typedef struct fp8_adapters {
     const uint16_t *a;      /* device bf16 [count, rank, in], 16-byte aligned  */

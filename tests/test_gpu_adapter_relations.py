@@ -5,7 +5,7 @@ import torch
 
 import delayed_scaling_linear_amd as dsl
 from tests.gpu_util import DEV, bits16
-from tests.test_gpu_adapter import Case, _exact, _ids
+from tests.test_gpu_adapter import Case, _exact, _ids, _same_bf16
 
 pytestmark = pytest.mark.gpu
 
@@ -100,3 +100,32 @@ def test_an_infinite_row_is_infinite_or_nan_everywhere_and_alone(rows, rank):
     assert not torch.isfinite(hi[5]).any() and not torch.isfinite(yi[5]).any()
     others = [r for r in range(rows) if r != 5]
     assert torch.equal(hi[others], h[others]) and torch.equal(yi[others], y[others])
+
+
+@pytest.mark.parametrize("rows", [20, 300])
+def test_lower_ranks_padded_with_zeros(rows):
+    """Adapters of rank 4, 12 and 16 in one call of rank 16: the results of their
+    own ranks, and zero gradients for the padding."""
+    c = Case(rows, 136, 264, 16, 3, _ids(rows, 3), p=0.5)
+    for i, rank in enumerate((4, 12, 16)):
+        c.a[i, rank:] = 0
+        c.b[i, :, rank:] = 0
+        c.h[c.ids == i, rank:] = 0
+    c.w = dsl.Adapters(c.dev(c.a), c.dev(c.b), c.dev(c.alpha))
+    _exact(c)
+    _, h = c.forward()
+    _, da, db = c.backward()
+    for i, rank in enumerate((4, 12, 16)):
+        assert (h.cpu()[c.ids == i, rank:] == 0).all()
+        assert (da[i, rank:] == 0).all() and (db[i, :, rank:] == 0).all()
+
+
+def test_a_rank_above_the_most_in_two_calls():
+    """Rank 160 as 128 and 32, the second onto what the first wrote."""
+    first, second = (Case(90, 136, 264, rank, 3, _ids(90, 3), seed=rank) for rank in (128, 32))
+    x, y = first.dev(first.x), torch.empty(90, 264, dtype=torch.bfloat16, device=DEV)
+    dsl.fp8_adapter_fwd(first.w, first.plan, x, first.dev(first.base), y, workspace=first.ws)
+    _same_bf16(y, first.want_forward()[0])
+    second.x, second.base = first.x, y.cpu()
+    dsl.fp8_adapter_fwd(second.w, second.plan, x, y, y, workspace=second.ws)
+    _same_bf16(y, second.want_forward()[0])
