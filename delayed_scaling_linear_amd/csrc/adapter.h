@@ -55,12 +55,26 @@ inline int64_t adapter_padded_rank(int64_t rank) {
 // of rank 128) of the shrink kernel.
 //   Fewer tiles than CUs: a workgroup per CU, each at least 256 columns, at most
 //   16.
-//   Else as many as are resident at once, if each keeps 2048 columns: over 8192
-//   columns of dy, 257 tiles, 3 parts take 55 us against 68 at rank 64 and 2
-//   take 41 against 49 at rank 32; rank 16 is bound by dy itself (35 us either
-//   way).  Over 2048 columns parts measured no faster, and each is one more
-//   read of the sums for the kernels behind (expand at rank 64: 61 us with one
-//   part, 67 with three).
+//   Else up to `resident` workgroups, if each keeps 2048 columns.  A CU holds two
+//   (512 in all), from rank 33 to 64 three (768); `resident` is a little more, so
+//   that the few tiles that the adapters' ends add to a full batch take no part
+//   away.  A forward of 8192 rows from 8192 columns to 2048, us by parts (* the
+//   rule's):
+//                              1     2     3     4
+//     rank 16, 257 tiles      41*   45    49    49
+//              265 tiles      56*   52    52    51
+//     rank 32, 257 tiles      44    48*   51    54
+//              265 tiles      62*   57    56    55
+//     rank 64, 257 tiles      63    58    61*   65
+//              265 tiles      81    72    72*   72
+//     rank 128, 257 tiles    105   108    93    85*
+//               265 tiles    114   123   111*  117
+//               388 tiles    120   136*  129   132
+//   (257: one adapter, exactly 256 tiles with rows; 265: nine, a few more than one a
+//   CU.)  So it pays from rank 33 on while tiles are few more than CUs.  It costs a
+//   tenth at rank 32 with 257 to 260 tiles; at rank 128 with more than 270 an
+//   eighth, and over 40 adapters (295 tiles) 157 us against 122.  Over 2048 columns
+//   parts measured no faster (rank 64, 260 tiles: 65 us, 69 with two).
 inline int adapter_parts(int64_t tiles, int64_t C, int64_t rank) {
     const int64_t groups = std::max<int64_t>(1, rank > 64 ? (tiles + 1) / 2 : tiles);
     const int64_t resident = rank <= 16 ? 256 : rank <= 32 || rank > 64 ? 520 : 800;

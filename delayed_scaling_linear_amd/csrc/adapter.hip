@@ -27,11 +27,12 @@
 // Dropout multiplies by the mask on the operand (exact) and by f in fp32 on
 // the sums.
 //
-// Measured on MI355X, where a large copy moves 5.1 TB/s (us of a whole call,
-// and in brackets its bytes at that rate): 8192 rows of 2048 -> 6144, rank 64,
-// nine requests 65 (47); 2048 -> 8192, rank 16 with dropout, forward 64 (59),
-// backward 90 (46, reading dy once; it is read twice); 16384 rows of 8192 ->
-// 2048, rank 128, backward 320 (178).
+// Measured on MI355X, where a large copy moves 5.1 TB/s (us of a whole call on
+// inputs that are not in the caches, and in brackets its bytes at that rate): 8192
+// rows of 2048 -> 6144, rank 64, nine requests 66 to 70 (47); 2048 -> 8192, rank
+// 16 with dropout, forward 66 (59), backward 92 to 94 (46, reading dy once; it is
+// read twice); 16384 rows of 8192 -> 2048, rank 128, backward 324 to 343 over
+// several cards (178).
 #include "adapter.h"
 
 #include "fp8dsl_internal.h"
@@ -324,11 +325,14 @@ static_assert(shrink_wave_pieces(128) * 16 >= 16 * 128 * 4 &&
 //   TRANS false, W [R, C] (A in the forward): staged as x is.
 //   TRANS true, W [C, R] (B in the backward): a lane reads V ranks of 8 columns
 //   and turns them in registers.
-// Bound by reading x at low rank: dy [8192, 8192] at rank 16 28 us (134 MB, 4.8
-// TB/s; a library maximum over as much reads 3.0).  From rank 32 on the weights,
-// read again by each tile, and the latency of a wave's steps count: 39 us at rank
-// 32, 54 at 64; x [8192, 2048] at rank 64 17 us; [16384, 2048] at rank 128 52 (as
-// long with one tile a workgroup or steps of 64 columns).
+// Bound by reading x at low rank: dy [8192, 8192] at rank 16 30 us (134 MB, 4.5
+// TB/s; a library maximum over as much reads 3.0).  Workgroups that begin at
+// different steps, against the memory channels that rows a multiple of 4 KiB apart
+// share, take 28, but a row's sums then follow from the tile that it is in; two
+// starting points over two sums gain nothing.  From rank 32 on the weights, read
+// again by each tile, and the latency of a wave's steps count: 39 us at rank 32, 47
+// at 64, 51 at 128; x [8192, 2048] at rank 64 17 us; [16384, 2048] at rank 128 52
+// (as long with one tile a workgroup or steps of 64 columns).
 template <int RP, bool TRANS, bool DROP>
 __global__ __launch_bounds__(shrink_threads(RP), 2) void adapter_shrink_kernel(
     PlanView plan, int tiles_max, const uint16_t *__restrict__ src, uint32_t ld, int64_t C,
@@ -644,8 +648,8 @@ struct PackArgs {
 // and output).  A wave keeps the weights of its columns while its tiles' adapter
 // stays the same.
 // Bound by base and output: [8192, 8192] at rank 16 49 us (268 MB, 5.5 TB/s),
-// [8192, 6144] at rank 64 48 (201 MB, 4.2 TB/s).  [16384, 8192] at rank 128 135
-// (537 MB, 4.0 TB/s): there the two bf16 parts' 69 GFLOP take a fifth of the
+// [8192, 6144] at rank 64 48 (201 MB, 4.2 TB/s).  [16384, 8192] at rank 128 137 to
+// 143 (537 MB, 3.8 TB/s): there the two bf16 parts' 69 GFLOP take a fifth of the
 // cycles and the vector work of a tile (h's split, addresses, sums) a third.
 template <int RP, bool TRANS, bool DROP>
 __global__ __launch_bounds__(expand_threads(RP), 2) void adapter_expand_kernel(
@@ -1085,9 +1089,10 @@ constexpr int wgrad_threads(int rp) { return kAdapterCols / wgrad_lane_cols(rp) 
 // wave's 16 L); the short operand comes through LDS, once for the workgroup.
 // The next tile's loads of both are in flight while the current one is
 // multiplied.
-// Bound by x and dy at low rank: [8192, 2048 + 8192] at rank 16 39 us (168 MB,
-// 4.3 TB/s); at rank 64 70, bf16 results alike.  At rank 128, [16384, 2048 + 8192], 146 us: three bf16 parts
-// make 129 GFLOP of 43, 0.88 PFLOP/s where a large library product reaches 1.24.
+// Bound by x and dy at low rank: [8192, 2048 + 8192] at rank 16 40 us (168 MB,
+// 4.2 TB/s), at rank 32 45, at rank 64 62 (10 registers spill, 16 with dropout).  At
+// rank 128, [16384, 2048 + 8192], 144 to 155 us: three bf16 parts make 129 GFLOP of
+// 43, 0.83 to 0.89 PFLOP/s where a large library product reaches 1.24.
 template <int RP, bool DROP>
 __global__ __launch_bounds__(wgrad_threads(RP), 2) void adapter_wgrad_kernel(
     PlanView plan, WgradSide left, WgradSide right, int left_blocks, int R, int chunk,
@@ -1189,7 +1194,7 @@ __global__ __launch_bounds__(wgrad_threads(RP), 2) void adapter_wgrad_kernel(
                                    ? high_halves(in[2 * d].d[t >> 1], in[2 * d + 1].d[t >> 1])
                                    : low_halves(in[2 * d].d[t >> 1], in[2 * d + 1].d[t >> 1]);
             // The operands are read two steps ahead of their use (a rank block ahead
-            // takes twice the registers: at rank 64 84 us against 70).
+            // takes twice the registers and at rank 64 a fifth longer).
             constexpr int STEPS = J * PARTS, RING = 3;
             auto operand = [&](int q) { return hs[buf][(q % PARTS * J + q / PARTS) * 64 + lane]; };
             u32x4 b[RING];
@@ -1373,11 +1378,17 @@ hipError_t launch_expand(const AdapterArgs &w, const AdapterPlanShape &shape, co
 
 // Whether the forward runs in one launch (adapter_small_kernel).  Its column
 // blocks read each tile's A again, 16 rows at a time.  Measured against the two
-// launches (in a graph, us): A of 32 or 64 KiB 5.2 against 7.0 (one token), 7.0
-// against 8.2 (64 tokens over 32 adapters, 8 MiB of A read in all), 10.7 against
-// 9.7 (33 MiB, where the launch saved, 3 us of the host's time, still makes an
-// ungraphed call faster); A of 128 KiB level up to 17 MiB, of 256 KiB a third
-// slower; 64 rows an adapter a third slower from 128 KiB on.
+// launches (us, in a graph and, in brackets, of an eager call):
+//   A of 64 KiB, one token                           5.7 : 7.3   (10.5 : 13.4)
+//   64 tokens, 32 adapters, 8 MiB of A read in all   6.5 : 7.9   (10.7 : 13.6)
+//     16.5 MiB                                       6.6 : 7.9   (10.2 : 13.2)
+//     33 MiB                                         9.7 : 9.2   (10.7 : 13.3)
+//   64 tokens, 64 adapters, 64 MiB                  14.4 : 10.2  (14.8 : 13.5)
+//   A of 128 KiB, 8 adapters, 4.5 MiB                8.5 : 8.6   (10.6 : 13.4)
+//     20 MiB                                         9.1 : 8.9   (10.4 : 13.2)
+// A bound of 34 MiB takes what an eager call gains, 3 us of the host's time for the
+// launch saved, against 0.5 that a graph loses between 17 and 34 MiB.  A of 256 KiB
+// is a third slower, and so are 64 rows an adapter from 128 KiB on.
 bool one_launch(const AdapterArgs &w, const AdapterPlanShape &shape) {
     const int64_t blocks = (w.out + kAdapterCols - 1) / kAdapterCols;
     const int64_t a_bytes = adapter_padded_rank(w.rank) * w.in * 2;

@@ -895,8 +895,8 @@ hipError_t launch_produce_op_fmt(const uint16_t *x, int64_t ldx, const uint16_t 
 // once, past the last-level cache, which keeps the codes for the products.
 // Bound by its bytes: [8192, 2048] with a residual to E4M3 28 us (134 MB, 4.8
 // TB/s; 31 us with ordinary loads; a copy of as much 26), the gradient
-// [8192, 8192] to E5M2 with its column sums 60 us (268 MB, 4.5 TB/s) and 4.8 for
-// the sums of the tile rows.
+// [8192, 8192] to E5M2 with its column sums 61 to 63 us (268 MB, 4.3 TB/s) and 5
+// for the sums of the tile rows.
 template <int FMT, bool WANT_Q, bool WANT_QT, bool DBIAS>
 __global__ __launch_bounds__(THREADS) void dropout_cast_kernel(
     const uint16_t *x, int64_t ldx, const uint16_t *res, int64_t ldres, uint16_t *y, int64_t ldy,
