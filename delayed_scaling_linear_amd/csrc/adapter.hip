@@ -1366,8 +1366,9 @@ hipError_t launch_expand(const AdapterArgs &w, const AdapterPlanShape &shape, co
             hipLaunchKernelGGL((adapter_expand_kernel<decltype(rp)::value, TRANS,
                                                       decltype(dropped)::value>),
                                grid, dim3(expand_threads(decltype(rp)::value)), 0, stream, v,
-                               (int)shape.tiles_max, (int)chunk, h, parts, shape.rows * w.rank, TRANS ? w.a : w.b, w.rank, C, base,
-                               row_bytes(ldbase), out, row_bytes(ldo), h_out, packing, drop);
+                               (int)shape.tiles_max, (int)chunk, h, parts, shape.rows * w.rank,
+                               TRANS ? w.a : w.b, w.rank, C, base, row_bytes(ldbase), out,
+                               row_bytes(ldo), h_out, packing, drop);
         };
         if constexpr (TRANS) {
             if (drop.rng) return go(std::true_type{});
