@@ -19,6 +19,10 @@ The pieces, with the pages that define them:
   FP8 Layers" (history 16, "max").
 * ``fp8_cast_transpose_amax``, ``fp8_scale_update``, ``fp8_linear_fwd``,
   ``fp8_linear_dgrad``, ``fp8_linear_wgrad`` -- the C entry points.
+
+Beside them, on no page: :class:`Dropout`, :class:`Adapters`,
+:class:`ExpertPlan` (tokens sorted by expert and back) and :class:`AdamW`, with
+the entry points that take them.
 """
 from __future__ import annotations
 
@@ -44,6 +48,11 @@ __all__ = [
     "Adapters", "AdapterPlan", "fp8_adapter_plan", "fp8_adapter_plan_bytes",
     "fp8_adapter_workspace_bytes", "fp8_adapter_fwd_workspace_bytes", "fp8_adapter_fwd",
     "fp8_adapter_backward",
+    "ExpertPlan", "fp8_expert_rows", "fp8_expert_plan_bytes", "fp8_expert_plan",
+    "fp8_expert_gather", "fp8_expert_gather_cast_transpose_amax", "fp8_expert_combine",
+    "fp8_expert_combine_backward",
+    "AdamW", "AdamWTensor", "ADAMW_BLOCK", "fp8_adamw_step", "fp8_grad_norm",
+    "fp8_grad_norm_workspace_bytes",
     "library_path", "lib",
 ]
 
@@ -57,6 +66,7 @@ PRODUCE_ADD2 = 3
 PRODUCE_MODULATE_FINITE = 4      # the library's addition: non-finite quotients -> +0
 NOALLOC_SCRATCH_BYTES = 4 << 20     # FP8DSL_NOALLOC_SCRATCH_BYTES
 CAST_GROUP_MAX = 8                  # FP8DSL_CAST_GROUP_MAX
+ADAMW_BLOCK = 256                   # FP8DSL_ADAMW_BLOCK
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 library_path = os.path.join(_PKG, "libfp8dsl.so")
@@ -116,6 +126,66 @@ class _AdaptersDesc(ctypes.Structure):
     ]
 
 
+class _ExpertSizes(ctypes.Structure):
+    """Mirror of fp8_expert_sizes_t."""
+    _fields_ = [
+        ("tokens", ctypes.c_int64),
+        ("capacity", ctypes.c_int64),
+        ("top_k", ctypes.c_int32),
+        ("experts", ctypes.c_int32),
+    ]
+
+
+class _ExpertLayout(ctypes.Structure):
+    """Mirror of fp8_expert_layout_t."""
+    _fields_ = [
+        ("offsets", ctypes.c_int64),
+        ("counts", ctypes.c_int64),
+        ("slots", ctypes.c_int64),
+        ("sources", ctypes.c_int64),
+    ]
+
+
+class _GradDesc(ctypes.Structure):
+    """Mirror of fp8_grad_t."""
+    _fields_ = [
+        ("grad", ctypes.c_void_p),
+        ("n", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
+class _AdamWTensorDesc(ctypes.Structure):
+    """Mirror of fp8_adamw_tensor_t."""
+    _fields_ = [
+        ("param", ctypes.c_void_p),
+        ("grad", ctypes.c_void_p),
+        ("m", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("m_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p),
+        ("copy", ctypes.c_void_p),
+        ("n", ctypes.c_int64),
+        ("weight_decay", ctypes.c_float),
+        ("param_dtype", ctypes.c_int32),
+        ("grad_dtype", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
+class _AdamWDesc(ctypes.Structure):
+    """Mirror of fp8_adamw_t."""
+    _fields_ = [
+        ("lr", ctypes.c_void_p),
+        ("steps", ctypes.c_void_p),
+        ("beta1", ctypes.c_double),
+        ("beta2", ctypes.c_double),
+        ("eps", ctypes.c_double),
+        ("seed", ctypes.c_uint64),
+    ]
+
+
 _lib: Optional[ctypes.CDLL] = None
 
 
@@ -171,6 +241,28 @@ def lib() -> ctypes.CDLL:
                                       vp]
         L.fp8_adapter_backward.argtypes = [ap, vp, i64, pp, vp, i64, vp, i64, vp, vp, i64, vp, i64,
                                            i64, vp, vp, i32, vp, i64, vp]
+        sp = ctypes.POINTER(_ExpertSizes)
+        for f in (L.fp8_expert_rows, L.fp8_expert_plan_bytes):
+            f.argtypes = [sp]
+            f.restype = i64
+        L.fp8_expert_plan_layout.argtypes = [sp, ctypes.POINTER(_ExpertLayout)]
+        L.fp8_expert_plan.argtypes = [sp, vp, vp, i64, vp]
+        L.fp8_expert_gather.argtypes = [sp, vp, i64, vp, i64, vp, i64, i64, vp]
+        L.fp8_expert_gather_cast_transpose_amax.argtypes = [sp, vp, i64, vp, i64, i64, vp, vp, dp,
+                                                            vp, vp, vp]
+        L.fp8_expert_combine.argtypes = [sp, vp, i64, vp, i64, vp, vp, i64, vp, i64, i64, vp]
+        L.fp8_expert_combine_backward.argtypes = [sp, vp, i64, vp, i64, vp, i64, vp, vp, vp, i64,
+                                                  i64, vp]
+        L.fp8_grad_norm_workspace_bytes.argtypes = []
+        L.fp8_grad_norm_workspace_bytes.restype = i64
+        L.fp8_grad_norm.argtypes = [ctypes.POINTER(_GradDesc), i32, ctypes.c_float, vp, vp, vp, vp,
+                                    i64, vp]
+        L.fp8_adamw_step.argtypes = [ctypes.POINTER(_AdamWDesc), ctypes.POINTER(_AdamWTensorDesc),
+                                     i32, vp, vp, vp]
+        for f in (L.fp8_expert_plan_layout, L.fp8_expert_plan, L.fp8_expert_gather,
+                  L.fp8_expert_gather_cast_transpose_amax, L.fp8_expert_combine,
+                  L.fp8_expert_combine_backward, L.fp8_grad_norm, L.fp8_adamw_step):
+            f.restype = ctypes.c_int
         for f in (L.fp8_adapter_plan, L.fp8_adapter_fwd, L.fp8_adapter_backward, L.fp8_dropout,
                   L.fp8_dropout_cast_transpose_amax, L.fp8_scale_update, L.fp8_cast_transpose_amax,
                   L.fp8_cast_transpose_amax_dbias,
@@ -597,17 +689,18 @@ _NONE = (None, 0)     # pointer and stride of a matrix that is not there
 
 
 def _need_apart(y, t, rows: int, y_cols: int, t_cols: int, size: int, what: str,
-                same: bool = False) -> None:
+                same: bool = False, t_rows: Optional[int] = None) -> None:
     """Refuses an output y (pointer, stride) that overlaps the input t, unless
     it is t itself and `same` allows that.  Columns of their own in rows of one
-    stride lie apart."""
+    stride lie apart.  t has `rows` rows like y unless t_rows says otherwise."""
     yp, yld = y
     tp, tld = t
-    if yp is None or tp is None or rows == 0 or y_cols == 0 or t_cols == 0:
+    t_rows = rows if t_rows is None else t_rows
+    if yp is None or tp is None or rows == 0 or t_rows == 0 or y_cols == 0 or t_cols == 0:
         return
     if same and yp == tp and yld == tld:
         return
-    if yp >= tp + ((rows - 1) * tld + t_cols) * size:
+    if yp >= tp + ((t_rows - 1) * tld + t_cols) * size:
         return
     if tp >= yp + ((rows - 1) * yld + y_cols) * size:
         return
@@ -851,6 +944,351 @@ def fp8_adapter_backward(w: Adapters, plan: AdapterPlan, x: Optional[torch.Tenso
     _check(lib().fp8_adapter_backward(*head, *xm, *gm, _ptr(h, torch.float32, "h"), *bm, *om, rows,
                                       _ptr(da, None, "da"), _ptr(db, None, "db"), dtype, *ws,
                                       _stream(stream)), "fp8_adapter_backward")
+
+
+@dataclass
+class ExpertPlan:
+    """Where the (token, choice) pairs of a batch lie in expert order
+    (fp8_expert_plan), for the calls of a layer until it is built again.
+    `rows` is the row count of every tensor in expert order."""
+    buf: torch.Tensor
+    tokens: int
+    top_k: int
+    experts: int
+    capacity: int = 0
+    built: bool = False
+
+    def __post_init__(self):
+        self._sizes = _ExpertSizes(self.tokens, self.capacity, self.top_k, self.experts)
+        self.rows = fp8_expert_rows(self.tokens, self.top_k, self.experts, self.capacity)
+        self._layout = _ExpertLayout()
+        _check(lib().fp8_expert_plan_layout(ctypes.byref(self._sizes),
+                                            ctypes.byref(self._layout)), "fp8_expert_plan_layout")
+
+    @staticmethod
+    def empty(tokens: int, top_k: int, experts: int, capacity: int = 0,
+              device="cuda") -> "ExpertPlan":
+        n = fp8_expert_plan_bytes(tokens, top_k, experts, capacity)
+        return ExpertPlan(torch.empty(n, dtype=torch.uint8, device=device), tokens, top_k, experts,
+                          capacity)
+
+    def _words(self, at: int, count: int) -> torch.Tensor:
+        return self.buf[at:at + 4 * count].view(torch.int32)
+
+    @property
+    def offsets(self) -> torch.Tensor:
+        """[experts + 1] int32: first row of each expert's segment, and the end."""
+        return self._words(self._layout.offsets, self.experts + 1)
+
+    @property
+    def counts(self) -> torch.Tensor:
+        """[experts] int32: the pairs that each expert keeps."""
+        return self._words(self._layout.counts, self.experts)
+
+    @property
+    def slots(self) -> torch.Tensor:
+        """[tokens, top_k] int32: the row of each pair, -1 for none."""
+        n = self.tokens * self.top_k
+        return self._words(self._layout.slots, n).view(self.tokens, self.top_k)
+
+    @property
+    def sources(self) -> torch.Tensor:
+        """[rows] int32: the pair t * top_k + k of each row, -1 for none."""
+        return self._words(self._layout.sources, self.rows)
+
+    def segments(self, t: Float8Tensor, offsets=None) -> list:
+        """Each expert's rows of t (fp8_expert_gather_cast_transpose_amax) as a
+        Float8Tensor of its own, sharing memory and the scale-inverse.
+        `offsets`: the host's copy of plan.offsets, not needed with a capacity."""
+        if t.rows != self.rows:
+            raise ValueError(f"t must have {self.rows} rows, got {t.rows}")
+        if offsets is None:
+            if not self.capacity:
+                raise ValueError("offsets are needed without a capacity")
+            offsets = [e * self.capacity for e in range(self.experts + 1)]
+        flat = None if t.data_t is None else t.data_t.view(-1)
+        out = []
+        for first, end in zip(offsets, offsets[1:]):
+            first, end = int(first), int(end)
+            data_t = None if flat is None else \
+                flat[first * t.cols:end * t.cols].view(t.cols, end - first)
+            out.append(Float8Tensor(None if t.data is None else t.data[first:end], data_t,
+                                    t.scale_inv, t.fmt, end - first, t.cols))
+        return out
+
+
+def fp8_expert_rows(tokens: int, top_k: int, experts: int, capacity: int = 0) -> int:
+    """Rows of a tensor in expert order."""
+    n = lib().fp8_expert_rows(ctypes.byref(_ExpertSizes(tokens, capacity, top_k, experts)))
+    if n < 0:
+        raise Fp8Error(n, "fp8_expert_rows")
+    return n
+
+
+def fp8_expert_plan_bytes(tokens: int, top_k: int, experts: int, capacity: int = 0) -> int:
+    """Device bytes of the plan of a batch."""
+    n = lib().fp8_expert_plan_bytes(ctypes.byref(_ExpertSizes(tokens, capacity, top_k, experts)))
+    if n < 0:
+        raise Fp8Error(n, "fp8_expert_plan_bytes")
+    return n
+
+
+def fp8_expert_plan(expert_ids: torch.Tensor, plan: ExpertPlan, stream=None) -> None:
+    """Build `plan` for expert_ids [tokens, top_k] (int32; any value outside
+    0 .. experts - 1 names no expert)."""
+    _need_shape(expert_ids, (plan.tokens, plan.top_k), "expert_ids")
+    ids = _ptr(expert_ids, torch.int32, "expert_ids")
+    _on_current_device(expert_ids, plan.buf)
+    _check(lib().fp8_expert_plan(ctypes.byref(plan._sizes), ids, *_ws(plan.buf), _stream(stream)),
+           "fp8_expert_plan")
+    plan.built = True
+
+
+def _expert_call(plan: ExpertPlan):
+    """The arguments that the calls with a plan begin with."""
+    if not plan.built:
+        raise ValueError("the plan has not been built (fp8_expert_plan)")
+    return (ctypes.byref(plan._sizes), *_ws(plan.buf))
+
+
+def _columns(t: torch.Tensor, what: str) -> int:
+    if t.dim() != 2:
+        raise ValueError(f"{what} must be 2-D")
+    return t.shape[1]
+
+
+def _pair_weights(weights: Optional[torch.Tensor], plan: ExpertPlan, what: str):
+    if weights is not None:
+        _need_shape(weights, (plan.tokens, plan.top_k), what)
+    return _ptr(weights, torch.float32, what)
+
+
+def fp8_expert_gather(plan: ExpertPlan, x: torch.Tensor, y: torch.Tensor, stream=None) -> None:
+    """y [plan.rows, cols] = the rows of x [tokens, cols] in expert order (bf16,
+    unit column stride); a segment's rows without a pair are zeros, rows behind
+    the last segment stay as they are.  The gradient of x is
+    fp8_expert_combine of y's without weights."""
+    cols = _columns(x, "x")
+    xm = _matrix(x, plan.tokens, cols, torch.bfloat16, "x")
+    ym = _matrix(y, plan.rows, cols, torch.bfloat16, "y")
+    head = _expert_call(plan)
+    _on_current_device(plan.buf, x, y)
+    _need_apart(ym, xm, plan.rows, cols, cols, 2, "y", t_rows=plan.tokens)
+    _check(lib().fp8_expert_gather(*head, *xm, *ym, cols, _stream(stream)), "fp8_expert_gather")
+
+
+def fp8_expert_gather_cast_transpose_amax(plan: ExpertPlan, x: torch.Tensor, scale: torch.Tensor,
+                                          out: Float8Tensor,
+                                          amax_cur: Optional[torch.Tensor] = None,
+                                          weights: Optional[torch.Tensor] = None,
+                                          noop_flag: Optional[torch.Tensor] = None,
+                                          stream=None) -> None:
+    """The rows of x [tokens, cols] (bf16), or bf16(weights * rows), in expert
+    order and cast into `out` (plan.rows rows) as fp8_cast_transpose_amax casts
+    them; out.data_t holds the segments' transposes one after another
+    (ExpertPlan.segments gives each expert its part).  weights [tokens, top_k]
+    fp32."""
+    _need_scalar(scale, "scale")
+    _need_scalar(amax_cur, "amax_cur")
+    _need_scalar(noop_flag, "noop_flag")
+    cols = _columns(x, "x")
+    xm = _matrix(x, plan.tokens, cols, torch.bfloat16, "x")
+    w = _pair_weights(weights, plan, "weights")
+    head, o = _expert_call(plan), out.desc()
+    _on_current_device(plan.buf, x, weights, scale, out.data, out.data_t, out.scale_inv, amax_cur,
+                       noop_flag)
+    _check(lib().fp8_expert_gather_cast_transpose_amax(
+        *head, *xm, cols, w, _ptr(scale, torch.float32, "scale"), ctypes.byref(o),
+        _ptr(amax_cur, torch.float32, "amax_cur"), _ptr(noop_flag, torch.int32, "noop_flag"),
+        _stream(stream)), "fp8_expert_gather_cast_transpose_amax")
+
+
+def fp8_expert_combine(plan: ExpertPlan, x: torch.Tensor, y: torch.Tensor,
+                       weights: Optional[torch.Tensor] = None,
+                       base: Optional[torch.Tensor] = None, stream=None) -> None:
+    """y [tokens, cols] = base + the sum of each token's rows of x [plan.rows,
+    cols] times weights [tokens, top_k] (fp32; None: ones).  x, y and base
+    (None: zeros) are bf16 with unit column stride; y may be base."""
+    cols = _columns(x, "x")
+    xm = _matrix(x, plan.rows, cols, torch.bfloat16, "x")
+    ym = _matrix(y, plan.tokens, cols, torch.bfloat16, "y")
+    bm = _NONE if base is None else _matrix(base, plan.tokens, cols, torch.bfloat16, "base")
+    w = _pair_weights(weights, plan, "weights")
+    head = _expert_call(plan)
+    _on_current_device(plan.buf, x, y, weights, base)
+    _need_apart(ym, xm, plan.tokens, cols, cols, 2, "y", t_rows=plan.rows)
+    _need_apart(ym, bm, plan.tokens, cols, cols, 2, "y", same=True)
+    _check(lib().fp8_expert_combine(*head, *xm, w, *bm, *ym, cols, _stream(stream)),
+           "fp8_expert_combine")
+
+
+def fp8_expert_combine_backward(plan: ExpertPlan, dy: torch.Tensor, x: torch.Tensor,
+                                dweights: torch.Tensor, weights: Optional[torch.Tensor] = None,
+                                dx: Optional[torch.Tensor] = None, stream=None) -> None:
+    """The gradients of fp8_expert_combine for dy [tokens, cols] (bf16):
+    dweights [tokens, top_k] (fp32) = the products of dy's rows with those of x,
+    and dx [plan.rows, cols] (bf16; None: not wanted, as where dy goes through
+    fp8_expert_gather_cast_transpose_amax) = weights times dy's rows in expert
+    order.  dx may be x."""
+    cols = _columns(dy, "dy")
+    gm = _matrix(dy, plan.tokens, cols, torch.bfloat16, "dy")
+    xm = _matrix(x, plan.rows, cols, torch.bfloat16, "x")
+    om = _NONE if dx is None else _matrix(dx, plan.rows, cols, torch.bfloat16, "dx")
+    if dx is not None and weights is None:
+        raise ValueError("dx needs weights")
+    w = _pair_weights(weights, plan, "weights")
+    dw = _pair_weights(dweights, plan, "dweights")
+    head = _expert_call(plan)
+    _on_current_device(plan.buf, dy, x, dweights, weights, dx)
+    if dx is not None:
+        _need_apart(om, xm, plan.rows, cols, cols, 2, "dx", same=True)
+        _need_apart(om, gm, plan.rows, cols, cols, 2, "dx", t_rows=plan.tokens)
+    _check(lib().fp8_expert_combine_backward(*head, *gm, *xm, w, dw, *om, cols, _stream(stream)),
+           "fp8_expert_combine_backward")
+
+
+_ADAMW_DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_FP32}
+
+
+@dataclass
+class AdamWTensor:
+    """One tensor of an AdamW step: param (fp32 or bf16), its gradient (either
+    type), and the moments m and v: fp32, or E4M3 codes (uint8) with a
+    power-of-two scale (fp32) per ADAMW_BLOCK values.  `copy` (bf16) is written
+    with an fp32 param's new values.  All contiguous, of one shape."""
+    param: torch.Tensor
+    grad: torch.Tensor
+    m: torch.Tensor
+    v: torch.Tensor
+    m_scale: Optional[torch.Tensor] = None
+    v_scale: Optional[torch.Tensor] = None
+    copy: Optional[torch.Tensor] = None
+    weight_decay: float = 0.0
+
+    @staticmethod
+    def zeros(param: torch.Tensor, grad: torch.Tensor, bits: int = 32, copy=None,
+              weight_decay: float = 0.0) -> "AdamWTensor":
+        """The state before the first step, with moments in 32 or 8 bits."""
+        if bits not in (8, 32):
+            raise ValueError("bits must be 8 or 32")
+        like = dict(dtype=torch.uint8 if bits == 8 else torch.float32, device=param.device)
+        m, v = (torch.zeros(param.shape, **like) for _ in range(2))
+        scales = (None, None)
+        if bits == 8:
+            blocks = (param.numel() + ADAMW_BLOCK - 1) // ADAMW_BLOCK
+            scales = tuple(torch.zeros(blocks, device=param.device) for _ in range(2))
+        return AdamWTensor(param, grad, m, v, *scales, copy=copy, weight_decay=weight_decay)
+
+    def desc(self) -> _AdamWTensorDesc:
+        """The C descriptor, checked on every call: a gradient is often another
+        tensor in the next step."""
+        p, g, m, v, copy = self.param, self.grad, self.m, self.v, self.copy
+        n, shape = p.numel(), p.shape
+        for t, what in ((p, "param"), (g, "grad")):
+            if t.dtype not in _ADAMW_DTYPES:
+                raise TypeError(f"{what} must be fp32 or bf16, got {t.dtype}")
+        state = torch.float32 if self.m_scale is None else torch.uint8
+        if (self.m_scale is None) != (self.v_scale is None):
+            raise ValueError("m_scale and v_scale come together")
+        if copy is not None and p.dtype is not torch.float32:
+            raise TypeError("a copy needs an fp32 param")
+        for t, dtype, what in ((p, None, "param"), (g, None, "grad"), (m, state, "m"),
+                               (v, state, "v"), (copy, torch.bfloat16, "copy")):
+            if t is None and what == "copy":
+                continue
+            if t.shape != shape:
+                raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+            _ptr(t, dtype, what)
+        blocks = (n + ADAMW_BLOCK - 1) // ADAMW_BLOCK
+        _need_shape(self.m_scale, (blocks,), "m_scale")
+        _need_shape(self.v_scale, (blocks,), "v_scale")
+        _on_current_device(p, g, m, v, copy, self.m_scale, self.v_scale)
+        return _AdamWTensorDesc(
+            p.data_ptr(), g.data_ptr(), m.data_ptr(), v.data_ptr(),
+            _ptr(self.m_scale, torch.float32, "m_scale"),
+            _ptr(self.v_scale, torch.float32, "v_scale"),
+            None if copy is None else copy.data_ptr(), n, self.weight_decay,
+            _ADAMW_DTYPES[p.dtype], _ADAMW_DTYPES[g.dtype], 0)
+
+
+class AdamW:
+    """AdamW over `tensors` (AdamWTensor): lr is a float or a 1-element fp32
+    device tensor (which a program changes between steps, graph replays
+    included), `steps` [1] (int64, device) the steps taken.  `seed` feeds the
+    stochastic rounding of 8-bit moments and bf16 parameters."""
+
+    def __init__(self, tensors, lr=1e-3, betas=(0.9, 0.999), eps: float = 1e-8, seed: int = 0,
+                 device="cuda"):
+        self.tensors = list(tensors)
+        self.lr = lr if isinstance(lr, torch.Tensor) else \
+            torch.full((1,), lr, dtype=torch.float32, device=device)
+        self.betas, self.eps, self.seed = betas, eps, seed
+        self._steps = torch.zeros(2, dtype=torch.int64, device=self.lr.device)
+
+    @property
+    def steps(self) -> torch.Tensor:
+        return self._steps[:1]
+
+    @property
+    def grads(self) -> list:
+        """The gradients, for fp8_grad_norm."""
+        return [t.grad for t in self.tensors]
+
+    def desc(self) -> _AdamWDesc:
+        _need_scalar(self.lr, "lr")
+        _on_current_device(self.lr, self._steps)
+        return _AdamWDesc(_ptr(self.lr, torch.float32, "lr"), self._steps.data_ptr(),
+                          self.betas[0], self.betas[1], self.eps, self.seed & (2 ** 64 - 1))
+
+    def step(self, grad_scale: Optional[torch.Tensor] = None,
+             noop_flag: Optional[torch.Tensor] = None, stream=None) -> None:
+        fp8_adamw_step(self, grad_scale=grad_scale, noop_flag=noop_flag, stream=stream)
+
+
+def fp8_grad_norm_workspace_bytes() -> int:
+    """Device workspace bytes of fp8_grad_norm."""
+    return lib().fp8_grad_norm_workspace_bytes()
+
+
+def fp8_grad_norm(grads, norm: torch.Tensor, workspace: torch.Tensor,
+                  max_norm: float = float("inf"), factor: Optional[torch.Tensor] = None,
+                  noop_flag: Optional[torch.Tensor] = None, stream=None) -> None:
+    """norm [1] (fp32) = the 2-norm of all values of `grads` (contiguous fp32 or
+    bf16 device tensors); factor [1] (fp32) = max_norm / norm where the norm is
+    larger, else 1; noop_flag [1] (int32) = 1 where the norm is not finite, else 0:
+    grad_scale and noop_flag of fp8_adamw_step."""
+    for t, what in ((norm, "norm"), (factor, "factor"), (noop_flag, "noop_flag")):
+        _need_scalar(t, what)
+    if norm is None or workspace is None:
+        raise ValueError("norm and workspace are required")
+    descs = []
+    for g in grads:
+        if g.dtype not in _ADAMW_DTYPES:
+            raise TypeError(f"grads must be fp32 or bf16, got {g.dtype}")
+        descs.append((_ptr(g, None, "grads"), g.numel(), _ADAMW_DTYPES[g.dtype], 0))
+    _on_current_device(norm, factor, noop_flag, workspace, *grads)
+    array = (_GradDesc * len(descs))(*descs)
+    _check(lib().fp8_grad_norm(array, len(descs), max_norm, _ptr(norm, torch.float32, "norm"),
+                               _ptr(factor, torch.float32, "factor"),
+                               _ptr(noop_flag, torch.int32, "noop_flag"), *_ws(workspace),
+                               _stream(stream)), "fp8_grad_norm")
+
+
+def fp8_adamw_step(opt: AdamW, grad_scale: Optional[torch.Tensor] = None,
+                   noop_flag: Optional[torch.Tensor] = None, stream=None) -> None:
+    """One step of `opt`: every tensor's param, moments and copy, and
+    opt.steps += 1.  `grad_scale` [1] (fp32) multiplies the gradients; a set
+    `noop_flag` [1] (int32) leaves everything as it is."""
+    _need_scalar(grad_scale, "grad_scale")
+    _need_scalar(noop_flag, "noop_flag")
+    descs = [t.desc() for t in opt.tensors]
+    array = (_AdamWTensorDesc * len(descs))(*descs)
+    d = opt.desc()
+    _on_current_device(grad_scale, noop_flag)
+    _check(lib().fp8_adamw_step(ctypes.byref(d), array, len(descs),
+                                _ptr(grad_scale, torch.float32, "grad_scale"),
+                                _ptr(noop_flag, torch.int32, "noop_flag"), _stream(stream)),
+           "fp8_adamw_step")
 
 
 def fp8_cast_transpose_dynamic(x: torch.Tensor, scale: torch.Tensor, out: Float8Tensor,

@@ -9,7 +9,9 @@
 #include <math.h>
 #include <string.h>
 
+#include "adamw.h"
 #include "adapter.h"
+#include "expert.h"
 #include "fp8dsl_internal.h"
 
 using namespace fp8dsl;
@@ -18,6 +20,7 @@ namespace {
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 bool valid_fmt(int32_t f) { return f == FP8_E4M3 || f == FP8_E5M2; }
+bool valid_dtype(int32_t d) { return d == FP8_DTYPE_BF16 || d == FP8_DTYPE_FP32; }
 
 // A launch on a device this library has no code object for (anything but a
 // gfx950) fails in the runtime; that is reported as FP8_ERR_DEVICE.
@@ -122,6 +125,30 @@ bool bad_stride(int64_t ld, int64_t cols) {
 
 AdapterArgs adapter_args(const fp8_adapters_t *w) {
     return {w->a, w->b, w->alpha, w->count, w->rank, w->in, w->out};
+}
+
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
+
+// Sizes of a plan of experts.
+int check_expert_sizes(const fp8_expert_sizes_t *s) {
+    if (s == nullptr) return FP8_ERR_NULL;
+    if (s->top_k < 1 || s->top_k > FP8DSL_EXPERT_TOP_K_MAX || s->experts < 1 ||
+        s->experts > kExpertsMax || s->tokens < 0 || s->tokens > ((int64_t)1 << 23) / s->top_k)
+        return FP8_ERR_SHAPE;
+    if (s->capacity < 0 || (s->capacity % 16) != 0 ||
+        s->capacity > ((int64_t)1 << 24) / s->experts)
+        return FP8_ERR_SHAPE;
+    return FP8_OK;
+}
+
+// What the calls that use such a plan share.
+int check_expert(const fp8_expert_sizes_t *sizes, const void *plan, int64_t plan_bytes,
+                 int64_t cols) {
+    if (int e = check_expert_sizes(sizes)) return e;
+    if (cols < 0 || cols > ((int64_t)1 << 22) || (cols % 8) != 0) return FP8_ERR_SHAPE;
+    if (plan == nullptr) return FP8_ERR_NULL;
+    if (!aligned16(plan)) return FP8_ERR_ALIGN;
+    return plan_bytes < fp8_expert_plan_bytes(sizes) ? FP8_ERR_SHAPE : FP8_OK;
 }
 
 // Scratch of fp8_cast_transpose_amax_dbias_noalloc: each GPU holds its own
@@ -576,6 +603,169 @@ int fp8_adapter_backward(const fp8_adapters_t *w, const void *plan, int64_t plan
                                              static_cast<const int32_t *>(plan), args, x, ldx, dy,
                                              lddy, h, dx_base, lddxbase, dx, lddx, da, db,
                                              out_dtype, workspace, s));
+}
+
+int64_t fp8_expert_rows(const fp8_expert_sizes_t *sizes) {
+    if (int e = check_expert_sizes(sizes)) return e;
+    return ExpertShape(*sizes).rows;
+}
+
+int64_t fp8_expert_plan_bytes(const fp8_expert_sizes_t *sizes) {
+    if (int e = check_expert_sizes(sizes)) return e;
+    return ExpertShape(*sizes).words * (int64_t)sizeof(int32_t);
+}
+
+int fp8_expert_plan_layout(const fp8_expert_sizes_t *sizes, fp8_expert_layout_t *layout) {
+    if (int e = check_expert_sizes(sizes)) return e;
+    if (layout == nullptr) return FP8_ERR_NULL;
+    const ExpertShape s(*sizes);
+    const int64_t word = sizeof(int32_t);
+    *layout = {word * s.offsets, word * s.counts, word * s.slots, word * s.sources};
+    return FP8_OK;
+}
+
+int fp8_expert_plan(const fp8_expert_sizes_t *sizes, const int32_t *expert_ids, void *plan,
+                    int64_t plan_bytes, fp8_stream_t stream) {
+    if (int e = check_expert(sizes, plan, plan_bytes, 0)) return e;
+    if (sizes->tokens > 0 && expert_ids == nullptr) return FP8_ERR_NULL;
+    if (!aligned4(expert_ids)) return FP8_ERR_ALIGN;
+    return status_of(launch_expert_plan(ExpertShape(*sizes), expert_ids,
+                                        static_cast<int32_t *>(plan),
+                                        static_cast<hipStream_t>(stream)));
+}
+
+int fp8_expert_gather(const fp8_expert_sizes_t *sizes, const void *plan, int64_t plan_bytes,
+                      const uint16_t *x, int64_t ldx, uint16_t *y, int64_t ldy, int64_t cols,
+                      fp8_stream_t stream) {
+    if (int e = check_expert(sizes, plan, plan_bytes, cols)) return e;
+    if (bad_stride(ldx, cols) || bad_stride(ldy, cols)) return FP8_ERR_SHAPE;
+    const ExpertShape shape(*sizes);
+    if (shape.rows == 0 || cols == 0) return FP8_OK;
+    if ((shape.tokens > 0 && x == nullptr) || y == nullptr) return FP8_ERR_NULL;
+    if (!aligned16(x) || !aligned16(y)) return FP8_ERR_ALIGN;
+    return status_of(launch_expert_gather(shape, static_cast<const int32_t *>(plan), x, ldx, y,
+                                          ldy, cols, static_cast<hipStream_t>(stream)));
+}
+
+int fp8_expert_gather_cast_transpose_amax(const fp8_expert_sizes_t *sizes, const void *plan,
+                                          int64_t plan_bytes, const uint16_t *x, int64_t ldx,
+                                          int64_t cols, const float *weights, const float *scale,
+                                          const fp8_tensor_t *out, float *amax_cur,
+                                          const int32_t *noop_flag, fp8_stream_t stream) {
+    if (int e = check_expert(sizes, plan, plan_bytes, cols)) return e;
+    const ExpertShape shape(*sizes);
+    // x has other rows than out: its pointer counts where it has any.
+    const bool reads = shape.tokens > 0;
+    if (int e = check_cast(reads ? static_cast<const void *>(x) : plan, FP8_DTYPE_BF16, shape.rows,
+                           cols, ldx, scale, out))
+        return e;
+    if (bad_stride(ldx, cols)) return FP8_ERR_SHAPE;
+    const int64_t tiles_c = (cols + 127) / 128;
+    // The launch's thread count, 256 per tile.
+    if (shape.tiles_max * tiles_c >= ((int64_t)1 << 24)) return FP8_ERR_SHAPE;
+    if (!aligned4(weights)) return FP8_ERR_ALIGN;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (shape.rows == 0 || cols == 0) {
+        if (out->scale_inv == nullptr) return FP8_OK;
+        return status_of(launch_scale_inv_only(scale, out->scale_inv, noop_flag, s));
+    }
+    return status_of(launch_expert_gather_cast(shape, static_cast<const int32_t *>(plan), x, ldx,
+                                               cols, weights, scale, out->fmt, out->data,
+                                               out->data_t, amax_cur, out->scale_inv, noop_flag,
+                                               s));
+}
+
+int fp8_expert_combine(const fp8_expert_sizes_t *sizes, const void *plan, int64_t plan_bytes,
+                       const uint16_t *x, int64_t ldx, const float *weights,
+                       const uint16_t *base, int64_t ldbase, uint16_t *y, int64_t ldy,
+                       int64_t cols, fp8_stream_t stream) {
+    if (int e = check_expert(sizes, plan, plan_bytes, cols)) return e;
+    if (bad_stride(ldx, cols) || bad_stride(ldy, cols) || (base && bad_stride(ldbase, cols)))
+        return FP8_ERR_SHAPE;
+    if (sizes->tokens == 0 || cols == 0) return FP8_OK;
+    const ExpertShape shape(*sizes);
+    if ((shape.rows > 0 && x == nullptr) || y == nullptr) return FP8_ERR_NULL;
+    if (!aligned16(x) || !aligned16(base) || !aligned16(y) || !aligned4(weights))
+        return FP8_ERR_ALIGN;
+    return status_of(launch_expert_combine(shape, static_cast<const int32_t *>(plan), x, ldx,
+                                           weights, base, ldbase, y, ldy, cols,
+                                           static_cast<hipStream_t>(stream)));
+}
+
+int fp8_expert_combine_backward(const fp8_expert_sizes_t *sizes, const void *plan,
+                                int64_t plan_bytes, const uint16_t *dy, int64_t lddy,
+                                const uint16_t *x, int64_t ldx, const float *weights,
+                                float *dweights, uint16_t *dx, int64_t lddx, int64_t cols,
+                                fp8_stream_t stream) {
+    if (int e = check_expert(sizes, plan, plan_bytes, cols)) return e;
+    if (bad_stride(lddy, cols) || bad_stride(ldx, cols) || (dx && bad_stride(lddx, cols)))
+        return FP8_ERR_SHAPE;
+    const ExpertShape shape(*sizes);
+    if (shape.tokens == 0 && (dx == nullptr || shape.rows == 0)) return FP8_OK;
+    if (shape.tokens > 0) {
+        if (dweights == nullptr) return FP8_ERR_NULL;
+        if (cols > 0 && (dy == nullptr || x == nullptr || (dx && weights == nullptr)))
+            return FP8_ERR_NULL;
+    }
+    if (!aligned16(dy) || !aligned16(x) || !aligned16(dx) || !aligned4(weights) ||
+        !aligned4(dweights))
+        return FP8_ERR_ALIGN;
+    return status_of(launch_expert_combine_backward(shape, static_cast<const int32_t *>(plan), dy,
+                                                    lddy, x, ldx, weights, dweights,
+                                                    cols > 0 ? dx : nullptr, lddx, cols,
+                                                    static_cast<hipStream_t>(stream)));
+}
+
+int64_t fp8_grad_norm_workspace_bytes(void) { return kNormParts * (int64_t)sizeof(double); }
+
+int fp8_grad_norm(const fp8_grad_t *grads, int32_t count, float max_norm, float *norm,
+                  float *factor, int32_t *noop_flag, void *workspace, int64_t workspace_bytes,
+                  fp8_stream_t stream) {
+    if (count < 0 || !(max_norm > 0.0f)) return FP8_ERR_ARG;
+    if (norm == nullptr || workspace == nullptr || (count > 0 && grads == nullptr))
+        return FP8_ERR_NULL;
+    if (!aligned16(workspace) || !aligned4(norm) || !aligned4(factor) || !aligned4(noop_flag))
+        return FP8_ERR_ALIGN;
+    if (workspace_bytes < fp8_grad_norm_workspace_bytes()) return FP8_ERR_SHAPE;
+    for (int32_t i = 0; i < count; ++i) {
+        const fp8_grad_t &g = grads[i];
+        if (!valid_dtype(g.dtype) || g.reserved != 0) return FP8_ERR_ARG;
+        if (g.n < 0 || g.n > kTensorMost) return FP8_ERR_SHAPE;
+        if (g.n > 0 && g.grad == nullptr) return FP8_ERR_NULL;
+        if (!aligned16(g.grad)) return FP8_ERR_ALIGN;
+    }
+    return status_of(launch_grad_norm(grads, count, max_norm, norm, factor, noop_flag,
+                                      static_cast<double *>(workspace),
+                                      static_cast<hipStream_t>(stream)));
+}
+
+int fp8_adamw_step(const fp8_adamw_t *opt, const fp8_adamw_tensor_t *tensors, int32_t count,
+                   const float *grad_scale, const int32_t *noop_flag, fp8_stream_t stream) {
+    if (opt == nullptr) return FP8_ERR_NULL;
+    if (count < 0 || !(opt->beta1 >= 0.0 && opt->beta1 < 1.0) ||
+        !(opt->beta2 >= 0.0 && opt->beta2 < 1.0) ||
+        !((float)opt->eps > 0.0f && (float)opt->eps <= 3.402823466e38f))
+        return FP8_ERR_ARG;
+    if (opt->lr == nullptr || opt->steps == nullptr || (count > 0 && tensors == nullptr))
+        return FP8_ERR_NULL;
+    if (!aligned4(opt->lr) || (reinterpret_cast<uintptr_t>(opt->steps) & 7) != 0 ||
+        !aligned4(grad_scale) || !aligned4(noop_flag))
+        return FP8_ERR_ALIGN;
+    for (int32_t i = 0; i < count; ++i) {
+        const fp8_adamw_tensor_t &t = tensors[i];
+        if (!valid_dtype(t.param_dtype) || !valid_dtype(t.grad_dtype) || t.reserved != 0 ||
+            !(t.weight_decay >= 0.0f && t.weight_decay <= 3.402823466e38f) ||
+            (t.copy && t.param_dtype != FP8_DTYPE_FP32) ||
+            (t.m_scale == nullptr) != (t.v_scale == nullptr))
+            return FP8_ERR_ARG;
+        if (t.n < 0 || t.n > kTensorMost) return FP8_ERR_SHAPE;
+        if (t.n > 0 && (!t.param || !t.grad || !t.m || !t.v)) return FP8_ERR_NULL;
+        if (!aligned16(t.param) || !aligned16(t.grad) || !aligned16(t.m) || !aligned16(t.v) ||
+            !aligned16(t.copy) || !aligned4(t.m_scale) || !aligned4(t.v_scale))
+            return FP8_ERR_ALIGN;
+    }
+    return status_of(launch_adamw(*opt, tensors, count, grad_scale, noop_flag,
+                                  static_cast<hipStream_t>(stream)));
 }
 
 int fp8_cast_transpose_dynamic(const void *x, int32_t src, int64_t rows, int64_t cols,

@@ -43,6 +43,7 @@
 #include <type_traits>
 
 #include "dropout.h"
+#include "expert.h"
 #include "fp8_codec.h"
 #include "fp8dsl_internal.h"
 
@@ -1012,6 +1013,106 @@ hipError_t launch_dropout_cast_fmt(const uint16_t *x, int64_t ldx, const uint16_
     return hipGetLastError();
 }
 
+// Rows gathered into expert order in front of a cast: y[slot(t, k)] = x[t], or
+// bf16(weights[t, k] * x[t]), cast as fp8_cast_transpose_amax casts y, each
+// segment of the plan with a transpose of its own.  One workgroup per 128 x 128
+// tile in the lane layout of the cast; a tile lies within one segment, and a lane
+// finds the tokens of its four rows in the plan's sources.  Rows without a pair are
+// zeros.  Workgroups behind the plan's last tile have nothing to do.
+template <int FMT, bool WANT_Q, bool WANT_QT, bool WEIGHTS>
+__global__ __launch_bounds__(THREADS) void expert_gather_cast_kernel(
+    ExpertView plan, const uint16_t *__restrict__ x, uint32_t ldx, int64_t cols,
+    const float *__restrict__ weights, const float *__restrict__ scale_ptr,
+    uint8_t *__restrict__ q, uint8_t *__restrict__ qt, float *__restrict__ amax_cur,
+    float *__restrict__ scale_inv_out, const int32_t *__restrict__ noop, int64_t tiles_c) {
+    if (noop != nullptr && *noop != 0) return;
+    if (!plan.built()) return;
+    __shared__ uint32_t lds_t[TILE * (TILE / 4)];
+    __shared__ uint32_t lds_amax[THREADS / 64];
+
+    const int tid = threadIdx.x;
+    const int lane = tid & 63;
+    const int wave = tid >> 6;
+    const int cc = lane & 7;
+    const int cq = store_chunk<FP8_DTYPE_BF16>(cc);
+    const int rg = wave * 8 + (lane >> 3);
+    const float s = *scale_ptr;
+    const bool s_special = !(fabsf(s) > 0.0f && fabsf(s) <= 3.402823466e38f);
+    if (blockIdx.x == 0 && tid == 0 && scale_inv_out != nullptr) *scale_inv_out = 1.0f / s;
+
+    const int64_t tr = blockIdx.x / tiles_c, tcn = blockIdx.x - tr * tiles_c;
+    if (tr >= plan.header[5]) return;
+    const int4 tile = plan.tiles[tr];
+    const int64_t rows = tile.y, first = tile.z;         // the segment
+    const int64_t row0 = tile.x, col0 = tcn * TILE;
+    const int64_t r = row0 + 4 * rg, c = col0 + 16 * cq;
+    const bool valid = (r < rows) && (c < cols);   // rows, cols are multiples of 16
+    q += first * cols;
+    qt += first * cols;
+
+    int4 source = {-1, -1, -1, -1};
+    if (r < rows) source = *reinterpret_cast<const int4 *>(plan.sources + first + r);
+    const int pair[4] = {source.x, source.y, source.z, source.w};
+    SrcRow<FP8_DTYPE_BF16> ys[4];
+    float w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        w[i] = WEIGHTS && pair[i] >= 0 ? weights[pair[i]] : 0.0f;
+        const char *row = reinterpret_cast<const char *>(x) +
+                          (uint64_t)((uint32_t)max(pair[i], 0) / (uint32_t)plan.top_k) * ldx;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int64_t ch = col0 + 64 * h + 8 * cc;
+            ys[i].v[h] = u32x4{0u, 0u, 0u, 0u};
+            if (pair[i] >= 0 && ch < cols)
+                ys[i].v[h] = *reinterpret_cast<const u32x4 *>(row + 2 * ch);
+        }
+    }
+    if constexpr (WEIGHTS) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t xw = ys[i].v[h][k];
+                    const float v0 = w[i] * bf16_lo(xw), v1 = w[i] * bf16_hi(xw);
+                    const uint32_t y0 = (v0 != v0) ? 0x7FC0u : f32_to_bf16_bits_rne(v0);
+                    const uint32_t y1 = (v1 != v1) ? 0x7FC0u : f32_to_bf16_bits_rne(v1);
+                    ys[i].v[h][k] = pair[i] >= 0 ? y0 | (y1 << 16) : 0u;
+                }
+    }
+    uint32_t key = 0;
+    encode_block<FP8_DTYPE_BF16, FMT, WANT_Q, WANT_QT>(ys, s, s_special, valid, q, r, c, cols, cq,
+                                                       rg, lane, nullptr, lds_t, key);
+    __syncthreads();
+    if constexpr (WANT_QT) store_transposed(lds_t, qt, rows, cols, row0, col0, lane, wave);
+    if (amax_cur != nullptr) flush_amax(key, amax_cur, lds_amax, lane, wave, tid);
+}
+
+template <int FMT, bool WEIGHTS>
+hipError_t launch_expert_gather_cast_fmt(const ExpertShape &shape, const int32_t *plan,
+                                         const uint16_t *x, int64_t ldx, int64_t cols,
+                                         const float *weights, const float *scale, uint8_t *q,
+                                         uint8_t *qt, float *amax_cur, float *scale_inv_out,
+                                         const int32_t *noop, hipStream_t stream) {
+    const int64_t tiles_c = (cols + TILE - 1) / TILE;
+    const dim3 grid((unsigned)(shape.tiles_max * tiles_c));
+    auto launch = [&](auto wq, auto wqt) {
+        hipLaunchKernelGGL((expert_gather_cast_kernel<FMT, decltype(wq)::value,
+                                                      decltype(wqt)::value, WEIGHTS>),
+                           grid, dim3(THREADS), 0, stream, ExpertView(shape, plan), x,
+                           (uint32_t)(2 * ldx), cols, weights, scale, q, qt, amax_cur,
+                           scale_inv_out, noop, tiles_c);
+    };
+    using T1 = std::true_type;
+    using F1 = std::false_type;
+    if (q && qt) launch(T1{}, T1{});
+    else if (q) launch(T1{}, F1{});
+    else launch(F1{}, T1{});
+    return hipGetLastError();
+}
+
 // Gradient of the modulation producer y = a * x / b (FP8_PRODUCE_MODULATE,
 // or _FINITE) with respect to x, a and b, for the output gradient dy of y.
 // fp32 on the widened bf16 inputs, each step rounded to nearest even:
@@ -1163,6 +1264,19 @@ hipError_t launch_dropout_cast(const uint16_t *x, int64_t ldx, const uint16_t *r
     return launch_dropout_cast_fmt<FP8_E5M2>(x, ldx, residual, ldres, y, ldy, rows, cols, drop,
                                              scale, q, qt, amax_cur, scale_inv_out, noop, dbias_ws,
                                              ws_ld, stream);
+}
+
+hipError_t launch_expert_gather_cast(const ExpertShape &shape, const int32_t *plan,
+                                     const uint16_t *x, int64_t ldx, int64_t cols,
+                                     const float *weights, const float *scale, int fmt, uint8_t *q,
+                                     uint8_t *qt, float *amax_cur, float *scale_inv_out,
+                                     const int32_t *noop, hipStream_t stream) {
+    const auto launch = fmt == FP8_E4M3 ? (weights ? launch_expert_gather_cast_fmt<FP8_E4M3, true>
+                                                   : launch_expert_gather_cast_fmt<FP8_E4M3, false>)
+                                        : (weights ? launch_expert_gather_cast_fmt<FP8_E5M2, true>
+                                                   : launch_expert_gather_cast_fmt<FP8_E5M2, false>);
+    return launch(shape, plan, x, ldx, cols, weights, scale, q, qt, amax_cur, scale_inv_out, noop,
+                  stream);
 }
 
 hipError_t launch_modulate_backward(bool finite, const uint16_t *dy, int64_t lddy,

@@ -39,6 +39,9 @@ struct DropoutKey {
         off_lo = (uint32_t)o;
         off_hi = (uint32_t)(o >> 32);
     }
+    // A generator whose key and stream the caller has in registers.
+    __device__ __forceinline__ DropoutKey(uint32_t lo, uint32_t hi, uint64_t stream)
+        : seed_lo(lo), seed_hi(hi), off_lo((uint32_t)stream), off_hi((uint32_t)(stream >> 32)) {}
 };
 
 // The eight 16-bit numbers of group e: element i in half i % 2 of word i / 2.

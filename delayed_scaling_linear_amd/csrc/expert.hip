@@ -1,0 +1,409 @@
+// Tokens sorted by expert, and back.
+//
+//   plan      a stable counting sort of the (token, choice) pairs by expert;
+//   gather    y[slot(t, k)] = x[t], and zeros in the segments' other rows;
+//   combine   y[t] = base[t] + sum over k of w[t, k] x[slot(t, k)];
+//   backward  dw[t, k] = dy[t] . x[slot(t, k)], dx[slot(t, k)] = w[t, k] dy[t].
+//
+// (The gather with the cast is in the cast's file, whose tile it uses.)
+#include "expert.h"
+
+#include "fp8dsl_internal.h"
+
+namespace fp8dsl {
+namespace {
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// ---- the plan ----------------------------------------------------------------
+
+constexpr int PLAN_THREADS = 512;
+constexpr int PLAN_WAVES = PLAN_THREADS / 64;
+
+__device__ __forceinline__ void wave_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+__device__ __forceinline__ int wave_inclusive(int v, int lane) {
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const int up = __shfl_up(v, d, 64);
+        v += lane >= d ? up : 0;
+    }
+    return v;
+}
+
+// Pairs of each expert in the workgroup's piece of the ids.
+__global__ __launch_bounds__(PLAN_THREADS) void expert_count_kernel(
+    const int32_t *__restrict__ ids, int64_t pairs, int64_t piece, int experts,
+    int32_t *__restrict__ hist) {
+    __shared__ int count[kExpertsMax];
+    for (int e = threadIdx.x; e < experts; e += PLAN_THREADS) count[e] = 0;
+    __syncthreads();
+    const int64_t p0 = (int64_t)blockIdx.x * piece, p1 = min(pairs, p0 + piece);
+    for (int64_t p = p0 + threadIdx.x; p < p1; p += PLAN_THREADS) {
+        const uint32_t e = (uint32_t)ids[p];
+        if (e < (uint32_t)experts) atomicAdd(&count[e], 1);
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < experts; e += PLAN_THREADS)
+        hist[(int64_t)blockIdx.x * experts + e] = count[e];
+}
+
+// Places the pairs of the workgroup's piece.  Each wave takes a run of the piece
+// and counts its pairs per expert (LDS counters: a count does not depend on their
+// order); the runs before it, in this piece and the earlier ones (hist), give the
+// first place of each expert's pairs.  It then walks its run 64 pairs at a time:
+// lanes that name the same expert find each other by ballots over the id's bits,
+// and their order among these is their order in the batch.
+__global__ __launch_bounds__(PLAN_THREADS) void expert_place_kernel(
+    const int32_t *__restrict__ ids, int64_t pairs, int64_t piece, int pieces, int tokens,
+    int top_k, int experts, int capacity, int rows, const int32_t *__restrict__ hist,
+    int32_t *__restrict__ header, int32_t *__restrict__ offsets, int32_t *__restrict__ counts,
+    int32_t *__restrict__ slots, int32_t *__restrict__ sources, int4 *__restrict__ tiles) {
+    extern __shared__ int lds[];
+    int *run = lds;                              // [waves][experts]
+    int *all = run + PLAN_WAVES * experts;       // [experts] pairs of all pieces
+    int *first = all + experts;                  // [experts + 1] first row
+    int *tile0 = first + experts + 1;            // [experts + 1] first tile
+    __shared__ int2 wave_sum[PLAN_WAVES];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int64_t p0 = (int64_t)blockIdx.x * piece, p1 = min(pairs, p0 + piece);
+    const int64_t per_wave = ((p1 - p0 + PLAN_WAVES - 1) / PLAN_WAVES + 63) / 64 * 64;
+    const int64_t w0 = min(p1, p0 + wave * per_wave), w1 = min(p1, w0 + per_wave);
+
+    for (int i = tid; i < PLAN_WAVES * experts; i += PLAN_THREADS) run[i] = 0;
+    __syncthreads();
+    for (int64_t p = w0 + lane; p < w1; p += 64) {
+        const uint32_t e = (uint32_t)ids[p];
+        if (e < (uint32_t)experts) atomicAdd(&run[wave * experts + e], 1);
+    }
+    __syncthreads();
+    // Pairs before each wave's run, and all pairs, of each expert.
+    for (int e = tid; e < experts; e += PLAN_THREADS) {
+        int before = 0, total = 0;
+        if (pieces > 1) {
+            for (int g = 0; g < pieces; ++g) {
+                const int c = hist[(int64_t)g * experts + e];
+                before += g < (int)blockIdx.x ? c : 0;
+                total += c;
+            }
+        }
+        for (int w = 0; w < PLAN_WAVES; ++w) {
+            const int c = run[w * experts + e];
+            run[w * experts + e] = before;
+            before += c;
+        }
+        all[e] = pieces > 1 ? total : before;
+    }
+    __syncthreads();
+    // First row and tile of each segment: a scan over the experts, two a thread.
+    static_assert(kExpertsMax <= 2 * PLAN_THREADS, "two experts a thread");
+    int2 length[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int e = 2 * tid + i;
+        const int l = e >= experts ? 0 : capacity ? capacity : (all[e] + 15) / 16 * 16;
+        length[i] = int2{l, (l + kExpertTile - 1) / kExpertTile};
+    }
+    const int2 mine = {length[0].x + length[1].x, length[0].y + length[1].y};
+    int2 sum = {wave_inclusive(mine.x, lane), wave_inclusive(mine.y, lane)};
+    if (lane == 63) wave_sum[wave] = sum;
+    __syncthreads();
+    for (int w = 0; w < wave; ++w) {
+        sum.x += wave_sum[w].x;
+        sum.y += wave_sum[w].y;
+    }
+    int2 at = {sum.x - mine.x, sum.y - mine.y};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int e = 2 * tid + i;
+        if (e < experts) {
+            first[e] = at.x;
+            tile0[e] = at.y;
+        }
+        at.x += length[i].x;
+        at.y += length[i].y;
+        if (e == experts - 1) {
+            first[experts] = at.x;
+            tile0[experts] = at.y;
+        }
+    }
+    __syncthreads();
+
+    const int end = first[experts], ntiles = tile0[experts];
+    if (blockIdx.x == 0) {
+        if (tid == 0) {
+            header[0] = kExpertMagic;
+            header[1] = tokens;
+            header[2] = top_k;
+            header[3] = experts;
+            header[4] = capacity;
+            header[5] = ntiles;
+            header[6] = end;
+        }
+        for (int e = tid; e <= experts; e += PLAN_THREADS) {
+            offsets[e] = first[e];
+            if (e < experts) counts[e] = capacity ? min(all[e], capacity) : all[e];
+        }
+    }
+    // The tiles, spread over the workgroups; a tile's expert by bisection.
+    for (int t = blockIdx.x * PLAN_THREADS + tid; t < ntiles; t += gridDim.x * PLAN_THREADS) {
+        int lo = 0, hi = experts;                // tile0[lo] <= t < tile0[hi]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if (tile0[mid] <= t) lo = mid;
+            else hi = mid;
+        }
+        tiles[t] = int4{(t - tile0[lo]) * kExpertTile, first[lo + 1] - first[lo], first[lo], 0};
+    }
+    // Slots without a pair: the ends of the segments (a wave each) and what lies
+    // behind the last one.
+    for (int e = blockIdx.x * PLAN_WAVES + wave; e < experts; e += gridDim.x * PLAN_WAVES) {
+        const int kept = capacity ? min(all[e], capacity) : all[e];
+        for (int r = first[e] + kept + lane; r < first[e + 1]; r += 64) sources[r] = -1;
+    }
+    for (int64_t r = end + (int64_t)blockIdx.x * PLAN_THREADS + tid; r < rows;
+         r += (int64_t)gridDim.x * PLAN_THREADS)
+        sources[r] = -1;
+
+    int *next = run + wave * experts;
+    for (int64_t pw = w0; pw < w1; pw += 64) {
+        const int64_t p = pw + lane;
+        const uint32_t id = p < w1 ? (uint32_t)ids[p] : 0xFFFFFFFFu;
+        const bool named = id < (uint32_t)experts;
+        uint64_t same = __ballot(named);
+        for (int b = 0; (1 << b) < experts; ++b) {
+            const bool bit = (id >> b) & 1;
+            const uint64_t votes = __ballot(bit);
+            same &= bit ? votes : ~votes;
+        }
+        int slot = -1;
+        if (named) {
+            const int base = next[id];
+            const int rank = base + __popcll(same & ((1ull << lane) - 1));
+            wave_fence();
+            if ((same >> lane) == 1ull) next[id] = rank + 1;     // the last of them
+            if (!capacity || rank < capacity) slot = first[id] + rank;
+        }
+        wave_fence();
+        if (p < w1) {
+            slots[p] = slot;
+            if (slot >= 0) sources[slot] = (int32_t)p;
+        }
+    }
+}
+
+// ---- rows --------------------------------------------------------------------
+
+constexpr int THREADS = 256;
+
+__device__ __forceinline__ float bf16_lo(uint32_t d) { return __uint_as_float(d << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t d) { return __uint_as_float(d & 0xFFFF0000u); }
+
+__device__ __forceinline__ uint32_t bf16_bits(float f) {
+    const uint32_t u = __float_as_uint(f);
+    return (f != f) ? 0x7FC0u : (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
+}
+
+// Row `row` (not negative) of a bf16 matrix with its stride in bytes.
+__device__ __forceinline__ const char *row_at(const void *p, int row, uint32_t ld_bytes) {
+    return static_cast<const char *>(p) + (uint64_t)(uint32_t)row * ld_bytes;
+}
+__device__ __forceinline__ char *row_at(void *p, int row, uint32_t ld_bytes) {
+    return static_cast<char *>(p) + (uint64_t)(uint32_t)row * ld_bytes;
+}
+
+// Zeros in the rows of the segments that have no pair: the workgroups behind
+// those of the tokens, ZERO_ROWS slots each.
+constexpr int ZERO_ROWS = 256;
+__device__ __forceinline__ void zero_rows(const ExpertView &plan, int64_t block, void *y,
+                                          uint32_t ldy, int64_t groups) {
+    __shared__ uint64_t empty[THREADS / 64];
+    const int tid = threadIdx.x, row0 = (int)(block * ZERO_ROWS), end = plan.offsets[plan.experts];
+    const int row = row0 + tid;
+    const uint64_t votes = __ballot(row < end && plan.sources[row] < 0);
+    if ((tid & 63) == 0) empty[tid >> 6] = votes;
+    __syncthreads();
+    for (int w = 0; w < THREADS / 64; ++w) {
+        for (uint64_t left = empty[w]; left; left &= left - 1) {
+            char *to = row_at(y, row0 + 64 * w + __builtin_ctzll(left), ldy);
+            for (int64_t g = tid; g < groups; g += THREADS)
+                *reinterpret_cast<u32x4 *>(to + 16 * g) = u32x4{0u, 0u, 0u, 0u};
+        }
+    }
+}
+
+// A workgroup covers 2^tx_log2 groups of 8 columns of 256 / 2^tx_log2 tokens.
+__global__ __launch_bounds__(THREADS) void expert_gather_kernel(
+    ExpertView plan, const uint16_t *__restrict__ x, uint32_t ldx, uint16_t *__restrict__ y,
+    uint32_t ldy, int64_t groups, int tx_log2, int64_t token_blocks) {
+    if (!plan.built()) return;
+    if (blockIdx.x >= token_blocks) {
+        if (blockIdx.y == 0) zero_rows(plan, blockIdx.x - token_blocks, y, ldy, groups);
+        return;
+    }
+    const int tx = 1 << tx_log2;
+    const int64_t g = (int64_t)blockIdx.y * tx + (threadIdx.x & (tx - 1));
+    const int64_t t = (int64_t)blockIdx.x * (THREADS >> tx_log2) + (threadIdx.x >> tx_log2);
+    if (g >= groups || t >= plan.tokens) return;
+    const u32x4 v = *reinterpret_cast<const u32x4 *>(row_at(x, (int)t, ldx) + 16 * g);
+    for (int k = 0; k < plan.top_k; ++k) {
+        const int slot = plan.slots[t * plan.top_k + k];
+        if (slot >= 0) *reinterpret_cast<u32x4 *>(row_at(y, slot, ldy) + 16 * g) = v;
+    }
+}
+
+// The same split.
+template <bool WEIGHTS>
+__global__ __launch_bounds__(THREADS) void expert_combine_kernel(
+    ExpertView plan, const uint16_t *__restrict__ x, uint32_t ldx,
+    const float *__restrict__ weights, const uint16_t *base, uint32_t ldbase, uint16_t *y,
+    uint32_t ldy, int64_t groups, int tx_log2) {
+    if (!plan.built()) return;
+    const int tx = 1 << tx_log2;
+    const int64_t g = (int64_t)blockIdx.y * tx + (threadIdx.x & (tx - 1));
+    const int64_t t = (int64_t)blockIdx.x * (THREADS >> tx_log2) + (threadIdx.x >> tx_log2);
+    if (g >= groups || t >= plan.tokens) return;
+    float sum[8];
+    u32x4 b = {0u, 0u, 0u, 0u};
+    if (base) b = *reinterpret_cast<const u32x4 *>(row_at(base, (int)t, ldbase) + 16 * g);
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+        sum[2 * d] = bf16_lo(b[d]);
+        sum[2 * d + 1] = bf16_hi(b[d]);
+    }
+    for (int k = 0; k < plan.top_k; ++k) {
+        const int64_t pair = t * plan.top_k + k;
+        const int slot = plan.slots[pair];
+        if (slot < 0) continue;
+        const u32x4 v = *reinterpret_cast<const u32x4 *>(row_at(x, slot, ldx) + 16 * g);
+        const float w = WEIGHTS ? weights[pair] : 1.0f;
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+            sum[2 * d] += w * bf16_lo(v[d]);
+            sum[2 * d + 1] += w * bf16_hi(v[d]);
+        }
+    }
+    u32x4 out;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) out[d] = bf16_bits(sum[2 * d]) | (bf16_bits(sum[2 * d + 1]) << 16);
+    *reinterpret_cast<u32x4 *>(row_at(y, (int)t, ldy) + 16 * g) = out;
+}
+
+// A wave per token: its lanes take the columns 8 lane + 512 i, their sums meet in a
+// butterfly.
+template <bool DX>
+__global__ __launch_bounds__(THREADS) void expert_combine_backward_kernel(
+    ExpertView plan, const uint16_t *__restrict__ dy, uint32_t lddy, const uint16_t *x,
+    uint32_t ldx, const float *__restrict__ weights, float *__restrict__ dweights, uint16_t *dx,
+    uint32_t lddx, int64_t groups, int64_t token_blocks) {
+    if (!plan.built()) return;
+    if (blockIdx.x >= token_blocks) {
+        zero_rows(plan, blockIdx.x - token_blocks, dx, lddx, groups);
+        return;
+    }
+    const int lane = threadIdx.x & 63;
+    const int64_t t = (int64_t)blockIdx.x * (THREADS / 64) + (threadIdx.x >> 6);
+    if (t >= plan.tokens) return;
+    for (int k = 0; k < plan.top_k; ++k) {
+        const int64_t pair = t * plan.top_k + k;
+        const int slot = plan.slots[pair];
+        float sum = 0.0f;
+        if (slot >= 0) {
+            const float w = DX ? weights[pair] : 0.0f;
+            for (int64_t g = lane; g < groups; g += 64) {
+                const u32x4 a = *reinterpret_cast<const u32x4 *>(row_at(dy, (int)t, lddy) + 16 * g);
+                const u32x4 v = *reinterpret_cast<const u32x4 *>(row_at(x, slot, ldx) + 16 * g);
+                u32x4 out;
+#pragma unroll
+                for (int d = 0; d < 4; ++d) {
+                    sum += bf16_lo(a[d]) * bf16_lo(v[d]);
+                    sum += bf16_hi(a[d]) * bf16_hi(v[d]);
+                    out[d] = bf16_bits(w * bf16_lo(a[d])) | (bf16_bits(w * bf16_hi(a[d])) << 16);
+                }
+                if constexpr (DX)
+                    *reinterpret_cast<u32x4 *>(row_at(dx, slot, lddx) + 16 * g) = out;
+            }
+        }
+#pragma unroll
+        for (int m = 32; m >= 1; m >>= 1) sum += __shfl_xor(sum, m, 64);
+        if (lane == 0) dweights[pair] = sum;
+    }
+}
+
+// Lanes of a workgroup along the columns: a power of two that covers them, or 256.
+int lanes_log2(int64_t groups) {
+    int tx_log2 = 3;
+    while (tx_log2 < 8 && (int64_t(1) << tx_log2) < groups) ++tx_log2;
+    return tx_log2;
+}
+
+int64_t zero_blocks(const ExpertShape &shape) { return (shape.rows + ZERO_ROWS - 1) / ZERO_ROWS; }
+
+}  // namespace
+
+hipError_t launch_expert_plan(const ExpertShape &s, const int32_t *ids, int32_t *plan,
+                              hipStream_t stream) {
+    const int64_t piece = (s.pairs + s.pieces - 1) / s.pieces;
+    if (s.pieces > 1) {
+        hipLaunchKernelGGL(expert_count_kernel, dim3((unsigned)s.pieces), dim3(PLAN_THREADS), 0,
+                           stream, ids, s.pairs, piece, s.experts, plan + s.hist);
+        if (hipError_t e = hipGetLastError()) return e;
+    }
+    const int lds_bytes = (int)sizeof(int) * ((PLAN_WAVES + 3) * s.experts + 2);
+    hipLaunchKernelGGL(expert_place_kernel, dim3((unsigned)s.pieces), dim3(PLAN_THREADS),
+                       lds_bytes, stream, ids, s.pairs, piece, (int)s.pieces, (int)s.tokens,
+                       s.top_k, s.experts, (int)s.capacity, (int)s.rows, plan + s.hist, plan,
+                       plan + s.offsets, plan + s.counts, plan + s.slots, plan + s.sources,
+                       reinterpret_cast<int4 *>(plan + s.tiles));
+    return hipGetLastError();
+}
+
+hipError_t launch_expert_gather(const ExpertShape &s, const int32_t *plan, const uint16_t *x,
+                                int64_t ldx, uint16_t *y, int64_t ldy, int64_t cols,
+                                hipStream_t stream) {
+    const int64_t groups = cols / 8;
+    const int tx_log2 = lanes_log2(groups), tokens = THREADS >> tx_log2;
+    const int64_t token_blocks = (s.tokens + tokens - 1) / tokens;
+    const int64_t tx = int64_t(1) << tx_log2;
+    const dim3 grid((unsigned)(token_blocks + zero_blocks(s)), (unsigned)((groups + tx - 1) / tx));
+    hipLaunchKernelGGL(expert_gather_kernel, grid, dim3(THREADS), 0, stream, ExpertView(s, plan), x,
+                       (uint32_t)(2 * ldx), y, (uint32_t)(2 * ldy), groups, tx_log2, token_blocks);
+    return hipGetLastError();
+}
+
+hipError_t launch_expert_combine(const ExpertShape &s, const int32_t *plan, const uint16_t *x,
+                                 int64_t ldx, const float *weights, const uint16_t *base,
+                                 int64_t ldbase, uint16_t *y, int64_t ldy, int64_t cols,
+                                 hipStream_t stream) {
+    const int64_t groups = cols / 8;
+    const int tx_log2 = lanes_log2(groups), tokens = THREADS >> tx_log2;
+    const int64_t tx = int64_t(1) << tx_log2;
+    const dim3 grid((unsigned)((s.tokens + tokens - 1) / tokens),
+                    (unsigned)((groups + tx - 1) / tx));
+    const auto kernel = weights ? expert_combine_kernel<true> : expert_combine_kernel<false>;
+    hipLaunchKernelGGL(kernel, grid, dim3(THREADS), 0, stream, ExpertView(s, plan), x,
+                       (uint32_t)(2 * ldx), weights, base, (uint32_t)(2 * ldbase), y,
+                       (uint32_t)(2 * ldy), groups, tx_log2);
+    return hipGetLastError();
+}
+
+hipError_t launch_expert_combine_backward(const ExpertShape &s, const int32_t *plan,
+                                          const uint16_t *dy, int64_t lddy, const uint16_t *x,
+                                          int64_t ldx, const float *weights, float *dweights,
+                                          uint16_t *dx, int64_t lddx, int64_t cols,
+                                          hipStream_t stream) {
+    const int64_t groups = cols / 8;
+    const int64_t token_blocks = (s.tokens + THREADS / 64 - 1) / (THREADS / 64);
+    const dim3 grid((unsigned)(token_blocks + (dx ? zero_blocks(s) : 0)));
+    const auto kernel = dx ? expert_combine_backward_kernel<true>
+                           : expert_combine_backward_kernel<false>;
+    hipLaunchKernelGGL(kernel, grid, dim3(THREADS), 0, stream, ExpertView(s, plan), dy,
+                       (uint32_t)(2 * lddy), x, (uint32_t)(2 * ldx), weights, dweights, dx,
+                       (uint32_t)(2 * lddx), groups, token_blocks);
+    return hipGetLastError();
+}
+
+}  // namespace fp8dsl

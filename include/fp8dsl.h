@@ -24,6 +24,11 @@
  * (fp8_dropout, fp8_dropout_cast_transpose_amax),
  * low-rank adapters of many requests beside a shared projection, forward and
  * backward (fp8_adapter_plan, fp8_adapter_fwd, fp8_adapter_backward),
+ * tokens sorted by expert and back, with the cast fused and the gradients
+ * (fp8_expert_plan, fp8_expert_gather, fp8_expert_gather_cast_transpose_amax,
+ * fp8_expert_combine, fp8_expert_combine_backward),
+ * the gradients' norm and an AdamW step over many tensors, with states in 32
+ * or 8 bits (fp8_grad_norm, fp8_adamw_step),
  * dynamic scaling as the comparator (fp8_cast_transpose_dynamic), the
  * forward with FP8 output and output amax (fp8_linear_fwd_fp8out), the three
  * products split over K through a caller workspace for shapes that alone
@@ -775,6 +780,299 @@ int fp8_adapter_backward(const fp8_adapters_t *w, const void *plan, int64_t plan
                          const uint16_t *dx_base, int64_t lddxbase, uint16_t *dx, int64_t lddx,
                          int64_t rows, void *da, void *db, int32_t out_dtype, void *workspace,
                          int64_t workspace_bytes, fp8_stream_t stream);
+
+/*
+ * Tokens sorted by expert, and back.
+ *
+ * In a layer of experts every token names top_k experts, each a stack of
+ * linears of its own.  The calls below bring the tokens' rows into expert
+ * order, where an expert's rows lie together for its casts and products, and
+ * its results back with the router's weights:
+ *
+ *   fp8_expert_plan       where each (token, choice) pair goes, once per layer
+ *                         and step;
+ *   fp8_expert_gather     rows to expert order, bf16;
+ *   fp8_expert_gather_cast_transpose_amax   the same with the cast: the first
+ *                         linears' input (E4M3), or with the router's weights
+ *                         the output gradient of the last ones (E5M2);
+ *   fp8_expert_combine    y[t] = base[t] + sum over k of w[t, k] x[slot(t, k)];
+ *                         without weights the gradient of the gathers;
+ *   fp8_expert_combine_backward   its gradients for w and, in bf16, for x.
+ *
+ * The plan.  Expert e keeps the pairs (t, k) with expert_ids[t, k] == e in the
+ * order of t * top_k + k, and gives them the slots offsets[e], offsets[e] + 1,
+ * ...  An expert's segment, offsets[e] .. offsets[e + 1] - 1, is a multiple of
+ * 16 rows, as the casts and products want them:
+ *
+ *   capacity 0   every pair is kept; the segment is the expert's count rounded
+ *                up to 16.  Its size is known on the device only: a program
+ *                that runs the experts' products reads `offsets` back.
+ *   capacity C   (a multiple of 16) at most C pairs are kept, the rest dropped;
+ *                every segment is C rows, so nothing needs to be read back and
+ *                the whole layer can be captured in a HIP graph.
+ *
+ * A token may name an expert twice (two slots).  An id outside 0 .. experts - 1
+ * (-1, say) names none: padding tokens of a batch.  Slots of a segment that
+ * hold no pair are rows of zeros.  Rows behind the last segment are left as
+ * they were.
+ *
+ * Sizes: 0 <= tokens, 1 <= top_k <= FP8DSL_EXPERT_TOP_K_MAX, tokens * top_k <=
+ * 2^23, 1 <= experts <= FP8DSL_EXPERTS_MAX, and at most 2^24 rows.
+ *
+ * fp8_expert_rows: rows of a tensor in expert order, fixed by the sizes:
+ * experts * capacity, or for capacity 0 the most that the segments can be,
+ * tokens * top_k + 15 * min(experts, tokens * top_k) rounded down to a multiple
+ * of 16.  fp8_expert_plan_bytes: the plan's size.  Both return a negative status
+ * for sizes out of range.
+ */
+#define FP8DSL_EXPERTS_MAX 1024
+#define FP8DSL_EXPERT_TOP_K_MAX 64
+
+typedef struct fp8_expert_sizes {
+    int64_t tokens;
+    int64_t capacity;       /* rows of a segment, a multiple of 16, or 0       */
+    int32_t top_k;
+    int32_t experts;
+} fp8_expert_sizes_t;
+
+/* Byte offsets of a plan's int32 arrays, for programs that read them. */
+typedef struct fp8_expert_layout {
+    int64_t offsets;        /* [experts + 1] first row of each segment, the end */
+    int64_t counts;         /* [experts] pairs that each expert keeps           */
+    int64_t slots;          /* [tokens, top_k] slot of each pair, -1: none      */
+    int64_t sources;        /* [rows] pair t * top_k + k of each slot, -1: none */
+} fp8_expert_layout_t;
+
+int64_t fp8_expert_rows(const fp8_expert_sizes_t *sizes);
+int64_t fp8_expert_plan_bytes(const fp8_expert_sizes_t *sizes);
+int fp8_expert_plan_layout(const fp8_expert_sizes_t *sizes, fp8_expert_layout_t *layout);
+
+/*
+ * fp8_expert_plan -- builds the plan of a batch.
+ *
+ * expert_ids  device int32 [tokens, top_k].
+ * plan        device, 16-byte aligned, fp8_expert_plan_bytes bytes, owned by
+ *             the caller; read by the calls below until it is built again.
+ * Sources behind the last segment are -1.  tokens 0 is a batch like any other:
+ * every segment is empty, or C rows of zeros.
+ * Errors: FP8_ERR_SHAPE (sizes, plan_bytes), FP8_ERR_NULL, FP8_ERR_ALIGN,
+ * FP8_ERR_LAUNCH / FP8_ERR_DEVICE.
+ */
+int fp8_expert_plan(const fp8_expert_sizes_t *sizes, const int32_t *expert_ids, void *plan,
+                    int64_t plan_bytes, fp8_stream_t stream);
+
+/*
+ * fp8_expert_gather -- y[slot(t, k)] = x[t], bf16.
+ *
+ * plan      built for these sizes (a buffer that holds no such plan leaves the
+ *           outputs of this and the calls below unwritten).
+ * x         device bf16 [tokens, cols], row stride ldx.
+ * y         device bf16 [rows, cols], row stride ldy; must not overlap x.
+ * cols >= 0 and a multiple of 8, at most 2^22; strides multiples of 8, at least
+ * cols and below 2^30; tensors 16-byte aligned.
+ * The gradient with respect to x is fp8_expert_combine without weights.
+ * Errors: FP8_ERR_NULL, FP8_ERR_SHAPE (sizes, plan_bytes, cols, strides),
+ * FP8_ERR_ALIGN, FP8_ERR_LAUNCH / FP8_ERR_DEVICE.
+ */
+int fp8_expert_gather(const fp8_expert_sizes_t *sizes, const void *plan, int64_t plan_bytes,
+                      const uint16_t *x, int64_t ldx, uint16_t *y, int64_t ldy, int64_t cols,
+                      fp8_stream_t stream);
+
+/*
+ * fp8_expert_gather_cast_transpose_amax -- the gather fused with the cast of
+ * its result, as fp8_dropout_cast_transpose_amax fuses a dropout.
+ *
+ *   y[slot(t, k)] = weights ? bf16(weights[t, k] * x[t]) : x[t]    (fp32 product)
+ *
+ * then what fp8_cast_transpose_amax writes for y with this scale, save that the
+ * transpose is one of each segment: with f = offsets[e], l the segment's rows
+ * and h = f * cols,
+ *
+ *   out->data[r * cols + c]                   code of y[r, c]
+ *   out->data_t[h + c * l + (r - f)]          the same code
+ *
+ * so that rows f .. f + l - 1 of data and the l * cols bytes of data_t from h on
+ * are the codes and the transpose of an [l, cols] fp8_tensor_t, expert e's
+ * operand of fp8_linear_fwd, fp8_linear_dgrad and fp8_linear_wgrad.  y itself is
+ * not stored.  A NaN product is a NaN in y (0x7FC0).
+ *
+ * x         device bf16 [tokens, cols], row stride ldx.
+ * weights   NULL, or device fp32 [tokens, top_k], 4-byte aligned.
+ * out       host descriptor with out->rows = fp8_expert_rows, out->cols = cols.
+ * scale, amax_cur, noop_flag, cols (a multiple of 16) and errors as
+ * fp8_cast_transpose_amax; sizes, plan, ldx and their errors as
+ * fp8_expert_gather.  Fewer than 2^24 tiles of 128 x 128 over all segments.
+ */
+int fp8_expert_gather_cast_transpose_amax(const fp8_expert_sizes_t *sizes, const void *plan,
+                                          int64_t plan_bytes, const uint16_t *x, int64_t ldx,
+                                          int64_t cols, const float *weights, const float *scale,
+                                          const fp8_tensor_t *out, float *amax_cur,
+                                          const int32_t *noop_flag, fp8_stream_t stream);
+
+/*
+ * fp8_expert_combine -- the experts' rows back to their tokens.
+ *
+ *   y[t] = bf16(base[t] + sum over k = 0, 1, ... of weights[t, k] x[slot(t, k)])
+ *
+ * Products and sums in fp32, k in order after base, one rounding; pairs without
+ * a slot add nothing (their weights are not read).
+ *
+ * x         device bf16 [rows, cols], row stride ldx; only rows with a pair are
+ *           read.
+ * weights   NULL (ones), or device fp32 [tokens, top_k], 4-byte aligned.
+ * base      NULL (zeros), or device bf16 [tokens, cols], row stride ldbase.
+ * y         device bf16 [tokens, cols], row stride ldy.  May be base (same
+ *           pointer and stride); must not overlap x or another base.
+ * Other constraints and errors as fp8_expert_gather.
+ */
+int fp8_expert_combine(const fp8_expert_sizes_t *sizes, const void *plan, int64_t plan_bytes,
+                       const uint16_t *x, int64_t ldx, const float *weights,
+                       const uint16_t *base, int64_t ldbase, uint16_t *y, int64_t ldy,
+                       int64_t cols, fp8_stream_t stream);
+
+/*
+ * fp8_expert_combine_backward -- the gradients of fp8_expert_combine.
+ *
+ *   dweights[t, k]  = sum over c of dy[t, c] x[slot(t, k), c]    (fp32; 0 without a slot)
+ *   dx[slot(t, k)]  = bf16(weights[t, k] dy[t])
+ *
+ * The sums' order follows from the sizes alone, so repeated calls give identical
+ * bits.  base's gradient is dy.  An FP8 layer takes the gradient of x in codes
+ * (fp8_expert_gather_cast_transpose_amax of dy with the weights) and passes
+ * dx NULL here.
+ *
+ * dy        device bf16 [tokens, cols], row stride lddy.
+ * x         device bf16 [rows, cols], row stride ldx, as in the forward.
+ * weights   device fp32 [tokens, top_k]; read for dx only.
+ * dweights  device fp32 [tokens, top_k], 4-byte aligned.
+ * dx        NULL, or device bf16 [rows, cols], row stride lddx.  May be x (same
+ *           pointer and stride); must not overlap dy or another x.
+ * Other constraints and errors as fp8_expert_gather.
+ */
+int fp8_expert_combine_backward(const fp8_expert_sizes_t *sizes, const void *plan,
+                                int64_t plan_bytes, const uint16_t *dy, int64_t lddy,
+                                const uint16_t *x, int64_t ldx, const float *weights,
+                                float *dweights, uint16_t *dx, int64_t lddx, int64_t cols,
+                                fp8_stream_t stream);
+
+/* One tensor of fp8_grad_norm. */
+typedef struct fp8_grad {
+    const void *grad;       /* device [n], 16-byte aligned                     */
+    int64_t n;              /* 0 .. 2^34                                       */
+    int32_t dtype;          /* fp8_dtype_t                                     */
+    int32_t reserved;       /* must be 0                                       */
+} fp8_grad_t;
+
+/* Device workspace (bytes) of fp8_grad_norm, the same for any tensors. */
+int64_t fp8_grad_norm_workspace_bytes(void);
+
+/*
+ * fp8_grad_norm -- the 2-norm of all gradients of a model, and what a clipped
+ * step needs of it.
+ *
+ *   *norm      = fp32(sqrt(sum of squares of all values))
+ *   *factor    = *norm > max_norm ? fp32(max_norm / *norm) : 1
+ *   *noop_flag = *norm is infinite or NaN ? 1 : 0
+ *
+ * Squares and sums are taken in 64 bits, in an order that follows from the
+ * tensors' sizes: identical bits on every call.  factor and noop_flag are
+ * grad_scale and noop_flag of fp8_adamw_step: a step whose gradients overflowed
+ * is then left out.
+ *
+ * grads      host array of `count` tensors (0 or more), read during the call.
+ * norm       device, 1 float.   factor, noop_flag   device, 1 float / int32, or NULL.
+ * workspace  device, 16-byte aligned, fp8_grad_norm_workspace_bytes bytes; its
+ *            contents on entry do not matter; calls that overlap on one race.
+ * max_norm   above 0; INFINITY never clips.
+ * One launch per 100 tensors, and one for the sum.
+ * Errors: FP8_ERR_NULL, FP8_ERR_SHAPE (n, workspace_bytes), FP8_ERR_ALIGN,
+ * FP8_ERR_ARG (dtype, count, reserved, max_norm), FP8_ERR_LAUNCH / FP8_ERR_DEVICE.
+ */
+int fp8_grad_norm(const fp8_grad_t *grads, int32_t count, float max_norm, float *norm,
+                  float *factor, int32_t *noop_flag, void *workspace, int64_t workspace_bytes,
+                  fp8_stream_t stream);
+
+/* Values per scale of a state in 8 bits. */
+#define FP8DSL_ADAMW_BLOCK 256
+
+/*
+ * One tensor of fp8_adamw_step: n values, stored one after another.
+ *
+ * The states m and v are fp32, or with m_scale and v_scale E4M3 codes: value i
+ * is the code's times scale[i / 256], a power of two.  Zeros (codes and scales)
+ * are the state before the first step in either form.
+ */
+typedef struct fp8_adamw_tensor {
+    void *param;            /* device [n], fp32 or bf16                        */
+    const void *grad;       /* device [n], fp32 or bf16                        */
+    void *m;                /* device [n], fp32 or codes                       */
+    void *v;                /* device [n], as m                                */
+    float *m_scale;         /* device [ceil(n / 256)], or NULL: fp32 states    */
+    float *v_scale;         /* device [ceil(n / 256)], NULL with m_scale       */
+    uint16_t *copy;         /* device [n] bf16 copy of an fp32 param, or NULL  */
+    int64_t n;              /* 0 .. 2^34                                       */
+    float weight_decay;     /* finite, not negative                            */
+    int32_t param_dtype;    /* fp8_dtype_t                                     */
+    int32_t grad_dtype;     /* fp8_dtype_t                                     */
+    int32_t reserved;       /* must be 0                                       */
+} fp8_adamw_tensor_t;
+
+/* What the tensors of a step share. */
+typedef struct fp8_adamw {
+    const float *lr;        /* device, 1 float                                 */
+    int64_t *steps;         /* device {steps taken, 0}, 8-byte aligned         */
+    double beta1;           /* 0 <= beta1 < 1                                  */
+    double beta2;           /* 0 <= beta2 < 1                                  */
+    double eps;             /* above 0 in fp32, finite                         */
+    uint64_t seed;          /* of the stochastic roundings                     */
+} fp8_adamw_t;
+
+/*
+ * fp8_adamw_step -- one step of AdamW over many tensors: the master weights of
+ * the linears, their biases, adapters.
+ *
+ * With t = steps[0] + 1, in fp32, every operation rounded (the factors from lr,
+ * beta1, beta2 and t in 64 bits first):
+ *
+ *   g = grad * *grad_scale                                  (grad without one)
+ *   m = beta1 m + (1 - beta1) g
+ *   v = beta2 v + ((1 - beta2) g) g
+ *   p = p (1 - lr weight_decay) - (lr / (1 - beta1^t) m) / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ *
+ * (the last quotient to within 2^-22 of itself), then steps[0] = t.
+ *
+ * Stored in 8 bits, m and v get new scales, the least power of two (2^-126 or
+ * more) that keeps each block's largest finite magnitude within 448, and are
+ * rounded stochastically, as bf16 parameters are: a magnitude between two
+ * neighbours of the format goes to floor(place + u / 65536) where place counts
+ * their distance from the lower one and u is a 16-bit random number.  Rounded to
+ * nearest instead, v would not fall (a step takes 1 - beta2 of it, the format's
+ * half step is 2^-4) and a bf16 parameter would not take small updates.  A v
+ * above 0 is never stored as 0; below 2^-6 after scaling the magnitudes are first
+ * rounded to multiples of 2^-29.  What is not finite is stored as the code 0x7F
+ * (NaN).  The update of p uses m and v before they are stored.  copy is p rounded
+ * to nearest even.
+ *
+ * Random numbers: Philox4x32 with 7 rounds (see fp8_dropout_desc), key seed,
+ * counter words (group, 2 i + s, t low, t high) for tensor i of the array.
+ * s = 0: value j of a state in 8 bits takes word j % 4 of group j / 4, its low
+ * half for m, its high half for v; s = 1: value j of a bf16 parameter takes half
+ * j % 2 of word (j % 8) / 2 of group j / 8.
+ *
+ * tensors    host array of `count` tensors (0 or more), read during the call.
+ *            Pointers 16-byte aligned, scales 4-byte.  No two tensors may share
+ *            what is written; types may differ from tensor to tensor.
+ * grad_scale NULL, or device, 1 float.
+ * noop_flag  as fp8_cast_transpose_amax: skips the whole step, its count included.
+ * lr, steps and grad_scale are read on the device when the kernels run, so a
+ * captured step follows a schedule.  Calls that overlap on one `steps` race.
+ * One launch per 48 tensors.
+ * Errors: FP8_ERR_NULL, FP8_ERR_SHAPE (n), FP8_ERR_ALIGN, FP8_ERR_ARG (betas,
+ * eps, weight_decay, dtypes, count, reserved, a copy of a bf16 param, one scale
+ * alone), FP8_ERR_LAUNCH / FP8_ERR_DEVICE.
+ */
+int fp8_adamw_step(const fp8_adamw_t *opt, const fp8_adamw_tensor_t *tensors, int32_t count,
+                   const float *grad_scale, const int32_t *noop_flag, fp8_stream_t stream);
 
 /* Human-readable name of a status code (static storage). */
 const char *fp8_status_string(int status);
