@@ -1,0 +1,132 @@
+"""The optimizer on the CPU: the reference against torch's AdamW in float64, the
+stochastic rounding's mean over all its numbers, and every refusal (nothing
+reaches a device)."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import delayed_scaling_linear_amd as dsl
+from tests import adamw_reference as ref
+
+F = np.float32
+
+
+def test_reference_against_torch():
+    """Ten steps with weight decay.  The reference rounds m, v and the gradient's
+    scaling to fp32: 8 roundings of 2^-24 a step in m or v, relative to their largest
+    terms, and an update is a few of them away; 1e-5 of the update's size (lr per
+    step) covers ten steps of it."""
+    r = np.random.default_rng(0)
+    n, lr, wd, b1, b2, eps = 500, 1e-2, 0.1, 0.9, 0.99, 1e-8
+    p = r.standard_normal(n)
+    t = torch.tensor(p, dtype=torch.float64, requires_grad=True)
+    opt = torch.optim.AdamW([t], lr=lr, betas=(b1, b2), eps=eps, weight_decay=wd)
+    m, v = np.zeros(n, F), np.zeros(n, F)
+    for step in range(1, 11):
+        g = r.standard_normal(n).astype(F)
+        t.grad = torch.tensor(g, dtype=torch.float64)
+        opt.step()
+        m, v, p, _ = ref.step(p, g, m, v, step, lr, wd, b1, b2, eps)
+        assert np.abs(p - t.detach().numpy()).max() <= 1e-5 * lr * step
+
+
+def test_mean_of_the_rounding():
+    """Over all 65536 numbers the codes' mean is the value: the lower neighbour
+    plus ceil or floor of place * 65536 of its 65536 parts, so within 2^-16 of the
+    neighbours' distance."""
+    r = np.random.default_rng(1)
+    u = np.arange(65536)
+    # As the encoder leaves them: fp32 values, below 2^-6 multiples of 2^-29.
+    for y in np.concatenate([r.uniform(0, 448, 12), 2.0 ** r.uniform(-12, 8, 12), [448.0, 0.0]]):
+        y = np.rint(y * 2.0 ** 29) * 2.0 ** -29 if y < 2.0 ** -6 else float(F(y))
+        got = ref.VALUES[ref.place(np.full(u.size, y), u, False)]
+        step = 2.0 ** (np.floor(np.log2(max(y, 2.0 ** -6))) - 3)
+        assert abs(got.mean() - y) <= step * 2.0 ** -16 * 1.001
+        assert got.max() - got.min() <= step * 1.001 and got.max() <= 448.0
+
+
+def test_scales():
+    x = np.zeros(4 * 256, F)
+    x[0], x[256], x[512], x[768] = 448.0, 448.0000305, 1e-45, 3.4e38
+    assert ref.scales_of(x).tolist() == [1.0, 2.0, 2.0 ** -126, 2.0 ** 120]
+    assert (ref.VALUES[[0x7E, 0x01, 0x08]] == [448.0, 2.0 ** -9, 2.0 ** -6]).all()
+
+
+def _tensor(param=0x10000, grad=0x20000, m=0x30000, v=0x40000, ms=None, vs=None, copy=None, n=100,
+            wd=0.0, pd=1, gd=1, reserved=0):
+    return dsl._AdamWTensorDesc(param, grad, m, v, ms, vs, copy, n, wd, pd, gd, reserved)
+
+
+def _opt(lr=0x50000, steps=0x60000, b1=0.9, b2=0.999, eps=1e-8):
+    return dsl._AdamWDesc(lr, steps, b1, b2, eps, 7)
+
+
+def test_step_refusals():
+    L = dsl.lib()
+
+    def call(t=_tensor(), opt=_opt(), count=1, scale=None, flag=None, tensors=True):
+        array = (dsl._AdamWTensorDesc * 2)(_tensor(), t) if tensors else None
+        return L.fp8_adamw_step(None if opt is None else ctypes.byref(opt), array,
+                                2 if count == 1 else count, scale, flag, None)
+
+    assert call(opt=None) == -1 and call(tensors=False) == -1
+    assert call(opt=_opt(lr=None)) == -1 and call(opt=_opt(steps=None)) == -1
+    assert call(opt=_opt(lr=0x50002)) == -3 and call(opt=_opt(steps=0x60004)) == -3
+    assert call(scale=0x70001) == -3 and call(flag=0x70002) == -3
+    assert call(count=-1) == -5
+    for bad in (dict(b1=1.0), dict(b1=-0.1), dict(b1=float("nan")), dict(b2=1.0), dict(b2=-1e-9),
+                dict(eps=0.0), dict(eps=-1e-8), dict(eps=1e-60), dict(eps=float("inf")),
+                dict(eps=float("nan")), dict(eps=1e39)):
+        assert call(opt=_opt(**bad)) == -5, bad
+    for bad in (dict(pd=2), dict(gd=-1), dict(reserved=1), dict(wd=-0.1), dict(wd=float("inf")),
+                dict(wd=float("nan")), dict(copy=0x80000, pd=0), dict(ms=0x80000),
+                dict(vs=0x80000)):
+        assert call(t=_tensor(**bad)) == -5, bad
+    assert call(t=_tensor(n=-1)) == -2 and call(t=_tensor(n=(1 << 34) + 1)) == -2
+    for name in ("param", "grad", "m", "v"):
+        assert call(t=_tensor(**{name: None})) == -1
+        assert call(t=_tensor(**{name: 0x10008})) == -3
+    assert call(t=_tensor(copy=0x80008)) == -3
+    assert call(t=_tensor(ms=0x80002, vs=0x90000)) == -3
+    assert call(t=_tensor(ms=0x80000, vs=0x90002)) == -3
+
+
+def test_norm_refusals():
+    L = dsl.lib()
+    need = dsl.fp8_grad_norm_workspace_bytes()
+
+    def call(g=0x10000, n=100, dtype=1, reserved=0, count=1, most=1.0, norm=0x20000, factor=None,
+             flag=None, ws=0x30000, size=need, grads=True):
+        array = (dsl._GradDesc * 1)((g, n, dtype, reserved)) if grads else None
+        return L.fp8_grad_norm(array, count, most, norm, factor, flag, ws, size, None)
+
+    for most in (0.0, -1.0, float("nan")):
+        assert call(most=most) == -5
+    assert call(count=-1) == -5 and call(dtype=2) == -5 and call(reserved=1) == -5
+    assert call(norm=None) == -1 and call(ws=None) == -1 and call(grads=False) == -1
+    assert call(g=None) == -1
+    assert call(g=0x10008) == -3 and call(norm=0x20002) == -3 and call(factor=0x20002) == -3
+    assert call(flag=0x20001) == -3 and call(ws=0x30008) == -3
+    assert call(size=need - 1) == -2 and call(n=-1) == -2 and call(n=(1 << 34) + 1) == -2
+
+
+def test_python_refusals():
+    p, g = torch.zeros(300), torch.zeros(300)
+    with pytest.raises(ValueError):
+        dsl.AdamWTensor.zeros(p, g, bits=16)
+    t = dsl.AdamWTensor.zeros(p, g, bits=8)
+    assert t.m.dtype == torch.uint8 and t.m_scale.shape == (2,) and t.m_scale.sum() == 0
+    with pytest.raises(ValueError):                     # not on a device
+        t.desc()
+    for change, error in ((dict(grad=g.double()), TypeError), (dict(param=p.half()), TypeError),
+                          (dict(v_scale=None), ValueError),
+                          (dict(param=p.bfloat16(), copy=p.bfloat16()), TypeError)):
+        fields = dict(param=p, grad=g, m=t.m, v=t.v, m_scale=t.m_scale, v_scale=t.v_scale)
+        with pytest.raises(error):
+            dsl.AdamWTensor(**{**fields, **change}).desc()
+    with pytest.raises(TypeError):
+        dsl.fp8_grad_norm([g.half()], torch.zeros(1), torch.zeros(8, dtype=torch.uint8))
+    with pytest.raises(ValueError):
+        dsl.fp8_grad_norm([g], torch.zeros(0), torch.zeros(8, dtype=torch.uint8))
