@@ -219,11 +219,10 @@ struct StepTensor {
     int64_t n;
     int32_t first;           // its first tile
     float weight_decay;
-    int32_t types;           // 1: bf16 param, 2: bf16 grad, 4: states in 8 bits
+    int32_t index;           // its place in the call
 };
 struct StepArgs {
     int count, tiles;
-    int base;                // tensors of earlier launches
     int last;                // the launch that counts the step
     const float *lr, *grad_scale;
     int64_t *steps;
@@ -243,8 +242,9 @@ __device__ __forceinline__ double power(double x, uint64_t n) {
     return r;
 }
 
+// What the step's values share.
 struct Factors {
-    float grad, step, root, lr;
+    float b1, c1, b2, c2, eps, grad, step, root, decay;
 };
 
 // Bits of the power of two that scales a block whose largest finite magnitude is
@@ -254,154 +254,174 @@ __device__ __forceinline__ uint32_t scale_bits(uint32_t most) {
     return (uint32_t)max(e - 8, 1) << 23;
 }
 
+// The maximum over the wave (all lanes active): within rows of 16, then across.
 __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-#pragma unroll
-    for (int m = 32; m >= 1; m >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, m, 64));
-    return v;
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x111, 0xF, 0xF, false));
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x112, 0xF, 0xF, false));
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x114, 0xF, 0xF, false));
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x118, 0xF, 0xF, false));
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xA, 0xF, false));
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xC, 0xF, false));
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 
-// The E4M3 code of x (|x| <= 448, or not finite), u a 16-bit number.  An fp32 value
-// from 2^-6 on has 20 bits below the code's three: adding u there and cutting rounds
-// up with the probability of the part cut.  Below 2^-6 the codes are as far
-// apart as from 2^-6 to 2^-5: the value is moved there.
-template <bool KEEP>
+// The E4M3 code of a magnitude x <= 448, u a 16-bit number.  An fp32 value from 2^-6
+// on has 20 bits below the code's three: adding u there and cutting rounds up with
+// the probability of the part cut.  Below 2^-6 the codes are as far apart as from
+// 2^-6 to 2^-5: x is moved there.  Each form is the larger where it holds.
 __device__ __forceinline__ uint32_t code_of(float x, uint32_t u) {
-    const uint32_t bits = __float_as_uint(x), mag = bits & 0x7FFFFFFFu;
-    const float ax = __uint_as_float(mag);
-    const bool low = ax < 0x1p-6f;
-    const uint32_t y = low ? __float_as_uint(ax + 0x1p-6f) : mag;
-    uint32_t code = ((y + (u << 4)) >> 20) - (low ? 968u : 960u);
-    if constexpr (KEEP) code = code == 0u && mag != 0u ? 1u : code;
-    code |= (bits >> 24) & 0x80u;
-    return mag >= 0x7F800000u ? 0x7Fu : code;
+    const int high = (int)(__float_as_uint(x) - (960u << 20));
+    const int low = (int)(__float_as_uint(x + 0x1p-6f) - (968u << 20));
+    return ((uint32_t)max(high, low) + (u << 4)) >> 20;
 }
 
-// One block of 256 values of a tensor: a lane's four begin at element i.
-template <typename P, typename G, bool STATE8>
-struct Block {
-    float p[4], g[4], m[4], v[4];
-    uint32_t mc, vc;
-    float ms, vs;
-
-    __device__ __forceinline__ void load(const StepTensor &t, int64_t i, int left) {
-        if (left <= 0) {
+// Four codes of a moment: SIGNED with the values' signs, else a value above 0 gets
+// a code above 0.  SPECIAL: what is not finite becomes 0x7F.
+template <bool SIGNED, bool SPECIAL>
+__device__ __forceinline__ uint32_t codes_of(const float (&x)[4], float inverse,
+                                             const uint32_t (&w)[4]) {
+    uint32_t out = 0;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) p[k] = g[k] = m[k] = v[k] = 0.0f;
-            mc = vc = 0;
-            ms = vs = 0.0f;
-            return;
-        }
-        Four<P>::load(t.param, i, left, p);
-        Four<G>::load(t.grad, i, left, g);
-        if constexpr (STATE8) {
-            mc = Four<uint8_t>::load(t.m, i, left);
-            vc = Four<uint8_t>::load(t.v, i, left);
-            ms = t.m_scale[i / BLOCK];
-            vs = t.v_scale[i / BLOCK];
+    for (int k = 0; k < 4; ++k) {
+        const float y = x[k] * inverse;
+        const uint32_t bits = __float_as_uint(y), u = SIGNED ? w[k] & 0xFFFFu : w[k] >> 16;
+        uint32_t code = code_of(SIGNED ? __uint_as_float(bits & 0x7FFFFFFFu) : y, u);
+        if constexpr (SIGNED) code |= (bits >> 24) & 0x80u;
+        else code = max(code, min(bits, 1u));
+        if constexpr (SPECIAL) code = (bits & 0x7F800000u) == 0x7F800000u ? 0x7Fu : code;
+        out |= code << (8 * k);
+    }
+    return out;
+}
+
+// Stores a moment's new values; returns its codes and sets the block's scale.
+template <bool SIGNED>
+__device__ __forceinline__ uint32_t encode(const float (&x)[4], const uint32_t (&w)[4],
+                                           uint32_t &scale) {
+    uint32_t mag[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        mag[k] = SIGNED ? __float_as_uint(x[k]) & 0x7FFFFFFFu : __float_as_uint(x[k]);
+    uint32_t most = wave_max(max(max(mag[0], mag[1]), max(mag[2], mag[3])));
+    if (most >= 0x7F800000u) {                           // rare, the same for the wave
+        most = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            most = max(most, (mag[k] & 0x7FFFFFFFu) < 0x7F800000u ? mag[k] : 0u);
+        scale = scale_bits(wave_max(most));
+        return codes_of<SIGNED, true>(x, __uint_as_float((254u << 23) - scale), w);
+    }
+    scale = scale_bits(most);
+    // 1 / 2^e: e and its negative are both exponents of normal numbers.
+    return codes_of<SIGNED, false>(x, __uint_as_float((254u << 23) - scale), w);
+}
+
+__device__ __forceinline__ void decode(uint32_t codes, float scale, float (&x)[4]) {
+    x[0] = __builtin_amdgcn_cvt_f32_fp8((int)codes, 0) * scale;
+    x[1] = __builtin_amdgcn_cvt_f32_fp8((int)codes, 1) * scale;
+    x[2] = __builtin_amdgcn_cvt_f32_fp8((int)codes, 2) * scale;
+    x[3] = __builtin_amdgcn_cvt_f32_fp8((int)codes, 3) * scale;
+}
+
+// sqrt within 2^-23 of itself: the instruction does not take denormal numbers.
+__device__ __forceinline__ float root_of(float x) {
+    const bool small = x < 0x1p-96f;
+    const float r = __builtin_amdgcn_sqrtf(small ? x * 0x1p32f : x);
+    return small ? r * 0x1p-16f : r;
+}
+
+// N blocks of 256 values of a tensor, a wave's; FULL: all of their values exist.
+template <typename P, typename G, bool STATE8, int N, bool FULL>
+__device__ __forceinline__ void step_blocks(const StepTensor &t, const Factors &f,
+                                            const DropoutKey &key, int64_t i0) {
+#pragma clang fp contract(off)
+    const int lane = threadIdx.x & 63;
+    float p[N][4], g[N][4], m[N][4], v[N][4], ms[N], vs[N];
+    uint32_t mc[N], vc[N];
+    int left[N];
+#pragma unroll
+    for (int s = 0; s < N; ++s) {
+        const int64_t b = i0 + s * BLOCK, i = b + 4 * lane;
+        left[s] = FULL ? 4 : (int)max((int64_t)0, min((int64_t)4, t.n - i));
+        if (FULL || left[s] > 0) {
+            Four<P>::load(t.param, i, left[s], p[s]);
+            Four<G>::load(t.grad, i, left[s], g[s]);
+            if constexpr (STATE8) {
+                mc[s] = Four<uint8_t>::load(t.m, i, left[s]);
+                vc[s] = Four<uint8_t>::load(t.v, i, left[s]);
+                ms[s] = t.m_scale[b / BLOCK];
+                vs[s] = t.v_scale[b / BLOCK];
+            } else {
+                Four<float>::load(t.m, i, left[s], m[s]);
+                Four<float>::load(t.v, i, left[s], v[s]);
+            }
         } else {
-            Four<float>::load(t.m, i, left, m);
-            Four<float>::load(t.v, i, left, v);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) p[s][k] = g[s][k] = m[s][k] = v[s][k] = 0.0f;
+            mc[s] = vc[s] = 0;
+            ms[s] = vs[s] = 0.0f;
         }
     }
-
-    __device__ __forceinline__ void step(const StepArgs &args, const StepTensor &t, int item,
-                                         uint64_t steps, const Factors &f, float decay, int64_t i,
-                                         int left) {
-#pragma clang fp contract(off)
+#pragma unroll
+    for (int s = 0; s < N; ++s) {
+        const int64_t b = i0 + s * BLOCK, i = b + 4 * lane;
         if constexpr (STATE8) {
-            m[0] = __builtin_amdgcn_cvt_f32_fp8((int)mc, 0) * ms;
-            m[1] = __builtin_amdgcn_cvt_f32_fp8((int)mc, 1) * ms;
-            m[2] = __builtin_amdgcn_cvt_f32_fp8((int)mc, 2) * ms;
-            m[3] = __builtin_amdgcn_cvt_f32_fp8((int)mc, 3) * ms;
-            v[0] = __builtin_amdgcn_cvt_f32_fp8((int)vc, 0) * vs;
-            v[1] = __builtin_amdgcn_cvt_f32_fp8((int)vc, 1) * vs;
-            v[2] = __builtin_amdgcn_cvt_f32_fp8((int)vc, 2) * vs;
-            v[3] = __builtin_amdgcn_cvt_f32_fp8((int)vc, 3) * vs;
+            decode(mc[s], ms[s], m[s]);
+            decode(vc[s], vs[s], v[s]);
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const float gk = g[k] * f.grad;
-            m[k] = m[k] * args.b1 + gk * args.c1;
-            v[k] = v[k] * args.b2 + (gk * args.c2) * gk;
-            p[k] = p[k] * decay - (m[k] * f.step) / (sqrtf(v[k]) * f.root + args.eps);
+            const float gk = g[s][k] * f.grad;
+            m[s][k] = m[s][k] * f.b1 + gk * f.c1;
+            v[s][k] = v[s][k] * f.b2 + (gk * f.c2) * gk;
+            const float d = root_of(v[s][k]) * f.root + f.eps;
+            p[s][k] = p[s][k] * f.decay - (m[s][k] * f.step) * __builtin_amdgcn_rcpf(d);
         }
-        const DropoutKey key(args.seed_lo, args.seed_hi, steps);
+        uint32_t sm, sv;
         if constexpr (STATE8) {
-            uint32_t most_m = 0, most_v = 0;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const uint32_t a = __float_as_uint(m[k]) & 0x7FFFFFFFu;
-                const uint32_t b = __float_as_uint(v[k]) & 0x7FFFFFFFu;
-                most_m = max(most_m, a < 0x7F800000u ? a : 0u);
-                most_v = max(most_v, b < 0x7F800000u ? b : 0u);
-            }
-            const uint32_t sm = scale_bits(wave_max(most_m)), sv = scale_bits(wave_max(most_v));
-            // 1 / 2^e: e and its negative are both exponents of normal numbers.
-            const float im = __uint_as_float((254u << 23) - sm);
-            const float iv = __uint_as_float((254u << 23) - sv);
             uint32_t w[4];
-            dropout_words(key, ((uint64_t)(2u * (uint32_t)item) << 32) | (uint64_t)(i / 4), w);
-            mc = vc = 0;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                mc |= code_of<false>(m[k] * im, w[k] & 0xFFFFu) << (8 * k);
-                vc |= code_of<true>(v[k] * iv, w[k] >> 16) << (8 * k);
-            }
-            if (left <= 0) return;
-            Four<uint8_t>::store(t.m, i, left, mc);
-            Four<uint8_t>::store(t.v, i, left, vc);
-            if (i % BLOCK == 0) {
-                t.m_scale[i / BLOCK] = __uint_as_float(sm);
-                t.v_scale[i / BLOCK] = __uint_as_float(sv);
+            dropout_words(key, ((uint64_t)(2u * (uint32_t)t.index) << 32) | (uint64_t)(i / 4), w);
+            mc[s] = encode<true>(m[s], w, sm);
+            vc[s] = encode<false>(v[s], w, sv);
+        }
+        if (!FULL && left[s] <= 0) continue;
+        if constexpr (STATE8) {
+            Four<uint8_t>::store(t.m, i, left[s], mc[s]);
+            Four<uint8_t>::store(t.v, i, left[s], vc[s]);
+            if (lane == 0) {
+                t.m_scale[b / BLOCK] = __uint_as_float(sm);
+                t.v_scale[b / BLOCK] = __uint_as_float(sv);
             }
         } else {
-            if (left <= 0) return;
-            Four<float>::store(t.m, i, left, m);
-            Four<float>::store(t.v, i, left, v);
+            Four<float>::store(t.m, i, left[s], m[s]);
+            Four<float>::store(t.v, i, left[s], v[s]);
         }
         if constexpr (std::is_same<P, float>::value) {
-            Four<float>::store(t.param, i, left, p);
+            Four<float>::store(t.param, i, left[s], p[s]);
             if (t.copy) {
-                const uint32_t bits[4] = {bf16_bits(p[0]), bf16_bits(p[1]), bf16_bits(p[2]),
-                                          bf16_bits(p[3])};
-                Four<uint16_t>::store(t.copy, i, left, bits);
+                const uint32_t bits[4] = {bf16_bits(p[s][0]), bf16_bits(p[s][1]),
+                                          bf16_bits(p[s][2]), bf16_bits(p[s][3])};
+                Four<uint16_t>::store(t.copy, i, left[s], bits);
             }
         } else {
             uint32_t w[4], bits[4];
-            dropout_words(key, ((uint64_t)(2u * (uint32_t)item + 1u) << 32) | (uint64_t)(i / 8), w);
+            dropout_words(key, ((uint64_t)(2u * (uint32_t)t.index + 1u) << 32) | (uint64_t)(i / 8),
+                          w);
+            // An even lane has the first half of its group of eight.
+            const uint32_t word[2] = {lane & 1 ? w[2] : w[0], lane & 1 ? w[3] : w[1]};
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const uint32_t word = (i & 4) ? w[2 + k / 2] : w[k / 2];
-                const uint32_t u = k & 1 ? word >> 16 : word & 0xFFFFu;
-                const uint32_t b = __float_as_uint(p[k]);
-                const bool finite = (b & 0x7F800000u) != 0x7F800000u;
-                bits[k] = p[k] != p[k] ? 0x7FC0u : (b + (finite ? u : 0u)) >> 16;
+                const uint32_t u = k & 1 ? word[k / 2] >> 16 : word[k / 2] & 0xFFFFu;
+                const uint32_t x = __float_as_uint(p[s][k]);
+                const bool finite = (x & 0x7F800000u) != 0x7F800000u;
+                bits[k] = p[s][k] != p[s][k] ? 0x7FC0u : (x + (finite ? u : 0u)) >> 16;
             }
-            Four<uint16_t>::store(t.param, i, left, bits);
+            Four<uint16_t>::store(t.param, i, left[s], bits);
         }
     }
-};
-
-template <typename P, typename G, bool STATE8>
-__device__ __forceinline__ void step_tile(const StepArgs &args, int item, uint64_t steps,
-                                          const Factors &f, int64_t i0) {
-    const StepTensor &t = args.t[item];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const float decay = (float)(1.0 - (double)f.lr * (double)t.weight_decay);
-    Block<P, G, STATE8> b[STEP_BLOCKS];
-    int64_t i[STEP_BLOCKS];
-    int left[STEP_BLOCKS];
-#pragma unroll
-    for (int s = 0; s < STEP_BLOCKS; ++s) {
-        i[s] = i0 + (wave * STEP_BLOCKS + s) * BLOCK + 4 * lane;
-        left[s] = (int)max((int64_t)0, min((int64_t)4, t.n - i[s]));
-        b[s].load(t, i[s], left[s]);
-    }
-#pragma unroll
-    for (int s = 0; s < STEP_BLOCKS; ++s)
-        b[s].step(args, t, args.base + item, steps, f, decay, i[s], left[s]);
 }
 
+template <typename P, typename G, bool STATE8>
 __global__ __launch_bounds__(THREADS) void adamw_kernel(const StepArgs args,
                                                         const int32_t *__restrict__ noop) {
     if (noop != nullptr && *noop != 0) return;
@@ -409,23 +429,22 @@ __global__ __launch_bounds__(THREADS) void adamw_kernel(const StepArgs args,
     if (threadIdx.x == 0) taken = args.steps[0];
     __syncthreads();
     const uint64_t steps = (uint64_t)taken + 1;
-    Factors f;
-    f.lr = *args.lr;
+    const double lr = *args.lr;
+    Factors f = {args.b1, args.c1, args.b2, args.c2, args.eps};
     f.grad = args.grad_scale ? *args.grad_scale : 1.0f;
-    f.step = (float)((double)f.lr / (1.0 - power(args.beta1, steps)));
+    f.step = (float)(lr / (1.0 - power(args.beta1, steps)));
     f.root = (float)(1.0 / sqrt(1.0 - power(args.beta2, steps)));
+    const DropoutKey key(args.seed_lo, args.seed_hi, steps);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     for (int tile = blockIdx.x; tile < args.tiles; tile += gridDim.x) {
-        const int item = tensor_of(args, tile);
-        const int64_t i0 = (int64_t)(tile - args.t[item].first) * STEP_TILE;
-        switch (args.t[item].types) {
-            case 0: step_tile<float, float, false>(args, item, steps, f, i0); break;
-            case 1: step_tile<uint16_t, float, false>(args, item, steps, f, i0); break;
-            case 2: step_tile<float, uint16_t, false>(args, item, steps, f, i0); break;
-            case 3: step_tile<uint16_t, uint16_t, false>(args, item, steps, f, i0); break;
-            case 4: step_tile<float, float, true>(args, item, steps, f, i0); break;
-            case 5: step_tile<uint16_t, float, true>(args, item, steps, f, i0); break;
-            case 6: step_tile<float, uint16_t, true>(args, item, steps, f, i0); break;
-            default: step_tile<uint16_t, uint16_t, true>(args, item, steps, f, i0); break;
+        const StepTensor &t = args.t[tensor_of(args, tile)];
+        const int64_t i0 = (int64_t)(tile - t.first) * STEP_TILE + wave * STEP_BLOCKS * BLOCK;
+        f.decay = (float)(1.0 - lr * (double)t.weight_decay);
+        if (t.n - i0 >= STEP_BLOCKS * BLOCK) {
+            step_blocks<P, G, STATE8, STEP_BLOCKS, true>(t, f, key, i0);
+        } else {
+            for (int64_t i = i0; i < min(t.n, i0 + STEP_BLOCKS * BLOCK); i += BLOCK)
+                step_blocks<P, G, STATE8, 1, false>(t, f, key, i);
         }
     }
     // The last workgroup to come here counts the step: all have read the count.
@@ -469,6 +488,15 @@ hipError_t launch_grad_norm(const fp8_grad_t *grads, int count, float max_norm, 
 
 hipError_t launch_adamw(const fp8_adamw_t &opt, const fp8_adamw_tensor_t *tensors, int count,
                         const float *grad_scale, const int32_t *noop, hipStream_t stream) {
+    const auto kind_of = [](const fp8_adamw_tensor_t &t) {
+        return (t.param_dtype == FP8_DTYPE_BF16 ? 1 : 0) | (t.grad_dtype == FP8_DTYPE_BF16 ? 2 : 0) |
+               (t.m_scale ? 4 : 0);
+    };
+    void (*const kernels[8])(StepArgs, const int32_t *) = {
+        adamw_kernel<float, float, false>,  adamw_kernel<uint16_t, float, false>,
+        adamw_kernel<float, uint16_t, false>, adamw_kernel<uint16_t, uint16_t, false>,
+        adamw_kernel<float, float, true>,   adamw_kernel<uint16_t, float, true>,
+        adamw_kernel<float, uint16_t, true>, adamw_kernel<uint16_t, uint16_t, true>};
     int cus = 0;
     if (hipError_t e = current_cu_count(&cus)) return e;
     StepArgs args;
@@ -484,24 +512,34 @@ hipError_t launch_adamw(const fp8_adamw_t &opt, const fp8_adamw_tensor_t *tensor
     args.eps = (float)opt.eps;
     args.seed_lo = (uint32_t)opt.seed;
     args.seed_hi = (uint32_t)(opt.seed >> 32);
-    args.base = 0;
-    do {
-        args.count = std::min(STEP_TENSORS, count - args.base);
-        args.last = args.base + args.count == count;
-        args.tiles = 0;
-        for (int i = 0; i < args.count; ++i) {
-            const fp8_adamw_tensor_t &t = tensors[args.base + i];
-            args.t[i] = {t.param, t.grad, t.m, t.v, t.m_scale, t.v_scale, t.copy, t.n, args.tiles,
-                         t.weight_decay,
-                         (t.param_dtype == FP8_DTYPE_BF16 ? 1 : 0) |
-                             (t.grad_dtype == FP8_DTYPE_BF16 ? 2 : 0) | (t.m_scale ? 4 : 0)};
-            args.tiles += (int)((t.n + STEP_TILE - 1) / STEP_TILE);
-        }
-        const int grid = std::max(1, std::min(args.tiles, 8 * cus));
-        hipLaunchKernelGGL(adamw_kernel, dim3((unsigned)grid), dim3(THREADS), 0, stream, args, noop);
-        if (hipError_t e = hipGetLastError()) return e;
-        args.base += args.count;
-    } while (args.base < count);
+    // A launch holds tensors of one combination of types; the last one counts the step.
+    int kinds[8] = {};
+    for (int i = 0; i < count; ++i)
+        if (tensors[i].n > 0) ++kinds[kind_of(tensors[i])];
+    int left = 0;
+    for (int kind = 0; kind < 8; ++kind) left += kinds[kind];
+    for (int kind = 0; kind < 8; ++kind) {
+        if (kinds[kind] == 0 && !(left == 0 && kind == 0)) continue;
+        int at = 0;
+        do {
+            args.count = args.tiles = 0;
+            for (; at < count && args.count < STEP_TENSORS; ++at) {
+                const fp8_adamw_tensor_t &t = tensors[at];
+                if (t.n == 0 || kind_of(t) != kind) continue;
+                args.t[args.count++] = {t.param, t.grad, t.m, t.v, t.m_scale, t.v_scale, t.copy, t.n,
+                                        args.tiles, t.weight_decay, at};
+                args.tiles += (int)((t.n + STEP_TILE - 1) / STEP_TILE);
+            }
+            kinds[kind] -= args.count;
+            left -= args.count;
+            args.last = left == 0;
+            const int grid = std::max(1, std::min(args.tiles, 8 * cus));
+            hipLaunchKernelGGL(kernels[kind], dim3((unsigned)grid), dim3(THREADS), 0, stream, args,
+                               noop);
+            if (hipError_t e = hipGetLastError()) return e;
+        } while (kinds[kind] > 0);
+        if (left == 0) break;
+    }
     return hipSuccess;
 }
 

@@ -1023,7 +1023,7 @@ typedef struct fp8_adamw {
     int64_t *steps;         /* device {steps taken, 0}, 8-byte aligned         */
     double beta1;           /* 0 <= beta1 < 1                                  */
     double beta2;           /* 0 <= beta2 < 1                                  */
-    double eps;             /* above 0 in fp32, finite                         */
+    double eps;             /* a normal number in fp32, 2^-126 or more         */
     uint64_t seed;          /* of the stochastic roundings                     */
 } fp8_adamw_t;
 
@@ -1066,7 +1066,7 @@ typedef struct fp8_adamw {
  * noop_flag  as fp8_cast_transpose_amax: skips the whole step, its count included.
  * lr, steps and grad_scale are read on the device when the kernels run, so a
  * captured step follows a schedule.  Calls that overlap on one `steps` race.
- * One launch per 48 tensors.
+ * One launch per 48 tensors of the same types.
  * Errors: FP8_ERR_NULL, FP8_ERR_SHAPE (n), FP8_ERR_ALIGN, FP8_ERR_ARG (betas,
  * eps, weight_decay, dtypes, count, reserved, a copy of a bf16 param, one scale
  * alone), FP8_ERR_LAUNCH / FP8_ERR_DEVICE.
