@@ -11,7 +11,7 @@ namespace fp8dsl {
 // Values of one tensor at most: the random numbers' group fits 32 bits.
 constexpr int64_t kTensorMost = (int64_t)1 << 34;
 // Partial sums of the norm, one per workgroup at most.
-constexpr int kNormParts = 1024;
+constexpr int kNormParts = 2048;
 
 hipError_t launch_grad_norm(const fp8_grad_t *grads, int count, float max_norm, float *norm,
                             float *factor, int32_t *flag, double *parts, hipStream_t stream);

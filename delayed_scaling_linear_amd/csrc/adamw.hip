@@ -108,9 +108,9 @@ struct Four<uint8_t> {
 
 // ---- the norm ----------------------------------------------------------------
 
-// Values of a tile: a lane takes NORM_LANE of them, four at a time.
-constexpr int NORM_STEPS = 8;
-constexpr int NORM_TILE = THREADS * 4 * NORM_STEPS;
+// Pieces of 16 bytes that a lane takes at once; a tile is a workgroup's.
+constexpr int NORM_STEPS = 4;
+constexpr int64_t NORM_TILE_BYTES = THREADS * 16 * NORM_STEPS;
 constexpr int NORM_TENSORS = 100;
 
 struct NormTensor {
@@ -144,35 +144,64 @@ __device__ __forceinline__ double wave_sum(double v) {
     return v;
 }
 
-template <typename T>
-__device__ __forceinline__ void add_squares(const NormTensor &t, int64_t i0, double (&sum)[4]) {
-    float v[NORM_STEPS][4];
+__device__ __forceinline__ void add_square(float x, double &sum) {
+    sum = fma((double)x, (double)x, sum);
+}
+
+// Adds the squares of tile `tile` of a tensor of 4-byte or 2-byte values.
+template <bool BF16, bool FULL>
+__device__ __forceinline__ void add_tile(const NormTensor &t, int tile, double (&sum)[4]) {
+    constexpr int E = BF16 ? 8 : 4;                      // values of 16 bytes
+    const int64_t i0 = tile * (NORM_TILE_BYTES / 16 * E) + E * threadIdx.x;
+    u32x4 v[NORM_STEPS];
 #pragma unroll
     for (int s = 0; s < NORM_STEPS; ++s) {
-        const int64_t i = i0 + (int64_t)s * THREADS * 4 + 4 * threadIdx.x;
-        const int left = (int)min((int64_t)4, t.n - i);
-        if (left > 0) {
-            Four<T>::load(t.grad, i, left, v[s]);
-        } else {
+        const int64_t i = i0 + s * THREADS * E;
+        v[s] = u32x4{0u, 0u, 0u, 0u};
+        if (FULL || i + E <= t.n) {
+            v[s] = *reinterpret_cast<const u32x4 *>(static_cast<const char *>(t.grad) +
+                                                    i * (16 / E));
+        } else if (BF16) {
+            const uint16_t *at = static_cast<const uint16_t *>(t.grad);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) v[s][k] = 0.0f;
+            for (int k = 0; k < E; ++k)
+                if (i + k < t.n) v[s][k / 2] |= (uint32_t)at[i + k] << (16 * (k & 1));
+        } else {
+            const uint32_t *at = static_cast<const uint32_t *>(t.grad);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (i + k < t.n) v[s][k] = at[i + k];
         }
     }
 #pragma unroll
     for (int s = 0; s < NORM_STEPS; ++s)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) sum[k] = fma((double)v[s][k], (double)v[s][k], sum[k]);
+        for (int k = 0; k < 4; ++k) {
+            if constexpr (BF16) {
+                add_square(__uint_as_float(v[s][k] << 16), sum[k]);
+                add_square(__uint_as_float(v[s][k] & 0xFFFF0000u), sum[k]);
+            } else {
+                add_square(__uint_as_float(v[s][k]), sum[k]);
+            }
+        }
 }
 
+// Each workgroup takes a run of tiles, so it looks for its first tensor only.
 __global__ __launch_bounds__(THREADS) void grad_norm_kernel(const NormArgs args,
                                                             double *__restrict__ parts) {
     __shared__ double waves[WAVES];
     double sum[4] = {0.0, 0.0, 0.0, 0.0};
-    for (int tile = blockIdx.x; tile < args.tiles; tile += gridDim.x) {
-        const NormTensor &t = args.t[tensor_of(args, tile)];
-        const int64_t i0 = (int64_t)(tile - t.first) * NORM_TILE;
-        if (t.bf16) add_squares<uint16_t>(t, i0, sum);
-        else add_squares<float>(t, i0, sum);
+    const int t0 = (int)((int64_t)args.tiles * blockIdx.x / gridDim.x);
+    const int t1 = (int)((int64_t)args.tiles * (blockIdx.x + 1) / gridDim.x);
+    int item = tensor_of(args, t0);
+    for (int tile = t0; tile < t1; ++tile) {
+        while (item + 1 < args.count && args.t[item + 1].first <= tile) ++item;
+        const NormTensor &t = args.t[item];
+        // Loads without branches where the tile is whole.
+        const int at = tile - t.first;
+        const bool full = t.n >= (at + 1) * (NORM_TILE_BYTES / (t.bf16 ? 2 : 4));
+        if (t.bf16) full ? add_tile<true, true>(t, at, sum) : add_tile<true, false>(t, at, sum);
+        else full ? add_tile<false, true>(t, at, sum) : add_tile<false, false>(t, at, sum);
     }
     const double all = wave_sum((sum[0] + sum[1]) + (sum[2] + sum[3]));
     if ((threadIdx.x & 63) == 0) waves[threadIdx.x >> 6] = all;
@@ -470,7 +499,8 @@ hipError_t launch_grad_norm(const fp8_grad_t *grads, int count, float max_norm, 
             if (grads[at].n == 0) continue;
             args.t[args.count++] = {grads[at].grad, grads[at].n, args.tiles,
                                     grads[at].dtype == FP8_DTYPE_BF16};
-            args.tiles += (int)((grads[at].n + NORM_TILE - 1) / NORM_TILE);
+            const int64_t bytes = grads[at].n * (grads[at].dtype == FP8_DTYPE_BF16 ? 2 : 4);
+            args.tiles += (int)((bytes + NORM_TILE_BYTES - 1) / NORM_TILE_BYTES);
         }
         if (args.count == 0) break;
         // The first launch writes the parts that all have.
