@@ -51,7 +51,8 @@ __all__ = [
     "ExpertPlan", "fp8_expert_rows", "fp8_expert_plan_bytes", "fp8_expert_plan",
     "fp8_expert_gather", "fp8_expert_gather_cast_transpose_amax", "fp8_expert_combine",
     "fp8_expert_combine_backward",
-    "AdamW", "AdamWTensor", "ADAMW_BLOCK", "fp8_adamw_step", "fp8_grad_norm",
+    "AdamW", "AdamWTensor", "ADAMW_BLOCK", "ADAMW_STATE_BYTES",
+    "fp8_adamw_step", "fp8_grad_norm",
     "fp8_grad_norm_workspace_bytes",
     "library_path", "lib",
 ]
@@ -67,6 +68,7 @@ PRODUCE_MODULATE_FINITE = 4      # the library's addition: non-finite quotients 
 NOALLOC_SCRATCH_BYTES = 4 << 20     # FP8DSL_NOALLOC_SCRATCH_BYTES
 CAST_GROUP_MAX = 8                  # FP8DSL_CAST_GROUP_MAX
 ADAMW_BLOCK = 256                   # FP8DSL_ADAMW_BLOCK
+ADAMW_STATE_BYTES = 8320            # FP8DSL_ADAMW_STATE_BYTES
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 library_path = os.path.join(_PKG, "libfp8dsl.so")
@@ -178,7 +180,7 @@ class _AdamWDesc(ctypes.Structure):
     """Mirror of fp8_adamw_t."""
     _fields_ = [
         ("lr", ctypes.c_void_p),
-        ("steps", ctypes.c_void_p),
+        ("state", ctypes.c_void_p),
         ("beta1", ctypes.c_double),
         ("beta2", ctypes.c_double),
         ("eps", ctypes.c_double),
@@ -1214,7 +1216,7 @@ class AdamWTensor:
 class AdamW:
     """AdamW over `tensors` (AdamWTensor): lr is a float or a 1-element fp32
     device tensor (which a program changes between steps, graph replays
-    included), `steps` [1] (int64, device) the steps taken.  `seed` feeds the
+    included), `steps` [1] (int64, device) the steps taken, a view of `state`.  `seed` feeds the
     stochastic rounding of 8-bit moments and bf16 parameters."""
 
     def __init__(self, tensors, lr=1e-3, betas=(0.9, 0.999), eps: float = 1e-8, seed: int = 0,
@@ -1223,11 +1225,11 @@ class AdamW:
         self.lr = lr if isinstance(lr, torch.Tensor) else \
             torch.full((1,), lr, dtype=torch.float32, device=device)
         self.betas, self.eps, self.seed = betas, eps, seed
-        self._steps = torch.zeros(2, dtype=torch.int64, device=self.lr.device)
+        self.state = torch.zeros(ADAMW_STATE_BYTES // 8, dtype=torch.int64, device=self.lr.device)
 
     @property
     def steps(self) -> torch.Tensor:
-        return self._steps[:1]
+        return self.state[:1]
 
     @property
     def grads(self) -> list:
@@ -1236,9 +1238,10 @@ class AdamW:
 
     def desc(self) -> _AdamWDesc:
         _need_scalar(self.lr, "lr")
-        _on_current_device(self.lr, self._steps)
-        return _AdamWDesc(_ptr(self.lr, torch.float32, "lr"), self._steps.data_ptr(),
-                          self.betas[0], self.betas[1], self.eps, self.seed & (2 ** 64 - 1))
+        _need_shape(self.state, (ADAMW_STATE_BYTES // 8,), "state")
+        _on_current_device(self.lr, self.state)
+        return _AdamWDesc(_ptr(self.lr, torch.float32, "lr"),
+                          _ptr(self.state, torch.int64, "state"), self.betas[0], self.betas[1], self.eps, self.seed & (2 ** 64 - 1))
 
     def step(self, grad_scale: Optional[torch.Tensor] = None,
              noop_flag: Optional[torch.Tensor] = None, stream=None) -> None:

@@ -27,7 +27,22 @@ __device__ __forceinline__ uint32_t bf16_bits(float f) {
     return (f != f) ? 0x7FC0u : (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
 }
 
-// Four values of a tensor from element i on, `left` of them (1 .. 4) there.
+template <typename V>
+__device__ __forceinline__ V load_once(const void *p) {
+    return __builtin_nontemporal_load(static_cast<const V *>(p));
+}
+template <typename V>
+__device__ __forceinline__ void store_once(void *p, V v) {
+    __builtin_nontemporal_store(v, static_cast<V *>(p));
+}
+
+// Four values of a tensor from element i on, `left` of them (1 .. 4) there, past the
+// last-level cache: a step touches every value once, and what it would leave there
+// are the last tensors' values only.  Measured (all loads and stores of a step so,
+// against none): a toy block in fp32 with the norm before it 456 us against 538,
+// 67 million values in 8 bits 224 against 263, 16 million fp32 values alone 84
+// against 94, 1 million 12.0 against 13.4.  (With the norm, gradients that it has read
+// are still in that cache, and the step begins with the last of them.)
 template <typename T>
 struct Four;
 template <>
@@ -35,7 +50,7 @@ struct Four<float> {
     static __device__ __forceinline__ void load(const void *p, int64_t i, int left, float (&o)[4]) {
         const float *at = static_cast<const float *>(p) + i;
         if (left >= 4) {
-            const u32x4 v = *reinterpret_cast<const u32x4 *>(at);
+            const u32x4 v = load_once<u32x4>(at);
 #pragma unroll
             for (int k = 0; k < 4; ++k) o[k] = __uint_as_float(v[k]);
         } else {
@@ -46,8 +61,8 @@ struct Four<float> {
     static __device__ __forceinline__ void store(void *p, int64_t i, int left, const float (&v)[4]) {
         float *at = static_cast<float *>(p) + i;
         if (left >= 4) {
-            *reinterpret_cast<u32x4 *>(at) = u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]),
-                                                   __float_as_uint(v[2]), __float_as_uint(v[3])};
+            store_once(at, u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]),
+                                 __float_as_uint(v[2]), __float_as_uint(v[3])});
         } else {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
@@ -61,7 +76,7 @@ struct Four<uint16_t> {
     static __device__ __forceinline__ void load(const void *p, int64_t i, int left, float (&o)[4]) {
         const uint16_t *at = static_cast<const uint16_t *>(p) + i;
         if (left >= 4) {
-            const u32x2 v = *reinterpret_cast<const u32x2 *>(at);
+            const u32x2 v = load_once<u32x2>(at);
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 o[k] = __uint_as_float(k & 1 ? v[k / 2] & 0xFFFF0000u : v[k / 2] << 16);
@@ -74,8 +89,7 @@ struct Four<uint16_t> {
                                                  const uint32_t (&bits)[4]) {
         uint16_t *at = static_cast<uint16_t *>(p) + i;
         if (left >= 4) {
-            *reinterpret_cast<u32x2 *>(at) = u32x2{bits[0] | (bits[1] << 16),
-                                                   bits[2] | (bits[3] << 16)};
+            store_once(at, u32x2{bits[0] | (bits[1] << 16), bits[2] | (bits[3] << 16)});
         } else {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
@@ -87,7 +101,7 @@ template <>
 struct Four<uint8_t> {
     static __device__ __forceinline__ uint32_t load(const void *p, int64_t i, int left) {
         const uint8_t *at = static_cast<const uint8_t *>(p) + i;
-        if (left >= 4) return *reinterpret_cast<const uint32_t *>(at);
+        if (left >= 4) return load_once<uint32_t>(at);
         uint32_t v = 0;
 #pragma unroll
         for (int k = 0; k < 3; ++k)
@@ -97,7 +111,7 @@ struct Four<uint8_t> {
     static __device__ __forceinline__ void store(void *p, int64_t i, int left, uint32_t v) {
         uint8_t *at = static_cast<uint8_t *>(p) + i;
         if (left >= 4) {
-            *reinterpret_cast<uint32_t *>(at) = v;
+            store_once(at, v);
         } else {
 #pragma unroll
             for (int k = 0; k < 3; ++k)
@@ -237,6 +251,9 @@ constexpr int BLOCK = FP8DSL_ADAMW_BLOCK;
 constexpr int STEP_BLOCKS = 2;                         // blocks of 256 a wave takes at once
 constexpr int STEP_TILE = WAVES * STEP_BLOCKS * BLOCK;
 constexpr int STEP_TENSORS = 48;
+// Counters behind the step count, 128 bytes apart.
+constexpr int TICKET_GROUPS = 64;
+static_assert(128 * (1 + TICKET_GROUPS) == FP8DSL_ADAMW_STATE_BYTES, "state");
 static_assert(BLOCK == 64 * 4, "a wave's lanes hold four values of a block each");
 
 struct StepTensor {
@@ -465,7 +482,7 @@ __global__ __launch_bounds__(THREADS) void adamw_kernel(const StepArgs args,
     f.root = (float)(1.0 / sqrt(1.0 - power(args.beta2, steps)));
     const DropoutKey key(args.seed_lo, args.seed_hi, steps);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    for (int tile = blockIdx.x; tile < args.tiles; tile += gridDim.x) {
+    for (int tile = args.tiles - 1 - (int)blockIdx.x; tile >= 0; tile -= gridDim.x) {
         const StepTensor &t = args.t[tensor_of(args, tile)];
         const int64_t i0 = (int64_t)(tile - t.first) * STEP_TILE + wave * STEP_BLOCKS * BLOCK;
         f.decay = (float)(1.0 - lr * (double)t.weight_decay);
@@ -476,12 +493,20 @@ __global__ __launch_bounds__(THREADS) void adamw_kernel(const StepArgs args,
                 step_blocks<P, G, STATE8, 1, false>(t, f, key, i);
         }
     }
-    // The last workgroup to come here counts the step: all have read the count.
+    // The last workgroup to come here counts the step: all have read the count.  Its
+    // tickets are in two levels, as one address takes an addition in 13 ns: 2048
+    // workgroups on one counter took 26 us.
     if (args.last && threadIdx.x == 0) {
-        unsigned long long *tickets = reinterpret_cast<unsigned long long *>(args.steps + 1);
-        if (atomicAdd(tickets, 1ull) == gridDim.x - 1) {
-            args.steps[0] = (int64_t)steps;
-            args.steps[1] = 0;
+        const int group = blockIdx.x % TICKET_GROUPS, groups = min(TICKET_GROUPS, (int)gridDim.x);
+        const int mine = ((int)gridDim.x - group + TICKET_GROUPS - 1) / TICKET_GROUPS;
+        uint32_t *root = reinterpret_cast<uint32_t *>(args.steps + 1);
+        uint32_t *ticket = reinterpret_cast<uint32_t *>(args.steps) + 32 * (1 + group);
+        if (atomicAdd(ticket, 1u) == (uint32_t)mine - 1u) {
+            *ticket = 0;
+            if (atomicAdd(root, 1u) == (uint32_t)groups - 1u) {
+                *root = 0;
+                args.steps[0] = (int64_t)steps;
+            }
         }
     }
 }
@@ -532,7 +557,7 @@ hipError_t launch_adamw(const fp8_adamw_t &opt, const fp8_adamw_tensor_t *tensor
     StepArgs args;
     args.lr = opt.lr;
     args.grad_scale = grad_scale;
-    args.steps = opt.steps;
+    args.steps = opt.state;
     args.beta1 = opt.beta1;
     args.beta2 = opt.beta2;
     args.b1 = (float)opt.beta1;

@@ -746,10 +746,10 @@ int fp8_adamw_step(const fp8_adamw_t *opt, const fp8_adamw_tensor_t *tensors, in
         !(opt->beta2 >= 0.0 && opt->beta2 < 1.0) ||
         !((float)opt->eps >= 0x1p-126f && (float)opt->eps <= 3.402823466e38f))
         return FP8_ERR_ARG;
-    if (opt->lr == nullptr || opt->steps == nullptr || (count > 0 && tensors == nullptr))
+    if (opt->lr == nullptr || opt->state == nullptr || (count > 0 && tensors == nullptr))
         return FP8_ERR_NULL;
-    if (!aligned4(opt->lr) || (reinterpret_cast<uintptr_t>(opt->steps) & 7) != 0 ||
-        !aligned4(grad_scale) || !aligned4(noop_flag))
+    if (!aligned4(opt->lr) || !aligned16(opt->state) || !aligned4(grad_scale) ||
+        !aligned4(noop_flag))
         return FP8_ERR_ALIGN;
     for (int32_t i = 0; i < count; ++i) {
         const fp8_adamw_tensor_t &t = tensors[i];

@@ -1017,10 +1017,14 @@ typedef struct fp8_adamw_tensor {
     int32_t reserved;       /* must be 0                                       */
 } fp8_adamw_tensor_t;
 
+/* Device bytes of an optimizer's state: the steps taken (int64), then counters
+ * that are zero between calls.  16-byte aligned, zeros before the first step. */
+#define FP8DSL_ADAMW_STATE_BYTES 8320
+
 /* What the tensors of a step share. */
 typedef struct fp8_adamw {
     const float *lr;        /* device, 1 float                                 */
-    int64_t *steps;         /* device {steps taken, 0}, 8-byte aligned         */
+    int64_t *state;         /* device, FP8DSL_ADAMW_STATE_BYTES                */
     double beta1;           /* 0 <= beta1 < 1                                  */
     double beta2;           /* 0 <= beta2 < 1                                  */
     double eps;             /* a normal number in fp32, 2^-126 or more         */
@@ -1031,7 +1035,7 @@ typedef struct fp8_adamw {
  * fp8_adamw_step -- one step of AdamW over many tensors: the master weights of
  * the linears, their biases, adapters.
  *
- * With t = steps[0] + 1, in fp32, every operation rounded (the factors from lr,
+ * With t = the steps taken + 1, in fp32, every operation rounded (the factors from lr,
  * beta1, beta2 and t in 64 bits first):
  *
  *   g = grad * *grad_scale                                  (grad without one)
@@ -1039,7 +1043,7 @@ typedef struct fp8_adamw {
  *   v = beta2 v + ((1 - beta2) g) g
  *   p = p (1 - lr weight_decay) - (lr / (1 - beta1^t) m) / (sqrt(v) / sqrt(1 - beta2^t) + eps)
  *
- * (the last quotient to within 2^-22 of itself), then steps[0] = t.
+ * (the last quotient to within 2^-22 of itself), then t is the steps taken.
  *
  * Stored in 8 bits, m and v get new scales, the least power of two (2^-126 or
  * more) that keeps each block's largest finite magnitude within 448, and are
@@ -1064,8 +1068,8 @@ typedef struct fp8_adamw {
  *            what is written; types may differ from tensor to tensor.
  * grad_scale NULL, or device, 1 float.
  * noop_flag  as fp8_cast_transpose_amax: skips the whole step, its count included.
- * lr, steps and grad_scale are read on the device when the kernels run, so a
- * captured step follows a schedule.  Calls that overlap on one `steps` race.
+ * lr, state and grad_scale are read on the device when the kernels run, so a
+ * captured step follows a schedule.  Calls that overlap on one state race.
  * One launch per 48 tensors of the same types.
  * Errors: FP8_ERR_NULL, FP8_ERR_SHAPE (n), FP8_ERR_ALIGN, FP8_ERR_ARG (betas,
  * eps, weight_decay, dtypes, count, reserved, a copy of a bf16 param, one scale

@@ -73,7 +73,7 @@ def test_step_refusals():
 
     assert call(opt=None) == -1 and call(tensors=False) == -1
     assert call(opt=_opt(lr=None)) == -1 and call(opt=_opt(steps=None)) == -1
-    assert call(opt=_opt(lr=0x50002)) == -3 and call(opt=_opt(steps=0x60004)) == -3
+    assert call(opt=_opt(lr=0x50002)) == -3 and call(opt=_opt(steps=0x60008)) == -3
     assert call(scale=0x70001) == -3 and call(flag=0x70002) == -3
     assert call(count=-1) == -5
     for bad in (dict(b1=1.0), dict(b1=-0.1), dict(b1=float("nan")), dict(b2=1.0), dict(b2=-1e-9),
