@@ -248,7 +248,7 @@ __global__ __launch_bounds__(THREADS) void grad_norm_sum_kernel(const double *__
 // ---- the step ----------------------------------------------------------------
 
 constexpr int BLOCK = FP8DSL_ADAMW_BLOCK;
-constexpr int STEP_BLOCKS = 2;                         // blocks of 256 a wave takes at once
+constexpr int STEP_BLOCKS = 4;                         // blocks of 256 a wave takes at once
 constexpr int STEP_TILE = WAVES * STEP_BLOCKS * BLOCK;
 constexpr int STEP_TENSORS = 48;
 // Counters behind the step count, 128 bytes apart.
@@ -311,55 +311,65 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
     return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 
-// The E4M3 code of a magnitude x <= 448, u a 16-bit number.  An fp32 value from 2^-6
-// on has 20 bits below the code's three: adding u there and cutting rounds up with
-// the probability of the part cut.  Below 2^-6 the codes are as far apart as from
-// 2^-6 to 2^-5: x is moved there.  Each form is the larger where it holds.
-__device__ __forceinline__ uint32_t code_of(float x, uint32_t u) {
-    const int high = (int)(__float_as_uint(x) - (960u << 20));
-    const int low = (int)(__float_as_uint(x + 0x1p-6f) - (968u << 20));
-    return ((uint32_t)max(high, low) + (u << 4)) >> 20;
+// Four E4M3 codes of x (magnitudes of at most 448), each rounded by the upper half of
+// its u: the converter adds u to the 20 bits below a code's three (below 2^-6, to as
+// many below the step of 2^-9) and cuts, which is floor(place + u / 2^16).
+__device__ __forceinline__ uint32_t convert4(const float (&x)[4], const uint32_t (&u)[4]) {
+    int c = __builtin_amdgcn_cvt_sr_fp8_f32(x[0], (int)u[0], 0, 0);
+    c = __builtin_amdgcn_cvt_sr_fp8_f32(x[1], (int)u[1], c, 1);
+    c = __builtin_amdgcn_cvt_sr_fp8_f32(x[2], (int)u[2], c, 2);
+    return (uint32_t)__builtin_amdgcn_cvt_sr_fp8_f32(x[3], (int)u[3], c, 3);
 }
 
-// Four codes of a moment: SIGNED with the values' signs, else a value above 0 gets
+// Four codes of a moment under the power of two `scale`.  KEEP: a value above 0 gets
 // a code above 0.  SPECIAL: what is not finite becomes 0x7F.
-template <bool SIGNED, bool SPECIAL>
-__device__ __forceinline__ uint32_t codes_of(const float (&x)[4], float inverse,
-                                             const uint32_t (&w)[4]) {
-    uint32_t out = 0;
+template <bool KEEP, bool SPECIAL>
+__device__ __forceinline__ uint32_t codes_of(const float (&x)[4], uint32_t scale,
+                                             const uint32_t (&u)[4]) {
+    // 1 / 2^e: e and its negative are both exponents of normal numbers.
+    const float inverse = __uint_as_float((254u << 23) - scale);
+    float y[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const float y = x[k] * inverse;
-        const uint32_t bits = __float_as_uint(y), u = SIGNED ? w[k] & 0xFFFFu : w[k] >> 16;
-        uint32_t code = code_of(SIGNED ? __uint_as_float(bits & 0x7FFFFFFFu) : y, u);
-        if constexpr (SIGNED) code |= (bits >> 24) & 0x80u;
-        else code = max(code, min(bits, 1u));
-        if constexpr (SPECIAL) code = (bits & 0x7F800000u) == 0x7F800000u ? 0x7Fu : code;
-        out |= code << (8 * k);
-    }
-    return out;
-}
-
-// Stores a moment's new values; returns its codes and sets the block's scale.
-template <bool SIGNED>
-__device__ __forceinline__ uint32_t encode(const float (&x)[4], const uint32_t (&w)[4],
-                                           uint32_t &scale) {
-    uint32_t mag[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-        mag[k] = SIGNED ? __float_as_uint(x[k]) & 0x7FFFFFFFu : __float_as_uint(x[k]);
-    uint32_t most = wave_max(max(max(mag[0], mag[1]), max(mag[2], mag[3])));
-    if (most >= 0x7F800000u) {                           // rare, the same for the wave
-        most = 0;
+    for (int k = 0; k < 4; ++k) y[k] = x[k] * inverse;
+    uint32_t codes = convert4(y, u);
+    // A byte of zero borrows from the one above; no other code has its upper bit set.
+    if (KEEP && ((codes - 0x01010101u) & 0x80808080u)) {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-            most = max(most, (mag[k] & 0x7FFFFFFFu) < 0x7F800000u ? mag[k] : 0u);
-        scale = scale_bits(wave_max(most));
-        return codes_of<SIGNED, true>(x, __uint_as_float((254u << 23) - scale), w);
+            if (y[k] > 0.0f && ((codes >> (8 * k)) & 0xFFu) == 0) codes |= 1u << (8 * k);
+    }
+    if constexpr (SPECIAL) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if ((__float_as_uint(x[k]) & 0x7F800000u) == 0x7F800000u)
+                codes = (codes & ~(0xFFu << (8 * k))) | (0x7Fu << (8 * k));
+    }
+    return codes;
+}
+
+// The largest magnitude (bits) of the wave's block of a moment.
+template <bool SIGNED>
+__device__ __forceinline__ uint32_t most_of(const float (&x)[4], bool finite_only) {
+    uint32_t mag[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        mag[k] = __float_as_uint(x[k]);
+        if (SIGNED || finite_only) mag[k] &= 0x7FFFFFFFu;
+        if (finite_only && mag[k] >= 0x7F800000u) mag[k] = 0;
+    }
+    return wave_max(max(max(mag[0], mag[1]), max(mag[2], mag[3])));
+}
+
+// The codes of a block's values and its scale; `most` is most_of(x, false).
+template <bool SIGNED>
+__device__ __forceinline__ uint32_t encode(const float (&x)[4], uint32_t most,
+                                           const uint32_t (&u)[4], uint32_t &scale) {
+    if (most >= 0x7F800000u) {                           // rare, the same for the wave
+        scale = scale_bits(most_of<SIGNED>(x, true));
+        return codes_of<!SIGNED, true>(x, scale, u);
     }
     scale = scale_bits(most);
-    // 1 / 2^e: e and its negative are both exponents of normal numbers.
-    return codes_of<SIGNED, false>(x, __uint_as_float((254u << 23) - scale), w);
+    return codes_of<!SIGNED, false>(x, scale, u);
 }
 
 __device__ __forceinline__ void decode(uint32_t codes, float scale, float (&x)[4]) {
@@ -375,6 +385,45 @@ __device__ __forceinline__ float root_of(float x) {
     const float r = __builtin_amdgcn_sqrtf(small ? x * 0x1p32f : x);
     return small ? r * 0x1p-16f : r;
 }
+// The same times 2^12 where x < 2^104.
+__device__ __forceinline__ float root_of_scaled(float x) {
+    return __builtin_amdgcn_sqrtf(x * 0x1p24f);
+}
+
+// Lane l's value of v on lane l ^ 1.
+__device__ __forceinline__ uint32_t from_neighbour(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, true);
+}
+
+// The two words of each of a lane's N fours of parameters.  An even lane has the first
+// half of a group of eight, its neighbour the second: of two blocks each makes one
+// block's words for both.
+template <int N>
+__device__ __forceinline__ void param_words(const DropoutKey &key, int index, int64_t i0, int lane,
+                                            uint32_t (&out)[N][2]) {
+    const bool odd = lane & 1;
+    const auto words = [&](int64_t i, uint32_t (&w)[4]) {
+        dropout_words(key, ((uint64_t)(2u * (uint32_t)index + 1u) << 32) | (uint64_t)(i / 8), w);
+    };
+    uint32_t w[4];
+    if constexpr (N == 1) {
+        words(i0 + 4 * lane, w);
+        out[0][0] = odd ? w[2] : w[0];
+        out[0][1] = odd ? w[3] : w[1];
+    } else {
+        static_assert(N % 2 == 0, "pairs of blocks");
+#pragma unroll
+        for (int s = 0; s < N; s += 2) {
+            words(i0 + (s + odd) * BLOCK + 4 * lane, w);
+            const uint32_t x0 = from_neighbour(odd ? w[0] : w[2]);
+            const uint32_t x1 = from_neighbour(odd ? w[1] : w[3]);
+            out[s][0] = odd ? x0 : w[0];
+            out[s][1] = odd ? x1 : w[1];
+            out[s + 1][0] = odd ? w[2] : x0;
+            out[s + 1][1] = odd ? w[3] : x1;
+        }
+    }
+}
 
 // N blocks of 256 values of a tensor, a wave's; FULL: all of their values exist.
 template <typename P, typename G, bool STATE8, int N, bool FULL>
@@ -383,7 +432,7 @@ __device__ __forceinline__ void step_blocks(const StepTensor &t, const Factors &
 #pragma clang fp contract(off)
     const int lane = threadIdx.x & 63;
     float p[N][4], g[N][4], m[N][4], v[N][4], ms[N], vs[N];
-    uint32_t mc[N], vc[N];
+    uint32_t mc[N], vc[N], pw[N][2];
     int left[N];
 #pragma unroll
     for (int s = 0; s < N; ++s) {
@@ -408,6 +457,7 @@ __device__ __forceinline__ void step_blocks(const StepTensor &t, const Factors &
             ms[s] = vs[s] = 0.0f;
         }
     }
+    if constexpr (std::is_same<P, uint16_t>::value) param_words(key, t.index, i0, lane, pw);
 #pragma unroll
     for (int s = 0; s < N; ++s) {
         const int64_t b = i0 + s * BLOCK, i = b + 4 * lane;
@@ -420,15 +470,33 @@ __device__ __forceinline__ void step_blocks(const StepTensor &t, const Factors &
             const float gk = g[s][k] * f.grad;
             m[s][k] = m[s][k] * f.b1 + gk * f.c1;
             v[s][k] = v[s][k] * f.b2 + (gk * f.c2) * gk;
-            const float d = root_of(v[s][k]) * f.root + f.eps;
-            p[s][k] = p[s][k] * f.decay - (m[s][k] * f.step) * __builtin_amdgcn_rcpf(d);
         }
+        uint32_t most = 0xFFFFFFFFu;
+        if constexpr (STATE8) most = most_of<false>(v[s], false);
+        // A wave of ordinary values needs no look at each for the root.
+        float r[4];
+        if (most < 0x73000000u) {                        // 2^103
+#pragma unroll
+            for (int k = 0; k < 4; ++k) r[k] = root_of_scaled(v[s][k]) * (f.root * 0x1p-12f);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) r[k] = root_of(v[s][k]) * f.root;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            p[s][k] = p[s][k] * f.decay -
+                      (m[s][k] * f.step) * __builtin_amdgcn_rcpf(r[k] + f.eps);
         uint32_t sm, sv;
         if constexpr (STATE8) {
-            uint32_t w[4];
+            uint32_t w[4], um[4], uv[4];
             dropout_words(key, ((uint64_t)(2u * (uint32_t)t.index) << 32) | (uint64_t)(i / 4), w);
-            mc[s] = encode<true>(m[s], w, sm);
-            vc[s] = encode<false>(v[s], w, sv);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                um[k] = w[k] << 16;
+                uv[k] = w[k] & 0xFFFF0000u;
+            }
+            mc[s] = encode<true>(m[s], most_of<true>(m[s], false), um, sm);
+            vc[s] = encode<false>(v[s], most, uv, sv);
         }
         if (!FULL && left[s] <= 0) continue;
         if constexpr (STATE8) {
@@ -450,17 +518,19 @@ __device__ __forceinline__ void step_blocks(const StepTensor &t, const Factors &
                 Four<uint16_t>::store(t.copy, i, left[s], bits);
             }
         } else {
-            uint32_t w[4], bits[4];
-            dropout_words(key, ((uint64_t)(2u * (uint32_t)t.index + 1u) << 32) | (uint64_t)(i / 8),
-                          w);
-            // An even lane has the first half of its group of eight.
-            const uint32_t word[2] = {lane & 1 ? w[2] : w[0], lane & 1 ? w[3] : w[1]};
+            uint32_t bits[4];
+            const uint32_t (&word)[2] = pw[s];
+            // An infinity's bits below the upper half are zero: nothing is carried.
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const uint32_t u = k & 1 ? word[k / 2] >> 16 : word[k / 2] & 0xFFFFu;
-                const uint32_t x = __float_as_uint(p[s][k]);
-                const bool finite = (x & 0x7F800000u) != 0x7F800000u;
-                bits[k] = p[s][k] != p[s][k] ? 0x7FC0u : (x + (finite ? u : 0u)) >> 16;
+                bits[k] = (__float_as_uint(p[s][k]) + u) >> 16;
+            }
+            const bool nan[4] = {p[s][0] != p[s][0], p[s][1] != p[s][1], p[s][2] != p[s][2],
+                                 p[s][3] != p[s][3]};
+            if (nan[0] | nan[1] | nan[2] | nan[3]) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) bits[k] = nan[k] ? 0x7FC0u : bits[k];
             }
             Four<uint16_t>::store(t.param, i, left[s], bits);
         }
@@ -588,7 +658,7 @@ hipError_t launch_adamw(const fp8_adamw_t &opt, const fp8_adamw_tensor_t *tensor
             kinds[kind] -= args.count;
             left -= args.count;
             args.last = left == 0;
-            const int grid = std::max(1, std::min(args.tiles, 8 * cus));
+            const int grid = std::max(1, std::min(args.tiles, 16 * cus));
             hipLaunchKernelGGL(kernels[kind], dim3((unsigned)grid), dim3(THREADS), 0, stream, args,
                                noop);
             if (hipError_t e = hipGetLastError()) return e;

@@ -1052,8 +1052,7 @@ typedef struct fp8_adamw {
  * their distance from the lower one and u is a 16-bit random number.  Rounded to
  * nearest instead, v would not fall (a step takes 1 - beta2 of it, the format's
  * half step is 2^-4) and a bf16 parameter would not take small updates.  A v
- * above 0 is never stored as 0; below 2^-6 after scaling the magnitudes are first
- * rounded to multiples of 2^-29.  What is not finite is stored as the code 0x7F
+ * above 0 is never stored as 0, and what is not finite is stored as the code 0x7F
  * (NaN).  The update of p uses m and v before they are stored.  copy is p rounded
  * to nearest even.
  *

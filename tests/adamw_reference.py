@@ -41,12 +41,9 @@ def scales_of(x):
     return out.astype(F)
 
 
-def place(y, u, keep):
+def place(y, u):
     """Codes of the magnitudes y <= 448 (float64): floor(place + u / 65536) in the
     distance of their neighbours."""
-    low = y < 2.0 ** -6
-    # Below 2^-6 magnitudes are first multiples of 2^-29 (ties to even).
-    y = np.where(low, np.rint(y * 2.0 ** 29) * 2.0 ** -29, y)
     e = np.floor(np.log2(np.maximum(y, 2.0 ** -6)))
     step = 2.0 ** (e - 3)
     value = np.floor(y / step + u / 65536.0) * step
@@ -61,7 +58,7 @@ def encode(x, u, keep):
     finite = np.isfinite(x)
     y = np.where(finite, x, 0).astype(np.float64) / np.repeat(scales.astype(np.float64),
                                                              BLOCK)[:x.size]
-    code = place(np.abs(y), u, keep)
+    code = place(np.abs(y), u)
     if keep:
         code = np.where((code == 0) & (y > 0), 1, code)
     code = code | np.where(np.signbit(y), 0x80, 0)
