@@ -664,9 +664,13 @@ class Dropout:
         return d
 
 
+def _device() -> int:
+    return torch.cuda.current_device() if _raw_device is None else _raw_device()
+
+
 def _on_current_device(*tensors) -> None:
     """The calls run on the current device: tensors of another one are refused."""
-    dev = torch.cuda.current_device() if _raw_device is None else _raw_device()
+    dev = _device()
     for t in tensors:
         if t is not None and t.get_device() != dev:
             raise ValueError(f"tensors must be on the current device cuda:{dev}, got {t.device}")
@@ -963,6 +967,7 @@ class ExpertPlan:
     def __post_init__(self):
         self._sizes = _ExpertSizes(self.tokens, self.capacity, self.top_k, self.experts)
         self.rows = fp8_expert_rows(self.tokens, self.top_k, self.experts, self.capacity)
+        self._viewed = None
         self._layout = _ExpertLayout()
         _check(lib().fp8_expert_plan_layout(ctypes.byref(self._sizes),
                                             ctypes.byref(self._layout)), "fp8_expert_plan_layout")
@@ -974,29 +979,36 @@ class ExpertPlan:
         return ExpertPlan(torch.empty(n, dtype=torch.uint8, device=device), tokens, top_k, experts,
                           capacity)
 
-    def _words(self, at: int, count: int) -> torch.Tensor:
-        return self.buf[at:at + 4 * count].view(torch.int32)
+    def _view(self, i: int) -> torch.Tensor:
+        """The plan's arrays, made once for the buffer."""
+        if self._viewed is not self.buf:
+            at, n, tk = self._layout, self.experts, self.tokens * self.top_k
+            words = lambda first, count: self.buf[first:first + 4 * count].view(torch.int32)
+            self._views = (words(at.offsets, n + 1), words(at.counts, n),
+                           words(at.slots, tk).view(self.tokens, self.top_k),
+                           words(at.sources, self.rows))
+            self._viewed = self.buf
+        return self._views[i]
 
     @property
     def offsets(self) -> torch.Tensor:
         """[experts + 1] int32: first row of each expert's segment, and the end."""
-        return self._words(self._layout.offsets, self.experts + 1)
+        return self._view(0)
 
     @property
     def counts(self) -> torch.Tensor:
         """[experts] int32: the pairs that each expert keeps."""
-        return self._words(self._layout.counts, self.experts)
+        return self._view(1)
 
     @property
     def slots(self) -> torch.Tensor:
         """[tokens, top_k] int32: the row of each pair, -1 for none."""
-        n = self.tokens * self.top_k
-        return self._words(self._layout.slots, n).view(self.tokens, self.top_k)
+        return self._view(2)
 
     @property
     def sources(self) -> torch.Tensor:
         """[rows] int32: the pair t * top_k + k of each row, -1 for none."""
-        return self._words(self._layout.sources, self.rows)
+        return self._view(3)
 
     def segments(self, t: Float8Tensor, offsets=None) -> list:
         """Each expert's rows of t (fp8_expert_gather_cast_transpose_amax) as a
@@ -1166,6 +1178,7 @@ class AdamWTensor:
     v_scale: Optional[torch.Tensor] = None
     copy: Optional[torch.Tensor] = None
     weight_decay: float = 0.0
+    _seen: Optional[tuple] = field(default=None, init=False, repr=False, compare=False)
 
     @staticmethod
     def zeros(param: torch.Tensor, grad: torch.Tensor, bits: int = 32, copy=None,
@@ -1182,8 +1195,25 @@ class AdamWTensor:
         return AdamWTensor(param, grad, m, v, *scales, copy=copy, weight_decay=weight_decay)
 
     def desc(self) -> _AdamWTensorDesc:
-        """The C descriptor, checked on every call: a gradient is often another
-        tensor in the next step."""
+        """The C descriptor, built at the first call and again if a field is another
+        tensor since, or has been moved, reshaped or given another type in place."""
+        fields = (self.param, self.grad, self.m, self.v, self.m_scale, self.v_scale, self.copy)
+        seen = self._seen
+        if seen is not None and seen[0] == self.weight_decay and seen[1] == _device():
+            for t, (old, ptr, shape, dtype) in zip(fields, seen[2]):
+                if t is not old or t is not None and (
+                        t.data_ptr() != ptr or t.shape != shape or t.dtype is not dtype
+                        or not t.is_contiguous()):
+                    break
+            else:
+                return seen[3]
+        d = self._checked()
+        self._seen = (self.weight_decay, _device(), tuple(
+            (t, None, None, None) if t is None else (t, t.data_ptr(), t.shape, t.dtype)
+            for t in fields), d)
+        return d
+
+    def _checked(self) -> _AdamWTensorDesc:
         p, g, m, v, copy = self.param, self.grad, self.m, self.v, self.copy
         n, shape = p.numel(), p.shape
         for t, what in ((p, "param"), (g, "grad")):
@@ -1225,11 +1255,9 @@ class AdamW:
         self.lr = lr if isinstance(lr, torch.Tensor) else \
             torch.full((1,), lr, dtype=torch.float32, device=device)
         self.betas, self.eps, self.seed = betas, eps, seed
+        self._array, self._descs = (_AdamWTensorDesc * 0)(), []
         self.state = torch.zeros(ADAMW_STATE_BYTES // 8, dtype=torch.int64, device=self.lr.device)
-
-    @property
-    def steps(self) -> torch.Tensor:
-        return self.state[:1]
+        self.steps = self.state[:1]
 
     @property
     def grads(self) -> list:
@@ -1242,6 +1270,18 @@ class AdamW:
         _on_current_device(self.lr, self.state)
         return _AdamWDesc(_ptr(self.lr, torch.float32, "lr"),
                           _ptr(self.state, torch.int64, "state"), self.betas[0], self.betas[1], self.eps, self.seed & (2 ** 64 - 1))
+
+    def _tensor_array(self):
+        """The tensors' descriptors as the C call takes them; those that have not changed
+        stay in place."""
+        descs = [t.desc() for t in self.tensors]
+        if len(descs) != len(self._descs):
+            self._array, self._descs = (_AdamWTensorDesc * len(descs))(), [None] * len(descs)
+        for i, d in enumerate(descs):
+            if d is not self._descs[i]:
+                self._array[i] = d
+                self._descs[i] = d
+        return self._array, len(descs)
 
     def step(self, grad_scale: Optional[torch.Tensor] = None,
              noop_flag: Optional[torch.Tensor] = None, stream=None) -> None:
@@ -1284,11 +1324,10 @@ def fp8_adamw_step(opt: AdamW, grad_scale: Optional[torch.Tensor] = None,
     `noop_flag` [1] (int32) leaves everything as it is."""
     _need_scalar(grad_scale, "grad_scale")
     _need_scalar(noop_flag, "noop_flag")
-    descs = [t.desc() for t in opt.tensors]
-    array = (_AdamWTensorDesc * len(descs))(*descs)
+    array, count = opt._tensor_array()
     d = opt.desc()
     _on_current_device(grad_scale, noop_flag)
-    _check(lib().fp8_adamw_step(ctypes.byref(d), array, len(descs),
+    _check(lib().fp8_adamw_step(ctypes.byref(d), array, count,
                                 _ptr(grad_scale, torch.float32, "grad_scale"),
                                 _ptr(noop_flag, torch.int32, "noop_flag"), _stream(stream)),
            "fp8_adamw_step")
