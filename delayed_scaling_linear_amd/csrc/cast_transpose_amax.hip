@@ -1026,7 +1026,6 @@ __global__ __launch_bounds__(THREADS) void expert_gather_cast_kernel(
     uint8_t *__restrict__ q, uint8_t *__restrict__ qt, float *__restrict__ amax_cur,
     float *__restrict__ scale_inv_out, const int32_t *__restrict__ noop, int64_t tiles_c) {
     if (noop != nullptr && *noop != 0) return;
-    if (!plan.built()) return;
     __shared__ uint32_t lds_t[TILE * (TILE / 4)];
     __shared__ uint32_t lds_amax[THREADS / 64];
 
@@ -1036,13 +1035,16 @@ __global__ __launch_bounds__(THREADS) void expert_gather_cast_kernel(
     const int cc = lane & 7;
     const int cq = store_chunk<FP8_DTYPE_BF16>(cc);
     const int rg = wave * 8 + (lane >> 3);
+    // The plan's header, the tile and the scale in one go (the grid ends with the
+    // plan's space for tiles).
+    const int64_t tr = blockIdx.x / tiles_c, tcn = blockIdx.x - tr * tiles_c;
+    const int4 tile = plan.tiles[tr];
+    const bool used = tr < plan.header[5];
     const float s = *scale_ptr;
     const bool s_special = !(fabsf(s) > 0.0f && fabsf(s) <= 3.402823466e38f);
+    if (!plan.built()) return;
     if (blockIdx.x == 0 && tid == 0 && scale_inv_out != nullptr) *scale_inv_out = 1.0f / s;
-
-    const int64_t tr = blockIdx.x / tiles_c, tcn = blockIdx.x - tr * tiles_c;
-    if (tr >= plan.header[5]) return;
-    const int4 tile = plan.tiles[tr];
+    if (!used) return;
     const int64_t rows = tile.y, first = tile.z;         // the segment
     const int64_t row0 = tile.x, col0 = tcn * TILE;
     const int64_t r = row0 + 4 * rg, c = col0 + 16 * cq;
@@ -1059,7 +1061,7 @@ __global__ __launch_bounds__(THREADS) void expert_gather_cast_kernel(
     for (int i = 0; i < 4; ++i) {
         w[i] = WEIGHTS && pair[i] >= 0 ? weights[pair[i]] : 0.0f;
         const char *row = reinterpret_cast<const char *>(x) +
-                          (uint64_t)((uint32_t)max(pair[i], 0) / (uint32_t)plan.top_k) * ldx;
+                          (uint64_t)plan.token_of((uint32_t)max(pair[i], 0)) * ldx;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int64_t ch = col0 + 64 * h + 8 * cc;

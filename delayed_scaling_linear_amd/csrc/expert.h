@@ -16,7 +16,7 @@ constexpr int kExpertsMax = FP8DSL_EXPERTS_MAX;
 constexpr int kExpertTile = 128;
 // Pairs that one workgroup of the plan sorts alone; more are split into pieces of
 // kPlanPiece or more over at most kPlanPieces workgroups.
-constexpr int64_t kPlanAlone = 8192;
+constexpr int64_t kPlanAlone = 4096;
 constexpr int64_t kPlanPiece = 2048;
 constexpr int64_t kPlanPieces = 128;
 
@@ -60,11 +60,18 @@ struct ExpertView {
     const int32_t *header, *offsets, *slots, *sources;
     const int4 *tiles;
     int32_t tokens, top_k, experts, capacity, rows;
+    uint32_t reciprocal;     // 2^32 / top_k rounded up; 0 stands for 2^32
     ExpertView(const ExpertShape &s, const int32_t *plan)
         : header(plan), offsets(plan + s.offsets), slots(plan + s.slots),
           sources(plan + s.sources), tiles(reinterpret_cast<const int4 *>(plan + s.tiles)),
           tokens((int32_t)s.tokens), top_k(s.top_k), experts(s.experts),
-          capacity((int32_t)s.capacity), rows((int32_t)s.rows) {}
+          capacity((int32_t)s.capacity), rows((int32_t)s.rows),
+          reciprocal((uint32_t)((((uint64_t)1 << 32) + s.top_k - 1) / s.top_k)) {}
+    // pair / top_k.  The rounding of the reciprocal, less than top_k <= 64 in 2^32, times
+    // a pair below 2^23 does not reach a unit of the quotient.
+    __device__ __forceinline__ uint32_t token_of(uint32_t pair) const {
+        return reciprocal ? __umulhi(pair, reciprocal) : pair;
+    }
     // A buffer that no plan of these sizes was written to has no work in it.
     __device__ __forceinline__ bool built() const {
         return (header[0] == kExpertMagic) & (header[1] == tokens) & (header[2] == top_k) &

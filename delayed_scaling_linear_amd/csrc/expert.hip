@@ -34,6 +34,23 @@ __device__ __forceinline__ int wave_inclusive(int v, int lane) {
     return v;
 }
 
+// Ids that a lane reads at once.
+constexpr int PLAN_IDS = 4;
+
+// Calls what(p, id) for the ids of p0 .. p1 - 1, `stride` of them a step.
+template <typename What>
+__device__ __forceinline__ void for_ids(const int32_t *__restrict__ ids, int64_t p0, int64_t p1,
+                                        int lane, int stride, What what) {
+    for (int64_t p = p0 + lane; p < p1; p += PLAN_IDS * stride) {
+        uint32_t id[PLAN_IDS];
+#pragma unroll
+        for (int i = 0; i < PLAN_IDS; ++i)
+            id[i] = p + i * stride < p1 ? (uint32_t)ids[p + i * stride] : 0xFFFFFFFFu;
+#pragma unroll
+        for (int i = 0; i < PLAN_IDS; ++i) what(id[i]);
+    }
+}
+
 // Pairs of each expert in the workgroup's piece of the ids.
 __global__ __launch_bounds__(PLAN_THREADS) void expert_count_kernel(
     const int32_t *__restrict__ ids, int64_t pairs, int64_t piece, int experts,
@@ -42,10 +59,9 @@ __global__ __launch_bounds__(PLAN_THREADS) void expert_count_kernel(
     for (int e = threadIdx.x; e < experts; e += PLAN_THREADS) count[e] = 0;
     __syncthreads();
     const int64_t p0 = (int64_t)blockIdx.x * piece, p1 = min(pairs, p0 + piece);
-    for (int64_t p = p0 + threadIdx.x; p < p1; p += PLAN_THREADS) {
-        const uint32_t e = (uint32_t)ids[p];
+    for_ids(ids, p0, p1, threadIdx.x, PLAN_THREADS, [&](uint32_t e) {
         if (e < (uint32_t)experts) atomicAdd(&count[e], 1);
-    }
+    });
     __syncthreads();
     for (int e = threadIdx.x; e < experts; e += PLAN_THREADS)
         hist[(int64_t)blockIdx.x * experts + e] = count[e];
@@ -57,6 +73,11 @@ __global__ __launch_bounds__(PLAN_THREADS) void expert_count_kernel(
 // first place of each expert's pairs.  It then walks its run 64 pairs at a time:
 // lanes that name the same expert find each other by ballots over the id's bits,
 // and their order among these is their order in the batch.
+//
+// Bound by latency: a chain of loads, LDS passes and barriers.  Every workgroup adds
+// up the counts of all pieces for itself (64 KB from the L2 at 128 experts), spread
+// over all its threads with eight loads in flight each, which is faster than a launch
+// between the two.
 __global__ __launch_bounds__(PLAN_THREADS) void expert_place_kernel(
     const int32_t *__restrict__ ids, int64_t pairs, int64_t piece, int pieces, int tokens,
     int top_k, int experts, int capacity, int rows, const int32_t *__restrict__ hist,
@@ -73,29 +94,47 @@ __global__ __launch_bounds__(PLAN_THREADS) void expert_place_kernel(
     const int64_t per_wave = ((p1 - p0 + PLAN_WAVES - 1) / PLAN_WAVES + 63) / 64 * 64;
     const int64_t w0 = min(p1, p0 + wave * per_wave), w1 = min(p1, w0 + per_wave);
 
-    for (int i = tid; i < PLAN_WAVES * experts; i += PLAN_THREADS) run[i] = 0;
+    // run, all and (as the pairs of the earlier pieces) first.
+    int *earlier = first;
+    for (int i = tid; i < (PLAN_WAVES + 2) * experts; i += PLAN_THREADS) run[i] = 0;
     __syncthreads();
-    for (int64_t p = w0 + lane; p < w1; p += 64) {
-        const uint32_t e = (uint32_t)ids[p];
+    for_ids(ids, w0, w1, lane, 64, [&](uint32_t e) {
         if (e < (uint32_t)experts) atomicAdd(&run[wave * experts + e], 1);
+    });
+    if (pieces > 1) {
+        int wide = 64;                           // threads side by side over the experts
+        while (wide < experts && wide < PLAN_THREADS) wide *= 2;
+        const int parts = PLAN_THREADS / wide, part = tid / wide;
+        const int g0 = pieces * part / parts, g1 = pieces * (part + 1) / parts;
+        for (int e = tid % wide; e < experts; e += wide) {
+            int before = 0, total = 0;
+            for (int g = g0; g < g1; g += 8) {
+                int c[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    c[i] = g + i < g1 ? hist[(int64_t)(g + i) * experts + e] : 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    total += c[i];
+                    before += g + i < (int)blockIdx.x ? c[i] : 0;
+                }
+            }
+            atomicAdd(&all[e], total);
+            atomicAdd(&earlier[e], before);
+        }
     }
     __syncthreads();
     // Pairs before each wave's run, and all pairs, of each expert.
     for (int e = tid; e < experts; e += PLAN_THREADS) {
-        int before = 0, total = 0;
-        if (pieces > 1) {
-            for (int g = 0; g < pieces; ++g) {
-                const int c = hist[(int64_t)g * experts + e];
-                before += g < (int)blockIdx.x ? c : 0;
-                total += c;
-            }
-        }
+        int before = earlier[e], c[PLAN_WAVES];
+#pragma unroll
+        for (int w = 0; w < PLAN_WAVES; ++w) c[w] = run[w * experts + e];
+#pragma unroll
         for (int w = 0; w < PLAN_WAVES; ++w) {
-            const int c = run[w * experts + e];
             run[w * experts + e] = before;
-            before += c;
+            before += c[w];
         }
-        all[e] = pieces > 1 ? total : before;
+        if (pieces == 1) all[e] = before;
     }
     __syncthreads();
     // First row and tile of each segment: a scan over the experts, two a thread.
@@ -158,39 +197,48 @@ __global__ __launch_bounds__(PLAN_THREADS) void expert_place_kernel(
         }
         tiles[t] = int4{(t - tile0[lo]) * kExpertTile, first[lo + 1] - first[lo], first[lo], 0};
     }
-    // Slots without a pair: the ends of the segments (a wave each) and what lies
+    // Slots without a pair: the ends of the segments (16 lanes each) and what lies
     // behind the last one.
-    for (int e = blockIdx.x * PLAN_WAVES + wave; e < experts; e += gridDim.x * PLAN_WAVES) {
-        const int kept = capacity ? min(all[e], capacity) : all[e];
-        for (int r = first[e] + kept + lane; r < first[e + 1]; r += 64) sources[r] = -1;
+    for (int i = blockIdx.x * PLAN_THREADS + tid; i < 16 * experts; i += gridDim.x * PLAN_THREADS) {
+        const int e = i / 16, kept = capacity ? min(all[e], capacity) : all[e];
+        for (int r = first[e] + kept + (i & 15); r < first[e + 1]; r += 16) sources[r] = -1;
     }
     for (int64_t r = end + (int64_t)blockIdx.x * PLAN_THREADS + tid; r < rows;
          r += (int64_t)gridDim.x * PLAN_THREADS)
         sources[r] = -1;
 
     int *next = run + wave * experts;
-    for (int64_t pw = w0; pw < w1; pw += 64) {
-        const int64_t p = pw + lane;
-        const uint32_t id = p < w1 ? (uint32_t)ids[p] : 0xFFFFFFFFu;
-        const bool named = id < (uint32_t)experts;
-        uint64_t same = __ballot(named);
-        for (int b = 0; (1 << b) < experts; ++b) {
-            const bool bit = (id >> b) & 1;
-            const uint64_t votes = __ballot(bit);
-            same &= bit ? votes : ~votes;
+    for (int64_t pw = w0; pw < w1; pw += PLAN_IDS * 64) {
+        uint32_t ids_of[PLAN_IDS];
+#pragma unroll
+        for (int i = 0; i < PLAN_IDS; ++i) {
+            const int64_t p = pw + 64 * i + lane;
+            ids_of[i] = p < w1 ? (uint32_t)ids[p] : 0xFFFFFFFFu;
         }
-        int slot = -1;
-        if (named) {
-            const int base = next[id];
-            const int rank = base + __popcll(same & ((1ull << lane) - 1));
+#pragma unroll
+        for (int i = 0; i < PLAN_IDS; ++i) {
+            const int64_t p = pw + 64 * i + lane;
+            const uint32_t id = ids_of[i];
+            const bool named = id < (uint32_t)experts;
+            uint64_t same = __ballot(named);
+            for (int b = 0; (1 << b) < experts; ++b) {
+                const bool bit = (id >> b) & 1;
+                const uint64_t votes = __ballot(bit);
+                same &= bit ? votes : ~votes;
+            }
+            int slot = -1;
+            if (named) {
+                const int base = next[id];
+                const int rank = base + __popcll(same & ((1ull << lane) - 1));
+                wave_fence();
+                if ((same >> lane) == 1ull) next[id] = rank + 1;     // the last of them
+                if (!capacity || rank < capacity) slot = first[id] + rank;
+            }
             wave_fence();
-            if ((same >> lane) == 1ull) next[id] = rank + 1;     // the last of them
-            if (!capacity || rank < capacity) slot = first[id] + rank;
-        }
-        wave_fence();
-        if (p < w1) {
-            slots[p] = slot;
-            if (slot >= 0) sources[slot] = (int32_t)p;
+            if (p < w1) {
+                slots[p] = slot;
+                if (slot >= 0) sources[slot] = (int32_t)p;
+            }
         }
     }
 }
@@ -292,44 +340,77 @@ __global__ __launch_bounds__(THREADS) void expert_combine_kernel(
     *reinterpret_cast<u32x4 *>(row_at(y, (int)t, ldy) + 16 * g) = out;
 }
 
-// A wave per token: its lanes take the columns 8 lane + 512 i, their sums meet in a
-// butterfly.
+// dy[t] . x[slot] for up to PAIRS choices of a token at once, so that dy is read once
+// for them and all their rows are in flight together.  2^tx_log2 lanes (64 or 256) take
+// a token; their sums meet in a butterfly, and those of four waves in LDS in wave order.
+constexpr int PAIRS = 4;
 template <bool DX>
 __global__ __launch_bounds__(THREADS) void expert_combine_backward_kernel(
     ExpertView plan, const uint16_t *__restrict__ dy, uint32_t lddy, const uint16_t *x,
     uint32_t ldx, const float *__restrict__ weights, float *__restrict__ dweights, uint16_t *dx,
-    uint32_t lddx, int64_t groups, int64_t token_blocks) {
+    uint32_t lddx, int64_t groups, int tx_log2, int64_t token_blocks) {
     if (!plan.built()) return;
     if (blockIdx.x >= token_blocks) {
         zero_rows(plan, blockIdx.x - token_blocks, dx, lddx, groups);
         return;
     }
-    const int lane = threadIdx.x & 63;
-    const int64_t t = (int64_t)blockIdx.x * (THREADS / 64) + (threadIdx.x >> 6);
-    if (t >= plan.tokens) return;
-    for (int k = 0; k < plan.top_k; ++k) {
-        const int64_t pair = t * plan.top_k + k;
-        const int slot = plan.slots[pair];
-        float sum = 0.0f;
-        if (slot >= 0) {
-            const float w = DX ? weights[pair] : 0.0f;
-            for (int64_t g = lane; g < groups; g += 64) {
-                const u32x4 a = *reinterpret_cast<const u32x4 *>(row_at(dy, (int)t, lddy) + 16 * g);
-                const u32x4 v = *reinterpret_cast<const u32x4 *>(row_at(x, slot, ldx) + 16 * g);
+    __shared__ float part[THREADS / 64][PAIRS];
+    const int tx = 1 << tx_log2, lane = threadIdx.x & (tx - 1);
+    // The same for the wave.
+    const int t = __builtin_amdgcn_readfirstlane(
+        (int)(blockIdx.x * (THREADS >> tx_log2) + (threadIdx.x >> tx_log2)));
+    if (t >= plan.tokens) return;                        // with 256 lanes, the workgroup
+    const char *row = row_at(dy, t, lddy);
+    for (int k0 = 0; k0 < plan.top_k; k0 += PAIRS) {
+        const int64_t pair = (int64_t)t * plan.top_k + k0;
+        int slot[PAIRS];
+        float w[PAIRS], sum[PAIRS];
+#pragma unroll
+        for (int j = 0; j < PAIRS; ++j) {
+            slot[j] = k0 + j < plan.top_k ? plan.slots[pair + j] : -1;
+            w[j] = DX && slot[j] >= 0 ? weights[pair + j] : 0.0f;
+            sum[j] = 0.0f;
+        }
+        for (int64_t g = lane; g < groups; g += tx) {
+            const u32x4 a = *reinterpret_cast<const u32x4 *>(row + 16 * g);
+            u32x4 v[PAIRS];
+#pragma unroll
+            for (int j = 0; j < PAIRS; ++j)
+                if (slot[j] >= 0)
+                    v[j] = *reinterpret_cast<const u32x4 *>(row_at(x, slot[j], ldx) + 16 * g);
+#pragma unroll
+            for (int j = 0; j < PAIRS; ++j) {
+                if (slot[j] < 0) continue;
                 u32x4 out;
 #pragma unroll
                 for (int d = 0; d < 4; ++d) {
-                    sum += bf16_lo(a[d]) * bf16_lo(v[d]);
-                    sum += bf16_hi(a[d]) * bf16_hi(v[d]);
-                    out[d] = bf16_bits(w * bf16_lo(a[d])) | (bf16_bits(w * bf16_hi(a[d])) << 16);
+                    sum[j] += bf16_lo(a[d]) * bf16_lo(v[j][d]);
+                    sum[j] += bf16_hi(a[d]) * bf16_hi(v[j][d]);
+                    out[d] = bf16_bits(w[j] * bf16_lo(a[d])) |
+                             (bf16_bits(w[j] * bf16_hi(a[d])) << 16);
                 }
                 if constexpr (DX)
-                    *reinterpret_cast<u32x4 *>(row_at(dx, slot, lddx) + 16 * g) = out;
+                    *reinterpret_cast<u32x4 *>(row_at(dx, slot[j], lddx) + 16 * g) = out;
             }
         }
 #pragma unroll
-        for (int m = 32; m >= 1; m >>= 1) sum += __shfl_xor(sum, m, 64);
-        if (lane == 0) dweights[pair] = sum;
+        for (int j = 0; j < PAIRS; ++j)
+#pragma unroll
+            for (int m = 32; m >= 1; m >>= 1) sum[j] += __shfl_xor(sum[j], m, 64);
+        if (tx > 64) {
+            if (k0 > 0) __syncthreads();                 // the earlier sums have been read
+            if ((threadIdx.x & 63) == 0)
+#pragma unroll
+                for (int j = 0; j < PAIRS; ++j) part[threadIdx.x >> 6][j] = sum[j];
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < PAIRS; ++j)
+                sum[j] = ((part[0][j] + part[1][j]) + part[2][j]) + part[3][j];
+        }
+        if (lane == 0)
+#pragma unroll
+            for (int j = 0; j < PAIRS; ++j)
+                if (k0 + j < plan.top_k) dweights[pair + j] = sum[j];
     }
 }
 
@@ -396,13 +477,18 @@ hipError_t launch_expert_combine_backward(const ExpertShape &s, const int32_t *p
                                           uint16_t *dx, int64_t lddx, int64_t cols,
                                           hipStream_t stream) {
     const int64_t groups = cols / 8;
-    const int64_t token_blocks = (s.tokens + THREADS / 64 - 1) / (THREADS / 64);
+    // A wave per token, or a workgroup where its row is longer than 1024 columns.  us
+    // with a wave / a workgroup, of two choices without dx: 16384 tokens of 512 columns
+    // 11.2 / 22.4, of 1024 18.5 / 27.6; 4096 of 2048 10.5 / 11.2 (with dx 15.6 / 15.6, 8192
+    // with dx 38.5 / 34.4); 1024 of 8192 12.4 / 10.9, 64 of 8192 with dx 12.6 / 8.9.
+    const int tx_log2 = groups > 128 ? 8 : 6, tokens = THREADS >> tx_log2;
+    const int64_t token_blocks = (s.tokens + tokens - 1) / tokens;
     const dim3 grid((unsigned)(token_blocks + (dx ? zero_blocks(s) : 0)));
     const auto kernel = dx ? expert_combine_backward_kernel<true>
                            : expert_combine_backward_kernel<false>;
     hipLaunchKernelGGL(kernel, grid, dim3(THREADS), 0, stream, ExpertView(s, plan), dy,
                        (uint32_t)(2 * lddy), x, (uint32_t)(2 * ldx), weights, dweights, dx,
-                       (uint32_t)(2 * lddx), groups, token_blocks);
+                       (uint32_t)(2 * lddx), groups, tx_log2, token_blocks);
     return hipGetLastError();
 }
 
