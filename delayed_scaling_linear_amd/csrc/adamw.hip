@@ -248,8 +248,13 @@ __global__ __launch_bounds__(THREADS) void grad_norm_sum_kernel(const double *__
 // ---- the step ----------------------------------------------------------------
 
 constexpr int BLOCK = FP8DSL_ADAMW_BLOCK;
-constexpr int STEP_BLOCKS = 4;                         // blocks of 256 a wave takes at once
-constexpr int STEP_TILE = WAVES * STEP_BLOCKS * BLOCK;
+// Blocks of 256 that a wave takes at once: four, for the bytes in flight, or one where
+// that gives a compute unit no more than one workgroup.  us in a graph with 1 / 2 / 4:
+// 524288 bf16 values with 8-bit states 6.0 / 6.2 / 7.5, 2^20 7.3 / 7.3 / 7.9, 2^21 10.6 /
+// 9.3 / 9.5; 2^20 fp32 values 8.1 / 8.1 / 8.0, 2^21 13.2 / 12.8 / 13.1; a toy block in fp32
+// 474 / 450 / 432 (8: 456).
+constexpr int STEP_BLOCKS = 4;
+constexpr int step_tile(int blocks) { return WAVES * blocks * BLOCK; }
 constexpr int STEP_TENSORS = 48;
 // Counters behind the step count, 128 bytes apart.
 constexpr int TICKET_GROUPS = 64;
@@ -537,7 +542,7 @@ __device__ __forceinline__ void step_blocks(const StepTensor &t, const Factors &
     }
 }
 
-template <typename P, typename G, bool STATE8>
+template <typename P, typename G, bool STATE8, int N>
 __global__ __launch_bounds__(THREADS) void adamw_kernel(const StepArgs args,
                                                         const int32_t *__restrict__ noop) {
     if (noop != nullptr && *noop != 0) return;
@@ -554,12 +559,12 @@ __global__ __launch_bounds__(THREADS) void adamw_kernel(const StepArgs args,
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     for (int tile = args.tiles - 1 - (int)blockIdx.x; tile >= 0; tile -= gridDim.x) {
         const StepTensor &t = args.t[tensor_of(args, tile)];
-        const int64_t i0 = (int64_t)(tile - t.first) * STEP_TILE + wave * STEP_BLOCKS * BLOCK;
+        const int64_t i0 = (int64_t)(tile - t.first) * step_tile(N) + wave * N * BLOCK;
         f.decay = (float)(1.0 - lr * (double)t.weight_decay);
-        if (t.n - i0 >= STEP_BLOCKS * BLOCK) {
-            step_blocks<P, G, STATE8, STEP_BLOCKS, true>(t, f, key, i0);
+        if (t.n - i0 >= N * BLOCK) {
+            step_blocks<P, G, STATE8, N, true>(t, f, key, i0);
         } else {
-            for (int64_t i = i0; i < min(t.n, i0 + STEP_BLOCKS * BLOCK); i += BLOCK)
+            for (int64_t i = i0; i < min(t.n, i0 + N * BLOCK); i += BLOCK)
                 step_blocks<P, G, STATE8, 1, false>(t, f, key, i);
         }
     }
@@ -579,6 +584,20 @@ __global__ __launch_bounds__(THREADS) void adamw_kernel(const StepArgs args,
             }
         }
     }
+}
+
+using StepKernel = void (*)(StepArgs, const int32_t *);
+template <int N>
+StepKernel adamw_kernel_of(int kind) {
+    constexpr StepKernel kernels[8] = {
+        adamw_kernel<float, float, false, N>,    adamw_kernel<uint16_t, float, false, N>,
+        adamw_kernel<float, uint16_t, false, N>, adamw_kernel<uint16_t, uint16_t, false, N>,
+        adamw_kernel<float, float, true, N>,     adamw_kernel<uint16_t, float, true, N>,
+        adamw_kernel<float, uint16_t, true, N>,  adamw_kernel<uint16_t, uint16_t, true, N>};
+    return kernels[kind];
+}
+StepKernel adamw_kernel_of(int kind, int blocks) {
+    return blocks == 1 ? adamw_kernel_of<1>(kind) : adamw_kernel_of<STEP_BLOCKS>(kind);
 }
 
 }  // namespace
@@ -617,13 +636,12 @@ hipError_t launch_adamw(const fp8_adamw_t &opt, const fp8_adamw_tensor_t *tensor
         return (t.param_dtype == FP8_DTYPE_BF16 ? 1 : 0) | (t.grad_dtype == FP8_DTYPE_BF16 ? 2 : 0) |
                (t.m_scale ? 4 : 0);
     };
-    void (*const kernels[8])(StepArgs, const int32_t *) = {
-        adamw_kernel<float, float, false>,  adamw_kernel<uint16_t, float, false>,
-        adamw_kernel<float, uint16_t, false>, adamw_kernel<uint16_t, uint16_t, false>,
-        adamw_kernel<float, float, true>,   adamw_kernel<uint16_t, float, true>,
-        adamw_kernel<float, uint16_t, true>, adamw_kernel<uint16_t, uint16_t, true>};
     int cus = 0;
     if (hipError_t e = current_cu_count(&cus)) return e;
+    int64_t tiles = 0;
+    for (int i = 0; i < count; ++i)
+        tiles += (tensors[i].n + step_tile(STEP_BLOCKS) - 1) / step_tile(STEP_BLOCKS);
+    const int blocks = tiles <= cus ? 1 : STEP_BLOCKS;
     StepArgs args;
     args.lr = opt.lr;
     args.grad_scale = grad_scale;
@@ -653,13 +671,13 @@ hipError_t launch_adamw(const fp8_adamw_t &opt, const fp8_adamw_tensor_t *tensor
                 if (t.n == 0 || kind_of(t) != kind) continue;
                 args.t[args.count++] = {t.param, t.grad, t.m, t.v, t.m_scale, t.v_scale, t.copy, t.n,
                                         args.tiles, t.weight_decay, at};
-                args.tiles += (int)((t.n + STEP_TILE - 1) / STEP_TILE);
+                args.tiles += (int)((t.n + step_tile(blocks) - 1) / step_tile(blocks));
             }
             kinds[kind] -= args.count;
             left -= args.count;
             args.last = left == 0;
             const int grid = std::max(1, std::min(args.tiles, 16 * cus));
-            hipLaunchKernelGGL(kernels[kind], dim3((unsigned)grid), dim3(THREADS), 0, stream, args,
+            hipLaunchKernelGGL(adamw_kernel_of(kind, blocks), dim3((unsigned)grid), dim3(THREADS), 0, stream, args,
                                noop);
             if (hipError_t e = hipGetLastError()) return e;
         } while (kinds[kind] > 0);

@@ -154,6 +154,20 @@ def test_many_tiles():
         _check(item, index, state, 100)
 
 
+@pytest.mark.parametrize("param, grad, bits", TYPES)
+def test_longer_waves(param, grad, bits):
+    """From a tile a compute unit on a wave takes four blocks at a time: whole ones, and
+    ends of one value to four blocks."""
+    sizes = [4096 * 300 + extra for extra in (0, 1, 255, 256, 1029, 2047, 4095)]
+    items = [_make(n, param, grad, bits, i, copy=param == torch.float32 and i % 2 == 1)
+             for i, n in enumerate(sizes)]
+    opt = _adamw(items, t=7)
+    before = [_state(i) for i in items]
+    opt.step()
+    for index, (item, state) in enumerate(zip(items, before)):
+        _check(item, index, state, 8)
+
+
 def test_no_tensors_count_a_step():
     opt = _adamw([], t=7)
     opt.step()
