@@ -340,15 +340,19 @@ __global__ __launch_bounds__(THREADS) void expert_combine_kernel(
 // dy[t] . x[slot] for up to PAIRS choices of a token at once, so that dy is read once
 // for them and all their rows are in flight together.  2^tx_log2 lanes (64 or 256) take
 // a token; their sums meet in a butterfly, and those of four waves in LDS in wave order.
+//
+// Bound by its bytes where tokens are many: 8192 x 2048, two choices, with dx 34 us (168
+// MB, 4.9 TB/s; eight choices at once 40, a workgroup for each four 37), and by the chain
+// plan, slots, rows where they are few (256 x 2048: 3.9 us in a graph).
 constexpr int PAIRS = 4;
 template <bool DX>
 __global__ __launch_bounds__(THREADS) void expert_combine_backward_kernel(
     ExpertView plan, const uint16_t *__restrict__ dy, uint32_t lddy, const uint16_t *x,
     uint32_t ldx, const float *__restrict__ weights, float *__restrict__ dweights, uint16_t *dx,
     uint32_t lddx, int64_t groups, int tx_log2, int64_t token_blocks) {
-    if (!plan.built()) return;
+    const bool built = plan.built();
     if (blockIdx.x >= token_blocks) {
-        zero_rows(plan, blockIdx.x - token_blocks, dx, lddx, groups);
+        if (built) zero_rows(plan, blockIdx.x - token_blocks, dx, lddx, groups);
         return;
     }
     __shared__ float part[THREADS / 64][PAIRS];
@@ -364,10 +368,12 @@ __global__ __launch_bounds__(THREADS) void expert_combine_backward_kernel(
         float w[PAIRS], sum[PAIRS];
 #pragma unroll
         for (int j = 0; j < PAIRS; ++j) {
-            slot[j] = k0 + j < plan.top_k ? plan.slots[pair + j] : -1;
-            w[j] = DX && slot[j] >= 0 ? weights[pair + j] : 0.0f;
+            const bool there = k0 + j < plan.top_k;
+            slot[j] = there ? plan.slots[pair + j] : -1;
+            w[j] = DX && there ? weights[pair + j] : 0.0f;    // not used without a slot
             sum[j] = 0.0f;
         }
+        if (!built) return;                              // read beside the slots
         for (int64_t g = lane; g < groups; g += tx) {
             const u32x4 a = *reinterpret_cast<const u32x4 *>(row + 16 * g);
             u32x4 v[PAIRS];
