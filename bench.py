@@ -791,6 +791,20 @@ def _adamw(params, capturable: bool = False):
         return torch.optim.AdamW(params, lr=1e-3, foreach=True, capturable=capturable)
 
 
+def _library_adamw(dsl, stack, bits: int = 32):
+    """The library's AdamW on the training stack's fp32 master weights and biases, with
+    moments in 32 or 8 bits; the biases' bf16 copies are written by the step."""
+    tensors = []
+    for b in range(stack.blocks):
+        for l in range(len(stack.lin)):
+            tensors.append(dsl.AdamWTensor.zeros(stack.w[b][l], stack.grad_w[b][l], bits,
+                                                 weight_decay=0.01))
+            if stack.b32[b][l] is not None:
+                tensors.append(dsl.AdamWTensor.zeros(stack.b32[b][l], stack.grad_b[b][l], bits,
+                                                     copy=stack.b16[b][l], weight_decay=0.01))
+    return dsl.AdamW(tensors, lr=1e-3)
+
+
 def capture_train_step(stack, x, target, opt, warmup: int = 2):
     """The whole training step of `stack` (forward, loss gradient, backward,
     scale update, optimizer step) captured in one HIP graph.  `opt` must be
@@ -813,7 +827,8 @@ def capture_train_step(stack, x, target, opt, warmup: int = 2):
 def toy_stack_train_step(dsl, workloads, blocks: int = 32, warmup: int = 10, iters: int = 50):
     """One training step of the 32-block toy stack, timed as the page times
     its model (10 warm-up iterations, then `iters` between one event pair):
-    forward, MSE loss, backward, AdamW on fp32 master weights.
+    forward, MSE loss, backward, AdamW on fp32 master weights (torch's; the FP8
+    step is also timed with the library's).
 
     FP8: the library stack (fused producers; per linear an E5M2 gradient cast
     with fused bias gradient, dgrad from the cached weight transpose, fp32
@@ -843,6 +858,15 @@ def toy_stack_train_step(dsl, workloads, blocks: int = 32, warmup: int = 10, ite
         g_ms, g_wall = _time_loop(graph.replay, iters, warmup)
     res["fp8_step_graph_ms"], res["fp8_step_graph_wall_ms"] = round(g_ms, 2), round(g_wall, 2)
     del graph, opt_g
+    # The same step with the library's AdamW, moments in 32 and in 8 bits.
+    for bits in (32, 8):
+        own = _library_adamw(dsl, stack, bits)
+        with torch.no_grad():
+            own_ms, _ = _time_loop(lambda: stack.train_step(x, target, own), 20, 5)
+            own_alone_ms, _ = _time_loop(own.step, 10, 2)
+        res[f"fp8_step_library_adamw_{bits}bit_ms"] = round(own_ms, 2)
+        res[f"library_adamw_{bits}bit_alone_ms"] = round(own_alone_ms, 2)
+        del own
 
     ws32 = [list(zip(stack.w[b], stack.b32[b])) for b in range(blocks)]
     crit = torch.nn.MSELoss()

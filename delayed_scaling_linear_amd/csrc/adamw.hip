@@ -383,6 +383,13 @@ __device__ __forceinline__ void decode(uint32_t codes, float scale, float (&x)[4
     x[2] = __builtin_amdgcn_cvt_f32_fp8((int)codes, 2) * scale;
     x[3] = __builtin_amdgcn_cvt_f32_fp8((int)codes, 3) * scale;
 }
+// The code 0x7F of a second moment is an infinity, as an overflowed sum of squares is
+// in fp32: it holds its parameter still (a NaN gradient leaves its NaN in m).
+__device__ __forceinline__ void decode_square(uint32_t codes, float scale, float (&x)[4]) {
+    decode(codes, scale, x);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[k] = fminf(x[k], __builtin_inff());   // of a NaN: the infinity
+}
 
 // sqrt within 2^-23 of itself: the instruction does not take denormal numbers.
 __device__ __forceinline__ float root_of(float x) {
@@ -468,7 +475,7 @@ __device__ __forceinline__ void step_blocks(const StepTensor &t, const Factors &
         const int64_t b = i0 + s * BLOCK, i = b + 4 * lane;
         if constexpr (STATE8) {
             decode(mc[s], ms[s], m[s]);
-            decode(vc[s], vs[s], v[s]);
+            decode_square(vc[s], vs[s], v[s]);
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {

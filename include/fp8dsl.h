@@ -999,7 +999,8 @@ int fp8_grad_norm(const fp8_grad_t *grads, int32_t count, float max_norm, float 
  * One tensor of fp8_adamw_step: n values, stored one after another.
  *
  * The states m and v are fp32, or with m_scale and v_scale E4M3 codes: value i
- * is the code's times scale[i / 256], a power of two.  Zeros (codes and scales)
+ * is the code's times scale[i / 256], a power of two (a v of code 0x7F is an
+ * infinity).  Zeros (codes and scales)
  * are the state before the first step in either form.
  */
 typedef struct fp8_adamw_tensor {
@@ -1052,9 +1053,10 @@ typedef struct fp8_adamw {
  * their distance from the lower one and u is a 16-bit random number.  Rounded to
  * nearest instead, v would not fall (a step takes 1 - beta2 of it, the format's
  * half step is 2^-4) and a bf16 parameter would not take small updates.  A v
- * above 0 is never stored as 0, and what is not finite is stored as the code 0x7F
- * (NaN).  The update of p uses m and v before they are stored.  copy is p rounded
- * to nearest even.
+ * above 0 is never stored as 0.  What is not finite is stored as the code 0x7F, in m
+ * a NaN, in v an infinity: a v that overflows (a gradient above 5e20 or so) then
+ * holds its own parameter still, as it does in fp32.  The update of p uses m and v
+ * before they are stored.  copy is p rounded to nearest even.
  *
  * Random numbers: Philox4x32 with 7 rounds (see fp8_dropout_desc), key seed,
  * counter words (group, 2 i + s, t low, t high) for tensor i of the array.

@@ -24,7 +24,10 @@ def e4m3_values():
 VALUES = e4m3_values()
 
 
-def decode(codes, scales):
+def decode(codes, scales, square=False):
+    """The values of codes; of a second moment (square) 0x7F is an infinity."""
+    if square:
+        return np.where(codes == 0x7F, F(np.inf), decode(codes, scales))
     return (VALUES[codes] * np.repeat(scales.astype(np.float64), BLOCK)[:codes.size]).astype(F)
 
 

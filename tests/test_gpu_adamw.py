@@ -59,8 +59,8 @@ def _state(item):
     if item.m_scale is None:
         m, v = f32(item.m), f32(item.v)
     else:
-        m, v = (ref.decode(bits8(c), f32(s)) for c, s in ((item.m, item.m_scale),
-                                                         (item.v, item.v_scale)))
+        m = ref.decode(bits8(item.m), f32(item.m_scale))
+        v = ref.decode(bits8(item.v), f32(item.v_scale), square=True)
     return _values(item.param), _values(item.grad).astype(F), m, v
 
 
@@ -207,6 +207,7 @@ def test_special_gradients(bits):
         got = f32(item.param)
         bad = np.isnan(p1)
         assert bad[3] and (np.isnan(got) == bad).all()
+        assert not bad[515] and v1[515] == np.inf            # overflowed: held still
         if bits == 32:
             np.testing.assert_array_equal(f32(item.m), m1)
             np.testing.assert_array_equal(f32(item.v), v1)
