@@ -3,6 +3,15 @@
 // The tensors of a launch are kernel arguments (by value, within the 4 KB that a
 // launch takes), so a call reads no host memory later and can be captured; their
 // tiles are one list, which the workgroups share evenly.
+//
+// Bound by memory: the step moves 28 bytes a value in fp32, 16 with 8-bit moments, 10
+// with bf16 parameters and gradients on top (there the generator, 13 quarter-rate multiplies
+// per four values, and the arithmetic come near the memory's time).  Measured on MI355X,
+// where a large copy moves 5.1 TB/s: 32 million values in fp32 159 us (5.9 TB/s), with 8-bit
+// moments 96 (5.6), all of it in bf16 with them 67 (5.0); the 2.7 billion of the 32-block
+// toy stack 13.2 ms (5.7) and 7.8 ms.  The norm reads 2 GiB at 6.0 TB/s, 336 MB at 5.3; behind
+// other kernels it pays for the writing back of what they left in the last-level cache.
+// Small calls: a step of two adapters (2^19 bf16 values) 6.1 us in a graph.
 #include "adamw.h"
 
 #include <math.h>

@@ -1019,6 +1019,12 @@ hipError_t launch_dropout_cast_fmt(const uint16_t *x, int64_t ldx, const uint16_
 // tile in the lane layout of the cast; a tile lies within one segment, and a lane
 // finds the tokens of its four rows in the plan's sources.  Rows without a pair are
 // zeros.  Workgroups behind the plan's last tile have nothing to do.
+//
+// A source row is read once for each of its pairs, from the last-level cache after the
+// first (ordinary loads: they have to stay there).  8192 tokens of 2048 columns, two
+// choices, to E4M3: 25.6 us a call for 101 MB that it cannot do without (3.9 TB/s; 134 MB
+// with the second reads, the rate of a plain cast of as many rows).  Small calls are the
+// chain plan, sources, rows, stores: 16 tokens 4.3 us in a graph.
 template <int FMT, bool WANT_Q, bool WANT_QT, bool WEIGHTS>
 __global__ __launch_bounds__(THREADS) void expert_gather_cast_kernel(
     ExpertView plan, const uint16_t *__restrict__ x, uint32_t ldx, int64_t cols,
@@ -1100,10 +1106,17 @@ hipError_t launch_expert_gather_cast_fmt(const ExpertShape &shape, const int32_t
                                          const int32_t *noop, hipStream_t stream) {
     const int64_t tiles_c = (cols + TILE - 1) / TILE;
     const dim3 grid((unsigned)(shape.tiles_max * tiles_c));
+    // Six workgroups of 17 KB of LDS fit a CU by their registers.  Where they are more
+    // than about a round, five do better, which 12 KB more of LDS each makes them: us
+    // with six / five, 16384 x 1024, two choices, E4M3 27.2 / 25.5, 2048 x 8192 28.1 / 25.8; a
+    // round and less 4096 x 2048 12.1 / 12.1, 5003 x 1168 (1560 tiles) 18.0 / 19.2.
+    int cus = 0;
+    if (hipError_t e = current_cu_count(&cus)) return e;
+    const unsigned lds = shape.tiles_max * tiles_c > 7 * (int64_t)cus ? 12 * 1024 : 0;
     auto launch = [&](auto wq, auto wqt) {
         hipLaunchKernelGGL((expert_gather_cast_kernel<FMT, decltype(wq)::value,
                                                       decltype(wqt)::value, WEIGHTS>),
-                           grid, dim3(THREADS), 0, stream, ExpertView(shape, plan), x,
+                           grid, dim3(THREADS), lds, stream, ExpertView(shape, plan), x,
                            (uint32_t)(2 * ldx), cols, weights, scale, q, qt, amax_cur,
                            scale_inv_out, noop, tiles_c);
     };

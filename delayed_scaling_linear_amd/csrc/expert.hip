@@ -6,6 +6,17 @@
 //   backward  dw[t, k] = dy[t] . x[slot(t, k)], dx[slot(t, k)] = w[t, k] dy[t].
 //
 // (The gather with the cast is in the cast's file, whose tile it uses.)
+//
+// The rows' kernels move bytes: a token's row is read once for all its choices (gather,
+// backward), an expert's row once (combine), and written in whole.  Everything about a
+// pair comes from the plan, so no kernel searches.
+//
+// Measured on MI355X, where a large copy moves 5.1 TB/s (us a call on inputs that are not
+// in the caches, and in brackets its bytes at that rate): gather of 4096 tokens x 2048
+// to 8 of 64 experts 27.4 (27.0), combine of 16384 x 4096 with 4 choices onto a residual
+// 161 (158), backward of 8192 x 2048 with 2 choices 34.1 (33.0), its weights alone of
+// 1037 x 1160 with 6 choices 7.5 (3.0); in a graph, combine of 16 x 2048 2.7, plan of 64
+// tokens with 8 of 64 experts 5.5 (one launch), of 65536 with 4 of 128 13.7 (two).
 #include "expert.h"
 
 #include "fp8dsl_internal.h"
@@ -76,8 +87,8 @@ __global__ __launch_bounds__(PLAN_THREADS) void expert_count_kernel(
 //
 // Bound by latency: a chain of loads, LDS passes and barriers.  Every workgroup adds
 // up the counts of all pieces for itself (64 KB from the L2 at 128 experts), spread
-// over all its threads with eight loads in flight each, which is faster than a launch
-// between the two.
+// over all its threads with eight loads in flight each: 65536 tokens with 4 of 128
+// experts 13.7 us, 37 with a thread an expert and a load at a time.
 __global__ __launch_bounds__(PLAN_THREADS) void expert_place_kernel(
     const int32_t *__restrict__ ids, int64_t pairs, int64_t piece, int pieces, int tokens,
     int top_k, int experts, int capacity, int rows, const int32_t *__restrict__ hist,
@@ -280,7 +291,8 @@ __device__ __forceinline__ void zero_rows(const ExpertView &plan, int64_t block,
     }
 }
 
-// A workgroup covers 2^tx_log2 groups of 8 columns of 256 / 2^tx_log2 tokens.
+// A workgroup covers 2^tx_log2 groups of 8 columns of 256 / 2^tx_log2 tokens; a lane
+// reads its 16 bytes once and writes them to each of the token's slots.
 __global__ __launch_bounds__(THREADS) void expert_gather_kernel(
     ExpertView plan, const uint16_t *__restrict__ x, uint32_t ldx, uint16_t *__restrict__ y,
     uint32_t ldy, int64_t groups, int tx_log2, int64_t token_blocks) {
@@ -300,7 +312,7 @@ __global__ __launch_bounds__(THREADS) void expert_gather_kernel(
     }
 }
 
-// The same split.
+// The same split; a lane keeps the fp32 sums of its 8 columns.
 template <bool WEIGHTS>
 __global__ __launch_bounds__(THREADS) void expert_combine_kernel(
     ExpertView plan, const uint16_t *__restrict__ x, uint32_t ldx,
