@@ -1053,16 +1053,25 @@ def fp8_expert_plan(expert_ids: torch.Tensor, plan: ExpertPlan, stream=None) -> 
     _need_shape(expert_ids, (plan.tokens, plan.top_k), "expert_ids")
     ids = _ptr(expert_ids, torch.int32, "expert_ids")
     _on_current_device(expert_ids, plan.buf)
-    _check(lib().fp8_expert_plan(ctypes.byref(plan._sizes), ids, *_ws(plan.buf), _stream(stream)),
+    _check(lib().fp8_expert_plan(_expert_sizes(plan), ids, *_ws(plan.buf), _stream(stream)),
            "fp8_expert_plan")
     plan.built = True
+
+
+def _expert_sizes(plan: ExpertPlan):
+    """The sizes as the C calls take them, which the checks of shapes have to agree with."""
+    s = plan._sizes
+    if s.tokens != plan.tokens or s.top_k != plan.top_k or s.experts != plan.experts \
+            or s.capacity != plan.capacity:
+        raise ValueError("a plan keeps the sizes that it was made for: make another one")
+    return ctypes.byref(s)
 
 
 def _expert_call(plan: ExpertPlan):
     """The arguments that the calls with a plan begin with."""
     if not plan.built:
         raise ValueError("the plan has not been built (fp8_expert_plan)")
-    return (ctypes.byref(plan._sizes), *_ws(plan.buf))
+    return (_expert_sizes(plan), *_ws(plan.buf))
 
 
 def _columns(t: torch.Tensor, what: str) -> int:
@@ -1195,26 +1204,32 @@ class AdamWTensor:
         return AdamWTensor(param, grad, m, v, *scales, copy=copy, weight_decay=weight_decay)
 
     def desc(self) -> _AdamWTensorDesc:
-        """The C descriptor, built at the first call and again if a field is another
-        tensor since, or has been moved, reshaped or given another type in place."""
+        """The C descriptor, built at the first call and again if a field is a tensor
+        elsewhere since, or of another shape or type.  Keeps no tensor alive: a gradient
+        may be dropped between steps."""
         fields = (self.param, self.grad, self.m, self.v, self.m_scale, self.v_scale, self.copy)
         seen = self._seen
         if seen is not None and seen[0] == self.weight_decay and seen[1] == _device():
-            for t, (old, ptr, shape, dtype) in zip(fields, seen[2]):
-                if t is not old or t is not None and (
-                        t.data_ptr() != ptr or t.shape != shape or t.dtype is not dtype
-                        or not t.is_contiguous()):
+            dev = seen[1]
+            for t, old in zip(fields, seen[2]):
+                if t is None or old is None:
+                    if t is not old:
+                        break
+                elif t.data_ptr() != old[0] or t.shape != old[1] or t.dtype is not old[2] \
+                        or not t.is_contiguous() or t.get_device() != dev:
                     break
             else:
                 return seen[3]
         d = self._checked()
         self._seen = (self.weight_decay, _device(), tuple(
-            (t, None, None, None) if t is None else (t, t.data_ptr(), t.shape, t.dtype)
-            for t in fields), d)
+            None if t is None else (t.data_ptr(), t.shape, t.dtype) for t in fields), d)
         return d
 
     def _checked(self) -> _AdamWTensorDesc:
         p, g, m, v, copy = self.param, self.grad, self.m, self.v, self.copy
+        for t, what in ((p, "param"), (g, "grad"), (m, "m"), (v, "v")):
+            if t is None:
+                raise ValueError(f"{what} is required")
         n, shape = p.numel(), p.shape
         for t, what in ((p, "param"), (g, "grad")):
             if t.dtype not in _ADAMW_DTYPES:
@@ -1304,7 +1319,7 @@ def fp8_grad_norm(grads, norm: torch.Tensor, workspace: torch.Tensor,
         _need_scalar(t, what)
     if norm is None or workspace is None:
         raise ValueError("norm and workspace are required")
-    descs = []
+    grads, descs = list(grads), []
     for g in grads:
         if g.dtype not in _ADAMW_DTYPES:
             raise TypeError(f"grads must be fp32 or bf16, got {g.dtype}")

@@ -48,7 +48,8 @@ __device__ __forceinline__ int wave_inclusive(int v, int lane) {
 // Ids that a lane reads at once.
 constexpr int PLAN_IDS = 4;
 
-// Calls what(p, id) for the ids of p0 .. p1 - 1, `stride` of them a step.
+// Calls what(id) for the ids of p0 .. p1 - 1, `stride` of them side by side, and for
+// some that name no expert behind them.
 template <typename What>
 __device__ __forceinline__ void for_ids(const int32_t *__restrict__ ids, int64_t p0, int64_t p1,
                                         int lane, int stride, What what) {

@@ -119,7 +119,8 @@ def test_python_refusals():
     assert t.m.dtype == torch.uint8 and t.m_scale.shape == (2,) and t.m_scale.sum() == 0
     with pytest.raises(ValueError):                     # not on a device
         t.desc()
-    for change, error in ((dict(grad=g.double()), TypeError), (dict(param=p.half()), TypeError),
+    for change, error in ((dict(grad=None), ValueError), (dict(v=None), ValueError),
+                          (dict(grad=g.double()), TypeError), (dict(param=p.half()), TypeError),
                           (dict(v_scale=None), ValueError),
                           (dict(param=p.bfloat16(), copy=p.bfloat16()), TypeError)):
         fields = dict(param=p, grad=g, m=t.m, v=t.v, m_scale=t.m_scale, v_scale=t.v_scale)

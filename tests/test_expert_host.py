@@ -187,6 +187,18 @@ def test_python_refusals():
         dsl.fp8_expert_combine_backward(plan, x.to("meta"), y.to("meta"), None, dx=y.to("meta"))
 
 
+def test_a_plan_keeps_its_sizes():
+    """The shapes that the calls check and the sizes that the kernels use are the same."""
+    for name, value in (("tokens", 5), ("top_k", 3), ("experts", 4), ("capacity", 16)):
+        plan = dsl.ExpertPlan.empty(4, 2, 3, device="cpu")
+        plan.built = True
+        setattr(plan, name, value)
+        with pytest.raises(ValueError, match="sizes"):
+            dsl._expert_call(plan)
+    with pytest.raises(ValueError, match="built"):
+        dsl._expert_call(dsl.ExpertPlan.empty(4, 2, 3, device="cpu"))
+
+
 def test_segments():
     """Each expert's part of a tensor in expert order."""
     plan = dsl.ExpertPlan.empty(40, 1, 3, device="cpu")

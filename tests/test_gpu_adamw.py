@@ -8,6 +8,8 @@ root, sum and quotient are within 6 * 2^-24 + 2^-22 of it.  A bf16 parameter mus
 lie between the stochastic roundings of the ends of that interval: with one number u
 the rounding never falls where its argument rises.  (Nearly always the ends agree;
 where p0 and the update nearly cancel, the interval holds several bf16 values.)"""
+import weakref
+
 import numpy as np
 import pytest
 import torch
@@ -409,6 +411,25 @@ def test_clipped_steps_captured(bits):
         assert int(own_a[2]) == (i == 3) and _state_words(a) == 3 + 1 + i + (i < 3)
 
 
+def test_a_dropped_gradient_is_not_kept():
+    """What a program frees between steps is free; the next gradient may lie in its place
+    or elsewhere."""
+    item = _make(3000, torch.float32, torch.float32, 8, 9)
+    opt = _adamw([item], t=1)
+    for t in (2, 3, 4):
+        before = _state(item)
+        opt.step()
+        _check(item, 0, before, t)
+        gone = weakref.ref(item.grad)
+        item.grad = None
+        assert gone() is None
+        with pytest.raises(ValueError):
+            opt.step()
+        hold = torch.empty(3000 * t, device=DEV)
+        item.grad = torch.randn(3000, generator=torch.Generator(DEV).manual_seed(t), device=DEV)
+        del hold
+
+
 def test_handles_see_what_changed():
     """A tensor of another shape or type in a handle is noticed at the next step."""
     item = _make(300, torch.float32, torch.float32, 8, 8)
@@ -426,6 +447,10 @@ def test_handles_see_what_changed():
     with pytest.raises(TypeError):
         opt.step()
     assert _state_words(opt) == 2
+    item.m = torch.zeros(300, dtype=torch.uint8, device=DEV)
+    item.m_scale, item.v_scale = item.m_scale.cpu(), item.v_scale.cpu()
+    with pytest.raises(ValueError):
+        opt.step()
     odd = torch.zeros(304, device=DEV)[1:301]
     item = dsl.AdamWTensor.zeros(odd, torch.zeros(300, device=DEV))
     with pytest.raises(dsl.Fp8Error):                        # not 16-byte aligned

@@ -181,6 +181,17 @@ def test_gather_cast_specials(how):
         assert not codes.any() and float(amax) == 0.0
 
 
+def test_gather_cast_without_a_kept_pair():
+    """Segments without rows: no tile, an untouched buffer and amax, the scale-inverse."""
+    plan, x = _plan(np.full((40, 2), -1, np.int32), 3), _rand((40, 64), 11).to(DEV)
+    q, amax = dsl.Float8Tensor.empty(plan.rows, 64, dsl.E4M3), torch.full((1,), 2.0, device=DEV)
+    q.data.fill_(7)
+    q.data_t.fill_(7)
+    dsl.fp8_expert_gather_cast_transpose_amax(plan, x, torch.tensor([4.0], device=DEV), q, amax)
+    assert (q.data == 7).all() and (q.data_t == 7).all()
+    assert float(amax) == 2.0 and float(q.scale_inv) == 0.25
+
+
 def test_gather_cast_noop_and_empty():
     ids = _ids(40, 2, 3, 10, "all")
     plan, x = _plan(ids, 3, 32), _rand((40, 64), 11).to(DEV)
