@@ -965,12 +965,19 @@ class ExpertPlan:
     built: bool = False
 
     def __post_init__(self):
-        self._sizes = _ExpertSizes(self.tokens, self.capacity, self.top_k, self.experts)
+        self._sizes = ctypes.byref(_ExpertSizes(self.tokens, self.capacity, self.top_k,
+                                                self.experts))
         self.rows = fp8_expert_rows(self.tokens, self.top_k, self.experts, self.capacity)
         self._viewed = None
         self._layout = _ExpertLayout()
-        _check(lib().fp8_expert_plan_layout(ctypes.byref(self._sizes),
-                                            ctypes.byref(self._layout)), "fp8_expert_plan_layout")
+        _check(lib().fp8_expert_plan_layout(self._sizes, ctypes.byref(self._layout)),
+               "fp8_expert_plan_layout")
+
+    def __setattr__(self, name, value):
+        # The checks of shapes and the kernels go by the same sizes.
+        if name in ("tokens", "top_k", "experts", "capacity", "rows") and "rows" in self.__dict__:
+            raise ValueError("a plan keeps the sizes that it was made for: make another one")
+        object.__setattr__(self, name, value)
 
     @staticmethod
     def empty(tokens: int, top_k: int, experts: int, capacity: int = 0,
@@ -1053,25 +1060,16 @@ def fp8_expert_plan(expert_ids: torch.Tensor, plan: ExpertPlan, stream=None) -> 
     _need_shape(expert_ids, (plan.tokens, plan.top_k), "expert_ids")
     ids = _ptr(expert_ids, torch.int32, "expert_ids")
     _on_current_device(expert_ids, plan.buf)
-    _check(lib().fp8_expert_plan(_expert_sizes(plan), ids, *_ws(plan.buf), _stream(stream)),
+    _check(lib().fp8_expert_plan(plan._sizes, ids, *_ws(plan.buf), _stream(stream)),
            "fp8_expert_plan")
     plan.built = True
-
-
-def _expert_sizes(plan: ExpertPlan):
-    """The sizes as the C calls take them, which the checks of shapes have to agree with."""
-    s = plan._sizes
-    if s.tokens != plan.tokens or s.top_k != plan.top_k or s.experts != plan.experts \
-            or s.capacity != plan.capacity:
-        raise ValueError("a plan keeps the sizes that it was made for: make another one")
-    return ctypes.byref(s)
 
 
 def _expert_call(plan: ExpertPlan):
     """The arguments that the calls with a plan begin with."""
     if not plan.built:
         raise ValueError("the plan has not been built (fp8_expert_plan)")
-    return (_expert_sizes(plan), *_ws(plan.buf))
+    return (plan._sizes, *_ws(plan.buf))
 
 
 def _columns(t: torch.Tensor, what: str) -> int:
@@ -1210,14 +1208,13 @@ class AdamWTensor:
         fields = (self.param, self.grad, self.m, self.v, self.m_scale, self.v_scale, self.copy)
         seen = self._seen
         if seen is not None and seen[0] == self.weight_decay and seen[1] == _device():
-            dev = seen[1]
             for t, old in zip(fields, seen[2]):
                 if t is None or old is None:
                     if t is not old:
                         break
                 elif t.data_ptr() != old[0] or t.shape != old[1] or t.dtype is not old[2] \
-                        or not t.is_contiguous() or t.get_device() != dev:
-                    break
+                        or not t.is_contiguous():
+                    break                    # (one address is one device's)
             else:
                 return seen[3]
         d = self._checked()
@@ -1280,11 +1277,12 @@ class AdamW:
         return [t.grad for t in self.tensors]
 
     def desc(self) -> _AdamWDesc:
-        _need_scalar(self.lr, "lr")
-        _need_shape(self.state, (ADAMW_STATE_BYTES // 8,), "state")
-        _on_current_device(self.lr, self.state)
-        return _AdamWDesc(_ptr(self.lr, torch.float32, "lr"),
-                          _ptr(self.state, torch.int64, "state"), self.betas[0], self.betas[1], self.eps, self.seed & (2 ** 64 - 1))
+        lr, state = self.lr, self.state
+        _need_scalar(lr, "lr")
+        _need_shape(state, (ADAMW_STATE_BYTES // 8,), "state")
+        _on_current_device(lr, state)
+        return _AdamWDesc(_ptr(lr, torch.float32, "lr"), _ptr(state, torch.int64, "state"),
+                          *self.betas, self.eps, self.seed & (2 ** 64 - 1))
 
     def _tensor_array(self):
         """The tensors' descriptors as the C call takes them; those that have not changed

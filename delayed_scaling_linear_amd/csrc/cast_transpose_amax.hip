@@ -1087,7 +1087,7 @@ __global__ __launch_bounds__(THREADS) void expert_gather_cast_kernel(
                     const float v0 = w[i] * bf16_lo(xw), v1 = w[i] * bf16_hi(xw);
                     const uint32_t y0 = (v0 != v0) ? 0x7FC0u : f32_to_bf16_bits_rne(v0);
                     const uint32_t y1 = (v1 != v1) ? 0x7FC0u : f32_to_bf16_bits_rne(v1);
-                    ys[i].v[h][k] = pair[i] >= 0 ? y0 | (y1 << 16) : 0u;
+                    ys[i].v[h][k] = y0 | (y1 << 16);     // +0 without a pair: 0 * 0
                 }
     }
     uint32_t key = 0;
@@ -1109,7 +1109,7 @@ hipError_t launch_expert_gather_cast_fmt(const ExpertShape &shape, const int32_t
     // Six workgroups of 17 KB of LDS fit a CU by their registers.  Where they are more
     // than about a round, five do better, which 12 KB more of LDS each makes them: us
     // with six / five, 16384 x 1024, two choices, E4M3 27.2 / 25.5, 2048 x 8192 28.1 / 25.8; a
-    // round and less 4096 x 2048 12.1 / 12.1, 5003 x 1168 (1560 tiles) 18.0 / 19.2.
+    // round and less 4096 x 2048 12.1 / 12.1, 5003 x 1168 (1560 tiles) 17.7 / 18.9.
     int cus = 0;
     if (hipError_t e = current_cu_count(&cus)) return e;
     const unsigned lds = shape.tiles_max * tiles_c > 7 * (int64_t)cus ? 12 * 1024 : 0;

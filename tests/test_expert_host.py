@@ -189,12 +189,12 @@ def test_python_refusals():
 
 def test_a_plan_keeps_its_sizes():
     """The shapes that the calls check and the sizes that the kernels use are the same."""
-    for name, value in (("tokens", 5), ("top_k", 3), ("experts", 4), ("capacity", 16)):
-        plan = dsl.ExpertPlan.empty(4, 2, 3, device="cpu")
-        plan.built = True
-        setattr(plan, name, value)
+    plan = dsl.ExpertPlan.empty(4, 2, 3, device="cpu")
+    for name, value in (("tokens", 5), ("top_k", 3), ("experts", 4), ("capacity", 16), ("rows", 8)):
         with pytest.raises(ValueError, match="sizes"):
-            dsl._expert_call(plan)
+            setattr(plan, name, value)
+    plan.built = True
+    assert dsl.ExpertPlan(plan.buf, 4, 2, 3).rows == plan.rows
     with pytest.raises(ValueError, match="built"):
         dsl._expert_call(dsl.ExpertPlan.empty(4, 2, 3, device="cpu"))
 
