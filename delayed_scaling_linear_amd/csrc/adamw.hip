@@ -494,7 +494,8 @@ __device__ __forceinline__ void step_blocks(const StepTensor &t, const Factors &
         }
         uint32_t most = 0xFFFFFFFFu;
         if constexpr (STATE8) most = most_of<false>(v[s], false);
-        // A wave of ordinary values needs no look at each for the root.
+        // A wave of ordinary values needs no look at each for the root.  (The divisor,
+        // between eps and 2^101, has a normal reciprocal, or is infinite.)
         float r[4];
         if (most < 0x73000000u) {                        // 2^103
 #pragma unroll
@@ -693,8 +694,8 @@ hipError_t launch_adamw(const fp8_adamw_t &opt, const fp8_adamw_tensor_t *tensor
             left -= args.count;
             args.last = left == 0;
             const int grid = std::max(1, std::min(args.tiles, 16 * cus));
-            hipLaunchKernelGGL(adamw_kernel_of(kind, blocks), dim3((unsigned)grid), dim3(THREADS), 0, stream, args,
-                               noop);
+            hipLaunchKernelGGL(adamw_kernel_of(kind, blocks), dim3((unsigned)grid), dim3(THREADS),
+                               0, stream, args, noop);
             if (hipError_t e = hipGetLastError()) return e;
         } while (kinds[kind] > 0);
         if (left == 0) break;

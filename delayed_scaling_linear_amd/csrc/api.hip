@@ -744,7 +744,7 @@ int fp8_adamw_step(const fp8_adamw_t *opt, const fp8_adamw_tensor_t *tensors, in
     if (opt == nullptr) return FP8_ERR_NULL;
     if (count < 0 || !(opt->beta1 >= 0.0 && opt->beta1 < 1.0) ||
         !(opt->beta2 >= 0.0 && opt->beta2 < 1.0) ||
-        !((float)opt->eps >= 0x1p-126f && (float)opt->eps <= 3.402823466e38f))
+        !((float)opt->eps >= 0x1p-126f && (float)opt->eps <= 0x1p100f))
         return FP8_ERR_ARG;
     if (opt->lr == nullptr || opt->state == nullptr || (count > 0 && tensors == nullptr))
         return FP8_ERR_NULL;

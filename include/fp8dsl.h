@@ -1028,7 +1028,7 @@ typedef struct fp8_adamw {
     int64_t *state;         /* device, FP8DSL_ADAMW_STATE_BYTES                */
     double beta1;           /* 0 <= beta1 < 1                                  */
     double beta2;           /* 0 <= beta2 < 1                                  */
-    double eps;             /* a normal number in fp32, 2^-126 or more         */
+    double eps;             /* 2^-126 .. 2^100 (in fp32)                       */
     uint64_t seed;          /* of the stochastic roundings                     */
 } fp8_adamw_t;
 

@@ -77,7 +77,7 @@ def test_step_refusals():
     assert call(count=-1) == -5
     for bad in (dict(b1=1.0), dict(b1=-0.1), dict(b1=float("nan")), dict(b2=1.0), dict(b2=-1e-9),
                 dict(eps=0.0), dict(eps=-1e-8), dict(eps=1e-60), dict(eps=float("inf")),
-                dict(eps=float("nan")), dict(eps=1e39)):
+                dict(eps=float("nan")), dict(eps=1e39), dict(eps=1.3e30), dict(eps=1.1e-38)):
         assert call(opt=_opt(**bad)) == -5, bad
     for bad in (dict(pd=2), dict(gd=-1), dict(reserved=1), dict(wd=-0.1), dict(wd=float("inf")),
                 dict(wd=float("nan")), dict(copy=0x80000, pd=0), dict(ms=0x80000),
