@@ -16,7 +16,7 @@
 // to 8 of 64 experts 27.4 (27.0), combine of 16384 x 4096 with 4 choices onto a residual
 // 161 (158), backward of 8192 x 2048 with 2 choices 34.1 (33.0), its weights alone of
 // 1037 x 1160 with 6 choices 7.5 (3.0); in a graph, combine of 16 x 2048 2.7, plan of 64
-// tokens with 8 of 64 experts 5.5 (one launch), of 65536 with 4 of 128 13.7 (two).
+// tokens with 8 of 64 experts 5.5 (one launch), of 65536 with 4 of 128 10.9 (two).
 #include "expert.h"
 
 #include "fp8dsl_internal.h"
@@ -88,8 +88,8 @@ __global__ __launch_bounds__(PLAN_THREADS) void expert_count_kernel(
 //
 // Bound by latency: a chain of loads, LDS passes and barriers.  Every workgroup adds
 // up the counts of all pieces for itself (64 KB from the L2 at 128 experts), spread
-// over all its threads with eight loads in flight each: 65536 tokens with 4 of 128
-// experts 13.7 us, 37 with a thread an expert and a load at a time.
+// over all its threads with 16 loads in flight each: 65536 tokens with 4 of 128
+// experts 10.9 us, 37 with a thread an expert and a load at a time.
 __global__ __launch_bounds__(PLAN_THREADS) void expert_place_kernel(
     const int32_t *__restrict__ ids, int64_t pairs, int64_t piece, int pieces, int tokens,
     int top_k, int experts, int capacity, int rows, const int32_t *__restrict__ hist,
@@ -110,9 +110,16 @@ __global__ __launch_bounds__(PLAN_THREADS) void expert_place_kernel(
     int *earlier = first;
     for (int i = tid; i < (PLAN_WAVES + 2) * experts; i += PLAN_THREADS) run[i] = 0;
     __syncthreads();
-    for_ids(ids, w0, w1, lane, 64, [&](uint32_t e) {
-        if (e < (uint32_t)experts) atomicAdd(&run[wave * experts + e], 1);
-    });
+    // The first ids of the run, read once for both passes.
+    uint32_t ids_of[PLAN_IDS];
+    const auto read = [&](int64_t pw) {
+#pragma unroll
+        for (int i = 0; i < PLAN_IDS; ++i) {
+            const int64_t p = pw + 64 * i + lane;
+            ids_of[i] = p < w1 ? (uint32_t)ids[p] : 0xFFFFFFFFu;
+        }
+    };
+    read(w0);
     if (pieces > 1) {
         int wide = 64;                           // threads side by side over the experts
         while (wide < experts && wide < PLAN_THREADS) wide *= 2;
@@ -120,13 +127,13 @@ __global__ __launch_bounds__(PLAN_THREADS) void expert_place_kernel(
         const int g0 = pieces * part / parts, g1 = pieces * (part + 1) / parts;
         for (int e = tid % wide; e < experts; e += wide) {
             int before = 0, total = 0;
-            for (int g = g0; g < g1; g += 8) {
-                int c[8];
+            for (int g = g0; g < g1; g += 16) {
+                int c[16];
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
+                for (int i = 0; i < 16; ++i)
                     c[i] = g + i < g1 ? hist[(int64_t)(g + i) * experts + e] : 0;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
+                for (int i = 0; i < 16; ++i) {
                     total += c[i];
                     before += g + i < (int)blockIdx.x ? c[i] : 0;
                 }
@@ -135,6 +142,12 @@ __global__ __launch_bounds__(PLAN_THREADS) void expert_place_kernel(
             atomicAdd(&earlier[e], before);
         }
     }
+    const auto count = [&](uint32_t e) {
+        if (e < (uint32_t)experts) atomicAdd(&run[wave * experts + e], 1);
+    };
+#pragma unroll
+    for (int i = 0; i < PLAN_IDS; ++i) count(ids_of[i]);
+    for_ids(ids, w0 + 64 * PLAN_IDS, w1, lane, 64, count);
     __syncthreads();
     // Pairs before each wave's run, and all pairs, of each expert.
     for (int e = tid; e < experts; e += PLAN_THREADS) {
@@ -221,12 +234,7 @@ __global__ __launch_bounds__(PLAN_THREADS) void expert_place_kernel(
 
     int *next = run + wave * experts;
     for (int64_t pw = w0; pw < w1; pw += PLAN_IDS * 64) {
-        uint32_t ids_of[PLAN_IDS];
-#pragma unroll
-        for (int i = 0; i < PLAN_IDS; ++i) {
-            const int64_t p = pw + 64 * i + lane;
-            ids_of[i] = p < w1 ? (uint32_t)ids[p] : 0xFFFFFFFFu;
-        }
+        if (pw > w0) read(pw);
 #pragma unroll
         for (int i = 0; i < PLAN_IDS; ++i) {
             const int64_t p = pw + 64 * i + lane;
