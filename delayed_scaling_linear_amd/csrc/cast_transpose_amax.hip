@@ -1022,7 +1022,7 @@ hipError_t launch_dropout_cast_fmt(const uint16_t *x, int64_t ldx, const uint16_
 //
 // A source row is read once for each of its pairs, from the last-level cache after the
 // first (ordinary loads: they have to stay there).  8192 tokens of 2048 columns, two
-// choices, to E4M3: 25.6 us a call for 101 MB that it cannot do without (3.9 TB/s; 134 MB
+// choices, to E4M3: 24 to 26 us a call for 101 MB that it cannot do without (4 TB/s; 134 MB
 // with the second reads, the rate of a plain cast of as many rows).  Small calls are the
 // chain plan, sources, rows, stores: 16 tokens 4.3 us in a graph.
 template <int FMT, bool WANT_Q, bool WANT_QT, bool WEIGHTS>
@@ -1080,15 +1080,18 @@ __global__ __launch_bounds__(THREADS) void expert_gather_cast_kernel(
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int h = 0; h < 2; ++h) {
+                // Past the columns 0 * 0 as well, whatever the weight.
+                const float wh = col0 + 64 * h + 8 * cc < cols ? w[i] : 0.0f;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const uint32_t xw = ys[i].v[h][k];
-                    const float v0 = w[i] * bf16_lo(xw), v1 = w[i] * bf16_hi(xw);
+                    const float v0 = wh * bf16_lo(xw), v1 = wh * bf16_hi(xw);
                     const uint32_t y0 = (v0 != v0) ? 0x7FC0u : f32_to_bf16_bits_rne(v0);
                     const uint32_t y1 = (v1 != v1) ? 0x7FC0u : f32_to_bf16_bits_rne(v1);
                     ys[i].v[h][k] = y0 | (y1 << 16);     // +0 without a pair: 0 * 0
                 }
+            }
     }
     uint32_t key = 0;
     encode_block<FP8_DTYPE_BF16, FMT, WANT_Q, WANT_QT>(ys, s, s_special, valid, q, r, c, cols, cq,

@@ -181,6 +181,24 @@ def test_gather_cast_specials(how):
         assert not codes.any() and float(amax) == 0.0
 
 
+@pytest.mark.parametrize("cols", [16, 144, 256])
+def test_gather_cast_infinite_weights(cols):
+    """An infinite weight makes its row infinite and nothing else, also where a tile
+    reaches past the columns."""
+    ids = _ids(40, 2, 3, 12, "all")
+    plan, want = _plan(ids, 3, 48), ref.plan(ids, 3, 48)
+    x = _rand((40, cols), 13).abs() + 1.0
+    w = torch.full((40, 2), 0.5)
+    w[7, 1], w[9, 0] = float("inf"), float("-inf")
+    amax, q = torch.zeros(1, device=DEV), dsl.Float8Tensor.empty(plan.rows, cols, dsl.E5M2)
+    dsl.fp8_expert_gather_cast_transpose_amax(plan, x.to(DEV), torch.ones(1, device=DEV), q, amax,
+                                              weights=w.to(DEV))
+    y = ref.gather(bits16(x), want[3], 2, plan.rows, w.numpy())
+    codes, _, top, _ = oracle.cast_transpose_amax(y, 1.0, dsl.E5M2)
+    np.testing.assert_array_equal(bits8(q.data), codes)
+    assert float(amax) == float(top) == float("inf")
+
+
 def test_gather_cast_without_a_kept_pair():
     """Segments without rows: no tile, an untouched buffer and amax, the scale-inverse."""
     plan, x = _plan(np.full((40, 2), -1, np.int32), 3), _rand((40, 64), 11).to(DEV)
