@@ -1258,8 +1258,8 @@ class AdamWTensor:
 class AdamW:
     """AdamW over `tensors` (AdamWTensor): lr is a float or a 1-element fp32
     device tensor (which a program changes between steps, graph replays
-    included), `steps` [1] (int64, device) the steps taken, a view of `state`.  `seed` feeds the
-    stochastic rounding of 8-bit moments and bf16 parameters."""
+    included), `state` (int64, device) the steps taken and the step's counters.  `seed`
+    feeds the stochastic rounding of 8-bit moments and bf16 parameters."""
 
     def __init__(self, tensors, lr=1e-3, betas=(0.9, 0.999), eps: float = 1e-8, seed: int = 0,
                  device="cuda"):
@@ -1269,7 +1269,22 @@ class AdamW:
         self.betas, self.eps, self.seed = betas, eps, seed
         self._array, self._descs = (_AdamWTensorDesc * 0)(), []
         self.state = torch.zeros(ADAMW_STATE_BYTES // 8, dtype=torch.int64, device=self.lr.device)
-        self.steps = self.state[:1]
+
+    @property
+    def steps(self) -> torch.Tensor:
+        """[1] int64: the steps taken, the first value of `state`.  Assigning a number or
+        a 1-element tensor writes it there, as a resumed run does; captured steps go on
+        from it too."""
+        return self.state[:1]
+
+    @steps.setter
+    def steps(self, taken) -> None:
+        if not isinstance(taken, torch.Tensor):
+            self.state[:1].fill_(taken)
+        elif taken.numel() == 1:
+            self.state[:1].copy_(taken.reshape(1))
+        else:
+            raise ValueError(f"steps must be a single value, got shape {tuple(taken.shape)}")
 
     @property
     def grads(self) -> list:

@@ -130,3 +130,24 @@ def test_python_refusals():
         dsl.fp8_grad_norm([g.half()], torch.zeros(1), torch.zeros(8, dtype=torch.uint8))
     with pytest.raises(ValueError):
         dsl.fp8_grad_norm([g], torch.zeros(0), torch.zeros(8, dtype=torch.uint8))
+
+
+def test_assigned_steps_are_the_state():
+    """A resumed run sets the count that the kernels read, and reads the one of a state
+    that it puts in place."""
+    opt = dsl.AdamW([], device="cpu")
+    assert opt.steps.tolist() == [0] and opt.state.tolist() == [0] * (dsl.ADAMW_STATE_BYTES // 8)
+    state = opt.state
+    for taken in (500, torch.tensor([2 ** 33]), torch.tensor(7.0), torch.zeros(1, 1).int()):
+        opt.steps = taken
+        assert opt.state is state                       # what a captured step reads
+        assert int(state[0]) == int(opt.steps) == int(taken) and not state[1:].any()
+    opt.steps += 3
+    assert int(state[0]) == 3
+    for bad in (torch.zeros(2), torch.zeros(0)):
+        with pytest.raises(ValueError, match="single"):
+            opt.steps = bad
+    opt.state = torch.arange(9, 9 + state.numel())
+    assert opt.steps.tolist() == [9] and opt.steps.dtype == torch.int64
+    opt.steps.fill_(4)
+    assert int(opt.state[0]) == 4
