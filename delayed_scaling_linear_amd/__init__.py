@@ -964,6 +964,15 @@ class ExpertPlan:
     capacity: int = 0
     built: bool = False
 
+    # A copy or an unpickled plan makes its own C arguments and views.
+    def __getstate__(self):
+        made = ("rows", "_sizes", "_layout", "_viewed", "_views")
+        return {k: v for k, v in self.__dict__.items() if k not in made}
+
+    def __setstate__(self, state):
+        self.__dict__.update(state)
+        self.__post_init__()
+
     def __post_init__(self):
         self._sizes = ctypes.byref(_ExpertSizes(self.tokens, self.capacity, self.top_k,
                                                 self.experts))

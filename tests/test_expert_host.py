@@ -1,6 +1,8 @@
 """Expert routing on the CPU: the reference against differences, sizes of plans
 and buffers, and every refusal (nothing reaches a device)."""
+import copy
 import ctypes
+import pickle
 
 import numpy as np
 import pytest
@@ -220,3 +222,24 @@ def test_segments():
         == [32, 32, 32]
     with pytest.raises(ValueError):
         fixed.segments(q)
+
+
+@pytest.mark.parametrize("capacity", [0, 32])
+def test_a_plan_is_copied_and_pickled(capacity):
+    """As part of a module it is: a copy has the sizes and a buffer and views of its own."""
+    plan = dsl.ExpertPlan.empty(40, 2, 3, capacity, device="cpu")
+    plan.buf.copy_((torch.arange(plan.buf.numel()) % 251).to(torch.uint8))
+    plan.built = True
+    offsets = plan.offsets
+    for other in (copy.deepcopy(plan), pickle.loads(pickle.dumps(plan)), copy.copy(plan)):
+        assert (other.tokens, other.top_k, other.experts, other.capacity, other.rows, other.built) \
+            == (40, 2, 3, capacity, plan.rows, True)
+        assert torch.equal(other.buf, plan.buf) and torch.equal(other.offsets, offsets)
+        sizes = other._sizes._obj
+        assert (sizes.tokens, sizes.top_k, sizes.experts, sizes.capacity) == (40, 2, 3, capacity)
+        with pytest.raises(ValueError, match="sizes"):
+            other.tokens = 41
+    deep = copy.deepcopy({"plan": plan, "buf": plan.buf})
+    assert deep["plan"].buf is deep["buf"] and deep["buf"].data_ptr() != plan.buf.data_ptr()
+    deep["buf"].zero_()
+    assert not deep["plan"].offsets.any() and torch.equal(plan.offsets, offsets)
