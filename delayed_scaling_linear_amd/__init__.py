@@ -996,14 +996,14 @@ class ExpertPlan:
                           capacity)
 
     def _view(self, i: int) -> torch.Tensor:
-        """The plan's arrays, made once for the buffer."""
-        if self._viewed is not self.buf:
+        """The plan's arrays, made once for the buffer's memory (which they keep alive)."""
+        if self._viewed != self.buf.data_ptr():
             at, n, tk = self._layout, self.experts, self.tokens * self.top_k
             words = lambda first, count: self.buf[first:first + 4 * count].view(torch.int32)
             self._views = (words(at.offsets, n + 1), words(at.counts, n),
                            words(at.slots, tk).view(self.tokens, self.top_k),
                            words(at.sources, self.rows))
-            self._viewed = self.buf
+            self._viewed = self.buf.data_ptr()
         return self._views[i]
 
     @property

@@ -243,3 +243,16 @@ def test_a_plan_is_copied_and_pickled(capacity):
     assert deep["plan"].buf is deep["buf"] and deep["buf"].data_ptr() != plan.buf.data_ptr()
     deep["buf"].zero_()
     assert not deep["plan"].offsets.any() and torch.equal(plan.offsets, offsets)
+
+
+def test_views_follow_the_buffer():
+    """A buffer given other memory in place, or replaced, is the one that is seen."""
+    plan = dsl.ExpertPlan.empty(40, 2, 3, device="cpu")
+    plan.buf.zero_()
+    assert plan.offsets.tolist() == [0, 0, 0, 0] and plan.offsets is plan.offsets
+    for change in (lambda b: setattr(plan.buf, "data", b), lambda b: plan.buf.set_(b),
+                   lambda b: setattr(plan, "buf", b)):
+        new = plan.buf + 1
+        change(new)
+        assert plan.offsets.data_ptr() - plan.buf.data_ptr() == plan._layout.offsets
+        assert torch.equal(plan.slots.view(torch.uint8).unique(), new.unique())
