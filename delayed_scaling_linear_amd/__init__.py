@@ -1196,6 +1196,10 @@ class AdamWTensor:
     weight_decay: float = 0.0
     _seen: Optional[tuple] = field(default=None, init=False, repr=False, compare=False)
 
+    # A copy or an unpickled tensor makes its own descriptor.
+    def __getstate__(self):
+        return {**self.__dict__, "_seen": None}
+
     @staticmethod
     def zeros(param: torch.Tensor, grad: torch.Tensor, bits: int = 32, copy=None,
               weight_decay: float = 0.0) -> "AdamWTensor":
@@ -1276,8 +1280,12 @@ class AdamW:
         self.lr = lr if isinstance(lr, torch.Tensor) else \
             torch.full((1,), lr, dtype=torch.float32, device=device)
         self.betas, self.eps, self.seed = betas, eps, seed
-        self._array, self._descs = (_AdamWTensorDesc * 0)(), []
+        self._array, self._descs = None, []
         self.state = torch.zeros(ADAMW_STATE_BYTES // 8, dtype=torch.int64, device=self.lr.device)
+
+    # A copy or an unpickled optimizer makes its own array of descriptors.
+    def __getstate__(self):
+        return {**self.__dict__, "_array": None, "_descs": []}
 
     @property
     def steps(self) -> torch.Tensor:
@@ -1312,7 +1320,7 @@ class AdamW:
         """The tensors' descriptors as the C call takes them; those that have not changed
         stay in place."""
         descs = [t.desc() for t in self.tensors]
-        if len(descs) != len(self._descs):
+        if self._array is None or len(descs) != len(self._descs):
             self._array, self._descs = (_AdamWTensorDesc * len(descs))(), [None] * len(descs)
         for i, d in enumerate(descs):
             if d is not self._descs[i]:

@@ -1,7 +1,9 @@
 """The optimizer on the CPU: the reference against torch's AdamW in float64, the
 stochastic rounding's mean over all its numbers, and every refusal (nothing
 reaches a device)."""
+import copy
 import ctypes
+import pickle
 
 import numpy as np
 import pytest
@@ -151,3 +153,36 @@ def test_assigned_steps_are_the_state():
     assert opt.steps.tolist() == [9] and opt.steps.dtype == torch.int64
     opt.steps.fill_(4)
     assert int(opt.state[0]) == 4
+
+
+def test_an_optimizer_is_copied_and_pickled(monkeypatch):
+    """As a checkpoint does: a copy holds the state in tensors of its own, which are the
+    same ones wherever the program has them, and descriptors of these."""
+    monkeypatch.setattr(dsl, "_ptr", lambda t, dtype=None, what="": None if t is None else t.data_ptr())
+    monkeypatch.setattr(dsl, "_on_current_device", lambda *tensors: None)
+    monkeypatch.setattr(dsl, "_device", lambda: -1)
+    param, grad = torch.randn(300), torch.randn(300)
+    opt = dsl.AdamW([dsl.AdamWTensor.zeros(param, grad, 8, weight_decay=0.5)], lr=0.25,
+                    betas=(0.5, 0.75), eps=1e-3, seed=9, device="cpu")
+    opt.steps = 41
+    opt.tensors[0].m[0] = 7
+    array, count = opt._tensor_array()                  # as after a step
+    assert count == 1 and array[0].param == param.data_ptr()
+    deep = copy.deepcopy({"opt": opt, "param": param})
+    for other in (deep["opt"], pickle.loads(pickle.dumps(opt))):
+        assert (int(other.steps), float(other.lr), other.betas, other.eps, other.seed) \
+            == (41, 0.25, (0.5, 0.75), 1e-3, 9)
+        mine, its = opt.tensors[0], other.tensors[0]
+        array, count = other._tensor_array()
+        assert count == 1 and array[0].n == 300 and array[0].weight_decay == 0.5
+        for name in ("param", "grad", "m", "v", "m_scale", "v_scale"):
+            a, b = getattr(mine, name), getattr(its, name)
+            assert torch.equal(a, b) and a.data_ptr() != b.data_ptr()
+            assert getattr(array[0], name) == b.data_ptr()
+        other.steps += 1
+        assert int(other.state[0]) == 42 and int(opt.state[0]) == 41
+    assert deep["opt"].tensors[0].param is deep["param"]
+    assert copy.copy(opt.tensors[0]).param is param
+    assert opt._tensor_array()[0][0].param == param.data_ptr()
+    empty = copy.deepcopy(dsl.AdamW([], device="cpu"))
+    assert empty._tensor_array()[1] == 0 and len(empty._tensor_array()[0]) == 0
