@@ -651,6 +651,10 @@ class Dropout:
     rng: torch.Tensor
     _desc: Optional[_DropoutDesc] = field(default=None, init=False, repr=False, compare=False)
 
+    # A copy or an unpickled handle makes its own descriptor.
+    def __getstate__(self):
+        return {**self.__dict__, "_desc": None}
+
     def desc(self) -> _DropoutDesc:
         """The C descriptor, built at the first call and again if the tensor
         has been moved, reshaped or given another type in place since."""
@@ -794,6 +798,10 @@ class Adapters:
     b: torch.Tensor
     alpha: torch.Tensor
     _desc: Optional[_AdaptersDesc] = field(default=None, init=False, repr=False, compare=False)
+
+    # A copy or an unpickled handle makes its own descriptor.
+    def __getstate__(self):
+        return {**self.__dict__, "_desc": None}
 
     def desc(self) -> _AdaptersDesc:
         """The C descriptor, built at the first call and again if a tensor has
