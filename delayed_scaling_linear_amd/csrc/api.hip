@@ -654,10 +654,11 @@ int fp8_expert_gather_cast_transpose_amax(const fp8_expert_sizes_t *sizes, const
                                           const int32_t *noop_flag, fp8_stream_t stream) {
     if (int e = check_expert(sizes, plan, plan_bytes, cols)) return e;
     const ExpertShape shape(*sizes);
-    // x has other rows than out: its pointer counts where it has any.
+    // x has other rows than out: its pointer counts where it has any, and its stride is
+    // not held to the 32-bit offsets of a plain cast's tile (rows have 64-bit addresses).
     const bool reads = shape.tokens > 0;
     if (int e = check_cast(reads ? static_cast<const void *>(x) : plan, FP8_DTYPE_BF16, shape.rows,
-                           cols, ldx, scale, out))
+                           cols, cols, scale, out))
         return e;
     if (bad_stride(ldx, cols)) return FP8_ERR_SHAPE;
     const int64_t tiles_c = (cols + 127) / 128;

@@ -256,3 +256,14 @@ def test_views_follow_the_buffer():
         change(new)
         assert plan.offsets.data_ptr() - plan.buf.data_ptr() == plan._layout.offsets
         assert torch.equal(plan.slots.view(torch.uint8).unique(), new.unique())
+
+
+def test_gather_cast_takes_the_gathers_strides():
+    """Every stride that fp8_expert_gather takes.  (The weights' misalignment, looked at
+    last, ends the call before anything reaches a device.)"""
+    L = dsl.lib()
+    out = ctypes.byref(dsl._Desc(0x60000, 0x70000, 0x80000, 0, 0, ROWS, 64))
+    for ldx, want in ((64, -3), ((1 << 23) - 8, -3), (1 << 23, -3), (1 << 24, -3),
+                      ((1 << 30) - 8, -3), (1 << 30, -2), (56, -2), (68, -2)):
+        assert L.fp8_expert_gather_cast_transpose_amax(
+            _sizes(), PLAN, NEED, X, ldx, 64, W + 2, 0x90000, out, None, None, None) == want, ldx

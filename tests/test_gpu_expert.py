@@ -448,3 +448,30 @@ def test_past_32_bits_of_elements():
     for part, a in zip(plan.segments(q, offsets), offsets):
         mine = want[a:a + part.rows]
         assert (part.data == mine[:, None]).all() and (part.data_t == mine).all()
+
+
+def test_rows_far_apart():
+    """A row stride past 2^23 elements, in every call that takes one: 4 rows of 2^24."""
+    ids = _ids(4, 2, 3, 30, "all")
+    plan, want = _plan(ids, 3), ref.plan(ids, 3)
+    end = int(want[0][-1])
+    wide = torch.empty(4, 1 << 24, dtype=BF16, device=DEV)
+    x, x0 = wide[:, :64], _rand((4, 64), 31)
+    x.copy_(x0)
+    q, amax = dsl.Float8Tensor.empty(plan.rows, 64, dsl.E4M3), torch.zeros(1, device=DEV)
+    dsl.fp8_expert_gather_cast_transpose_amax(plan, x, torch.ones(1, device=DEV), q, amax)
+    y = ref.gather(bits16(x0), want[3], 2, end)
+    codes, _, top, _ = oracle.cast_transpose_amax(y, 1.0, dsl.E4M3)
+    np.testing.assert_array_equal(bits8(q.data[:end]), codes)
+    assert float(amax) == float(top)
+    rows = torch.zeros(plan.rows, 64, dtype=BF16, device=DEV)
+    dsl.fp8_expert_gather(plan, x, rows)
+    np.testing.assert_array_equal(bits16(rows[:end]), y)
+    back = torch.empty(4, 64, dtype=BF16, device=DEV)
+    dsl.fp8_expert_combine(plan, rows, back, base=x)
+    assert torch.equal(back.cpu(), (3 * x0.float()).to(BF16))
+    dw, dx = torch.zeros(4, 2, device=DEV), torch.zeros_like(rows)
+    dsl.fp8_expert_combine_backward(plan, x, rows, dw, weights=torch.ones(4, 2, device=DEV), dx=dx)
+    np.testing.assert_array_equal(bits16(dx[:end]), y)
+    dot = (x0.double() ** 2).sum(1, keepdim=True)
+    assert ((dw.cpu().double() - dot).abs() <= 65 * 2.0 ** -24 * dot).all()
