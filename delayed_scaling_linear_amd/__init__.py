@@ -26,6 +26,7 @@ the entry points that take them.
 """
 from __future__ import annotations
 
+import bisect
 import ctypes
 import os
 from dataclasses import dataclass, field
@@ -1193,7 +1194,8 @@ class AdamWTensor:
     """One tensor of an AdamW step: param (fp32 or bf16), its gradient (either
     type), and the moments m and v: fp32, or E4M3 codes (uint8) with a
     power-of-two scale (fp32) per ADAMW_BLOCK values.  `copy` (bf16) is written
-    with an fp32 param's new values.  All contiguous, of one shape."""
+    with an fp32 param's new values.  All contiguous, of one shape.  What a step
+    writes lies apart: a parameter that a model uses twice is one tensor."""
     param: torch.Tensor
     grad: torch.Tensor
     m: torch.Tensor
@@ -1239,8 +1241,16 @@ class AdamWTensor:
             else:
                 return seen[3]
         d = self._checked()
-        self._seen = (self.weight_decay, _device(), tuple(
-            None if t is None else (t.data_ptr(), t.shape, t.dtype) for t in fields), d)
+        now = tuple(None if t is None else (t.data_ptr(), t.shape, t.dtype) for t in fields)
+        # The bytes that a step writes, and the gradient's.
+        if seen is not None and now[2:] == seen[2][2:] and now[0] == seen[2][0]:
+            written = seen[4]
+        else:
+            written = tuple((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size())
+                            for t in fields[:1] + fields[2:] if t is not None and d.n > 0)
+        first = now[1][0]
+        grad = (first, first + d.n * (2 if now[1][2] is torch.bfloat16 else 4))
+        self._seen = (self.weight_decay, _device(), now, d, written, grad)
         return d
 
     def _checked(self) -> _AdamWTensorDesc:
@@ -1289,6 +1299,7 @@ class AdamW:
             torch.full((1,), lr, dtype=torch.float32, device=device)
         self.betas, self.eps, self.seed = betas, eps, seed
         self._array, self._descs = None, []
+        self._written, self._spans = [], []
         self.state = torch.zeros(ADAMW_STATE_BYTES // 8, dtype=torch.int64, device=self.lr.device)
 
     # A copy or an unpickled optimizer makes its own array of descriptors.
@@ -1330,11 +1341,28 @@ class AdamW:
         descs = [t.desc() for t in self.tensors]
         if self._array is None or len(descs) != len(self._descs):
             self._array, self._descs = (_AdamWTensorDesc * len(descs))(), [None] * len(descs)
-        for i, d in enumerate(descs):
-            if d is not self._descs[i]:
-                self._array[i] = d
-                self._descs[i] = d
+        changed = [i for i, d in enumerate(descs) if d is not self._descs[i]]
+        if changed:
+            self._need_separate(changed)
+            for i in changed:
+                self._array[i] = self._descs[i] = descs[i]
         return self._array, len(descs)
+
+    def _need_separate(self, changed) -> None:
+        """Refuses tensors whose steps would race: two that write the same memory, or a
+        gradient in what is written (unless value for value by its own tensor's step).
+        Gradients, which move between steps, are looked up in the sorted rest."""
+        written = [t._seen[4] for t in self.tensors]
+        if written != self._written:
+            spans = sorted(s for w in written for s in w)
+            if any(first < end for (_, end), (first, _) in zip(spans, spans[1:])):
+                raise ValueError("tensors must not share what a step writes")
+            self._written, self._spans, changed = written, spans, range(len(written))
+        for i in changed:
+            first, end = grad = self.tensors[i]._seen[5]
+            at = bisect.bisect_left(self._spans, (end,)) - 1     # the last that begins before end
+            if first < end and at >= 0 and self._spans[at][1] > first and grad not in written[i]:
+                raise ValueError("grad must not overlap what a step writes")
 
     def step(self, grad_scale: Optional[torch.Tensor] = None,
              noop_flag: Optional[torch.Tensor] = None, stream=None) -> None:

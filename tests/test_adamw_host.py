@@ -186,3 +186,45 @@ def test_an_optimizer_is_copied_and_pickled(monkeypatch):
     assert opt._tensor_array()[0][0].param == param.data_ptr()
     empty = copy.deepcopy(dsl.AdamW([], device="cpu"))
     assert empty._tensor_array()[1] == 0 and len(empty._tensor_array()[0]) == 0
+
+
+def test_tensors_share_nothing_that_is_written(monkeypatch):
+    """A parameter listed twice (tied weights), moments in each other's place and a
+    gradient within a parameter race on the device and are refused; pieces of one
+    buffer, a shared gradient and a gradient that its own copy replaces are not."""
+    monkeypatch.setattr(dsl, "_ptr", lambda t, dtype=None, what="": None if t is None else t.data_ptr())
+    monkeypatch.setattr(dsl, "_on_current_device", lambda *tensors: None)
+    monkeypatch.setattr(dsl, "_device", lambda: -1)
+    flat, grads = torch.zeros(4 * 512), torch.zeros(4 * 512)
+    make = lambda i, **kw: dsl.AdamWTensor.zeros(flat[512 * i:][:512], grads[512 * i:][:512], **kw)
+    opt = dsl.AdamW([make(0), make(1, bits=8), make(2), make(3, bits=8)], device="cpu")
+    assert opt._tensor_array()[1] == 4
+    opt.tensors[2].grad = opt.tensors[0].grad           # read only
+    b16 = torch.zeros(512, dtype=torch.bfloat16)
+    opt.tensors[3].grad = opt.tensors[3].copy = b16     # read before it is written
+    assert opt._tensor_array()[1] == 4
+
+    def refused(what):
+        for _ in range(2):                              # the second call looks again
+            with pytest.raises(ValueError, match=what):
+                opt._tensor_array()
+
+    a, b, c, d = opt.tensors
+    opt.tensors = [a, b, c, d, a]
+    refused("share")
+    for t, name, bad, what in (
+            (c, "param", a.param, "share"), (c, "v", c.m, "share"), (c, "m", a.m, "share"),
+            (b, "v_scale", d.m_scale, "share"), (c, "param", flat[768:][:512], "share"),
+            (a, "copy", b16, "share"), (c, "grad", b.param, "grad"),
+            (c, "grad", flat[4:][:512], "grad"), (b, "grad", b16, "grad"),
+            (d, "copy", torch.zeros(516, dtype=torch.bfloat16)[4:], None)):
+        opt.tensors, old = [a, b, c, d], getattr(t, name)
+        assert opt._tensor_array()[1] == 4
+        setattr(t, name, bad)
+        refused(what) if what else opt._tensor_array()
+        setattr(t, name, old)
+    half = torch.zeros(1024, dtype=torch.bfloat16)
+    d.grad, d.copy = half[:512], half[8:][:512]
+    refused("grad")
+    opt.tensors = [dsl.AdamWTensor.zeros(flat[:0], flat[:0])] * 2
+    assert opt._tensor_array()[1] == 2                  # nothing is written
