@@ -1295,7 +1295,7 @@ class AdamW:
     def __init__(self, tensors, lr=1e-3, betas=(0.9, 0.999), eps: float = 1e-8, seed: int = 0,
                  device="cuda"):
         self.tensors = list(tensors)
-        self.lr = lr if isinstance(lr, torch.Tensor) else \
+        self._lr = lr if isinstance(lr, torch.Tensor) else \
             torch.full((1,), lr, dtype=torch.float32, device=device)
         self.betas, self.eps, self.seed = betas, eps, seed
         self._array, self._descs = None, []
@@ -1305,6 +1305,19 @@ class AdamW:
     # A copy or an unpickled optimizer makes its own array of descriptors.
     def __getstate__(self):
         return {**self.__dict__, "_array": None, "_descs": []}
+
+    @property
+    def lr(self) -> torch.Tensor:
+        """[1] fp32, on the device.  Assigning a number writes it there, for captured
+        steps too; assigning a tensor puts that in its place."""
+        return self._lr
+
+    @lr.setter
+    def lr(self, lr) -> None:
+        if isinstance(lr, torch.Tensor):
+            self._lr = lr
+        else:
+            self._lr.fill_(lr)
 
     @property
     def steps(self) -> torch.Tensor:

@@ -228,3 +228,18 @@ def test_tensors_share_nothing_that_is_written(monkeypatch):
     refused("grad")
     opt.tensors = [dsl.AdamWTensor.zeros(flat[:0], flat[:0])] * 2
     assert opt._tensor_array()[1] == 2                  # nothing is written
+
+
+def test_assigned_learning_rate():
+    """A number goes where captured steps read it, a tensor takes its place."""
+    opt = dsl.AdamW([], lr=0.5, device="cpu")
+    lr = opt.lr
+    opt.lr = 0.25
+    assert opt.lr is lr and lr.tolist() == [0.25] and lr.dtype == torch.float32
+    opt.lr *= 0.5
+    assert opt.lr is lr and lr.tolist() == [0.125]
+    schedule = torch.tensor([2.0])
+    opt.lr = schedule
+    assert opt.lr is schedule
+    opt.lr = 3
+    assert schedule.tolist() == [3.0] and lr.tolist() == [0.125]
