@@ -816,6 +816,14 @@ int fp8_adapter_backward(const fp8_adapters_t *w, const void *plan, int64_t plan
  * hold no pair are rows of zeros.  Rows behind the last segment are left as
  * they were.
  *
+ * Rows that are in expert order already, the activations between an expert's
+ * linears and their gradients, go through the same cast, all experts' in one
+ * call: by a second plan, of `rows` tokens with top_k 1 and the same experts and
+ * capacity, whose expert_ids[r] is the expert of sources[r]'s pair, or -1 where
+ * sources[r] is.  Its offsets, counts and slots are the first one's, so rows stay
+ * where they are, and those without a pair are zeros whatever x holds there.
+ * (Without a capacity its own `rows`, those of its output, are more.)
+ *
  * Sizes: 0 <= tokens, 1 <= top_k <= FP8DSL_EXPERT_TOP_K_MAX, tokens * top_k <=
  * 2^23, 1 <= experts <= FP8DSL_EXPERTS_MAX, and at most 2^24 rows.
  *
