@@ -19,6 +19,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "bf16.h"
 #include "dropout.h"
 #include "fp8dsl_internal.h"
 
@@ -30,11 +31,6 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int THREADS = 256;
 constexpr int WAVES = THREADS / 64;
-
-__device__ __forceinline__ uint32_t bf16_bits(float f) {
-    const uint32_t u = __float_as_uint(f);
-    return (f != f) ? 0x7FC0u : (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
-}
 
 template <typename V>
 __device__ __forceinline__ V load_once(const void *p) {

@@ -42,6 +42,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "bf16.h"
 #include "dropout.h"
 #include "expert.h"
 #include "fp8_codec.h"
@@ -56,9 +57,6 @@ constexpr int THREADS = 256;
 typedef unsigned short ushort2_t __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
-
-__device__ __forceinline__ float bf16_lo(uint32_t d) { return __uint_as_float(d << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t d) { return __uint_as_float(d & 0xFFFF0000u); }
 
 // A lane's sixteen source elements of one tile row, as loaded: kChunks
 // 16-byte chunks, chunk k at tile column (128 / kChunks) * k + (16 / kChunks)
@@ -760,11 +758,6 @@ hipError_t launch_cast_group(const CastGroupArgs &args, int src, int fmt, bool w
 //        cannot put infinities or NaNs into a model's activations.
 // One workgroup per 128 x 128 tile, the lane layout of the cast (4 rows x 16
 // columns, 16-byte loads and stores).
-__device__ __forceinline__ uint32_t f32_to_bf16_bits_rne(float f) {
-    const uint32_t u = __float_as_uint(f);
-    return (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;   // finite or inf input
-}
-
 template <int OP>
 __device__ __forceinline__ uint32_t produce_pair(uint32_t xw, uint32_t aw, uint32_t bw) {
     uint32_t out = 0;
@@ -776,19 +769,19 @@ __device__ __forceinline__ uint32_t produce_pair(uint32_t xw, uint32_t aw, uint3
         if constexpr (OP == FP8_PRODUCE_MODULATE || OP == FP8_PRODUCE_MODULATE_FINITE) {
             const float bv = __uint_as_float(h ? (bw & 0xFFFF0000u) : (bw << 16));
             const float v = (av * xv) / bv;
-            y = (v != v) ? 0x7FC0u : f32_to_bf16_bits_rne(v);
+            y = bf16_bits(v);
             if constexpr (OP == FP8_PRODUCE_MODULATE_FINITE)
                 y = ((y & 0x7F80u) == 0x7F80u) ? 0u : y;
         } else if constexpr (OP == FP8_PRODUCE_ADD) {
             const float v = xv + av;
-            y = (v != v) ? 0x7FC0u : f32_to_bf16_bits_rne(v);
+            y = bf16_bits(v);
         } else {
             // Two terms, added one at a time with a bf16 rounding after each.
             const float bv = __uint_as_float(h ? (bw & 0xFFFF0000u) : (bw << 16));
             const float v1 = xv + av;
-            const uint32_t t = (v1 != v1) ? 0x7FC0u : f32_to_bf16_bits_rne(v1);
+            const uint32_t t = bf16_bits(v1);
             const float v = __uint_as_float(t << 16) + bv;
-            y = (v != v) ? 0x7FC0u : f32_to_bf16_bits_rne(v);
+            y = bf16_bits(v);
         }
         out |= y << (16 * h);
     }
@@ -968,8 +961,8 @@ __global__ __launch_bounds__(THREADS) void dropout_cast_kernel(
                     v0 = bf16_lo(rw) + v0;
                     v1 = bf16_hi(rw) + v1;
                 }
-                const uint32_t y0 = (v0 != v0) ? 0x7FC0u : f32_to_bf16_bits_rne(v0);
-                const uint32_t y1 = (v1 != v1) ? 0x7FC0u : f32_to_bf16_bits_rne(v1);
+                const uint32_t y0 = bf16_bits(v0);
+                const uint32_t y1 = bf16_bits(v1);
                 ys[i].v[h][k] = y0 | (y1 << 16);
             }
             if (y != nullptr && in) *reinterpret_cast<u32x4 *>(y + (r + i) * ldy + ch) = ys[i].v[h];
@@ -1087,8 +1080,8 @@ __global__ __launch_bounds__(THREADS) void expert_gather_cast_kernel(
                 for (int k = 0; k < 4; ++k) {
                     const uint32_t xw = ys[i].v[h][k];
                     const float v0 = wh * bf16_lo(xw), v1 = wh * bf16_hi(xw);
-                    const uint32_t y0 = (v0 != v0) ? 0x7FC0u : f32_to_bf16_bits_rne(v0);
-                    const uint32_t y1 = (v1 != v1) ? 0x7FC0u : f32_to_bf16_bits_rne(v1);
+                    const uint32_t y0 = bf16_bits(v0);
+                    const uint32_t y1 = bf16_bits(v1);
                     ys[i].v[h][k] = y0 | (y1 << 16);     // +0 without a pair: 0 * 0
                 }
             }
@@ -1142,7 +1135,6 @@ template <bool FINITE>
 __device__ __forceinline__ void modulate_grad_pair(uint32_t gw, uint32_t xw, uint32_t aw,
                                                    uint32_t bw, uint32_t &ox, uint32_t &oa,
                                                    uint32_t &ob) {
-    auto rne = [](float f) -> uint32_t { return (f != f) ? 0x7FC0u : f32_to_bf16_bits_rne(f); };
     ox = oa = ob = 0;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -1150,9 +1142,9 @@ __device__ __forceinline__ void modulate_grad_pair(uint32_t gw, uint32_t xw, uin
         const float gv = wide(gw), xv = wide(xw), av = wide(aw), bv = wide(bw);
         const float u = (av * xv) / bv;
         const float t = gv / bv;
-        uint32_t rx = rne(t * av), ra = rne(t * xv), rb = rne(-(t * u));
+        uint32_t rx = bf16_bits(t * av), ra = bf16_bits(t * xv), rb = bf16_bits(-(t * u));
         if constexpr (FINITE) {
-            if ((rne(u) & 0x7F80u) == 0x7F80u) rx = ra = rb = 0u;
+            if ((bf16_bits(u) & 0x7F80u) == 0x7F80u) rx = ra = rb = 0u;
         }
         ox |= rx << (16 * h);
         oa |= ra << (16 * h);

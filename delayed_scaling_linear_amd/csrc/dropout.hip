@@ -17,6 +17,7 @@
 // 5.1 to 5.4; with non-temporal loads 14.6); fp32 [1037, 1160] with a residual
 // 4.7 us on the GPU, 7.1 a call.
 #include "dropout.h"
+#include "bf16.h"
 #include "fp8dsl_internal.h"
 
 namespace fp8dsl {
@@ -26,11 +27,6 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int THREADS = 256;
 constexpr int ROWS_PER_LANE = 4;
-
-__device__ __forceinline__ uint32_t bf16_bits(float f) {
-    const uint32_t u = __float_as_uint(f);
-    return (f != f) ? 0x7FC0u : (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
-}
 
 // res + (keep ? f * x : 0), the product and the sum each rounded.
 __device__ __forceinline__ float drop_add(float x, bool keep, float f, float res, bool add) {

@@ -19,6 +19,7 @@
 // tokens with 8 of 64 experts 5.5 (one launch), of 65536 with 4 of 128 10.9 (two).
 #include "expert.h"
 
+#include "bf16.h"
 #include "fp8dsl_internal.h"
 
 namespace fp8dsl {
@@ -266,14 +267,6 @@ __global__ __launch_bounds__(PLAN_THREADS) void expert_place_kernel(
 // ---- rows --------------------------------------------------------------------
 
 constexpr int THREADS = 256;
-
-__device__ __forceinline__ float bf16_lo(uint32_t d) { return __uint_as_float(d << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t d) { return __uint_as_float(d & 0xFFFF0000u); }
-
-__device__ __forceinline__ uint32_t bf16_bits(float f) {
-    const uint32_t u = __float_as_uint(f);
-    return (f != f) ? 0x7FC0u : (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
-}
 
 // Row `row` (not negative) of a bf16 matrix with its stride in bytes.
 __device__ __forceinline__ const char *row_at(const void *p, int row, uint32_t ld_bytes) {
