@@ -1102,13 +1102,19 @@ hipError_t launch_expert_gather_cast_fmt(const ExpertShape &shape, const int32_t
                                          const int32_t *noop, hipStream_t stream) {
     const int64_t tiles_c = (cols + TILE - 1) / TILE;
     const dim3 grid((unsigned)(shape.tiles_max * tiles_c));
-    // Six workgroups of 17 KB of LDS fit a CU by their registers.  Where they are more
-    // than about a round, five do better, which 12 KB more of LDS each makes them: us
-    // with six / five, 16384 x 1024, two choices, E4M3 27.2 / 25.5, 2048 x 8192 28.1 / 25.8; a
-    // round and less 4096 x 2048 12.1 / 12.1, 5003 x 1168 (1560 tiles) 17.7 / 18.9.
-    int cus = 0;
-    if (hipError_t e = current_cu_count(&cus)) return e;
-    const unsigned lds = shape.tiles_max * tiles_c > 7 * (int64_t)cus ? 12 * 1024 : 0;
+    // By registers a CU holds seven workgroups, six with weights; codes alone run so.  A
+    // tile with a transpose keeps 17 KB of LDS, and 12 KB more leave five: better in a grid
+    // of more than seven a CU, with weights more than eight.  us with 7 / 6 / 5 to E4M3 and
+    // 6 / 5 with weights to E5M2, two choices: 1664 tiles (6144 x 2048) 16.1 / 16.2 / 17.0
+    // and 19.7 / 20.8, 1920 (7168 x 2048) 21.1 to 22.5 / 20.2 / 20.9 and 23.2 / 24.8, 2176
+    // (8192 x 2048) 28.3 / 27.5 / 26.4 and 29.7 / 29.3, 2560 (2048 x 8192) 30.0 / 28.9 / 27.9
+    // and 30.7 / 29.9.
+    unsigned lds = 0;
+    if (qt) {
+        int cus = 0;
+        if (hipError_t e = current_cu_count(&cus)) return e;
+        if (shape.tiles_max * tiles_c > (WEIGHTS ? 8 : 7) * (int64_t)cus) lds = 12 * 1024;
+    }
     auto launch = [&](auto wq, auto wqt) {
         hipLaunchKernelGGL((expert_gather_cast_kernel<FMT, decltype(wq)::value,
                                                       decltype(wqt)::value, WEIGHTS>),
