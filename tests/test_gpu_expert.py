@@ -475,3 +475,17 @@ def test_rows_far_apart():
     np.testing.assert_array_equal(bits16(dx[:end]), y)
     dot = (x0.double() ** 2).sum(1, keepdim=True)
     assert ((dw.cpu().double() - dot).abs() <= 65 * 2.0 ** -24 * dot).all()
+
+
+@pytest.mark.parametrize("tokens, top_k, experts, cols", [
+    (17, 3, 4, 528), (130, 6, 3, 1024), (257, 2, 9, 1032), (33, 9, 5, 4104)])
+def test_weight_gradient_with_and_without_dx(tokens, top_k, experts, cols):
+    """The same bits: the sums' order follows from the sizes alone."""
+    ids = _ids(tokens, top_k, experts, 40)
+    plan = _plan(ids, experts)
+    dy, x = _rand((tokens, cols), 41).to(DEV), _rand((plan.rows, cols), 42).to(DEV)
+    a, b = (torch.empty(tokens, top_k, device=DEV) for _ in range(2))
+    dsl.fp8_expert_combine_backward(plan, dy, x, a)
+    dsl.fp8_expert_combine_backward(plan, dy, x, b, weights=torch.rand(tokens, top_k, device=DEV),
+                                    dx=torch.empty_like(x))
+    assert torch.equal(a, b)
