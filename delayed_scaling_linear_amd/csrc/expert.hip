@@ -224,7 +224,9 @@ __global__ __launch_bounds__(PLAN_THREADS) void expert_place_kernel(
         tiles[t] = int4{(t - tile0[lo]) * kExpertTile, first[lo + 1] - first[lo], first[lo], 0};
     }
     // Slots without a pair: the ends of the segments (16 lanes each) and what lies
-    // behind the last one.
+    // behind the last one.  Without a capacity an end is under 16 rows.  With one it is up
+    // to all of them, and few long ends are slow: 8192 tokens with 2 of 8 experts 8.7 us
+    // without, 13.0 at a capacity of 2560, 27.9 at 10240.
     for (int i = blockIdx.x * PLAN_THREADS + tid; i < 16 * experts; i += gridDim.x * PLAN_THREADS) {
         const int e = i / 16, kept = capacity ? min(all[e], capacity) : all[e];
         for (int r = first[e] + kept + (i & 15); r < first[e + 1]; r += 16) sources[r] = -1;
@@ -494,10 +496,17 @@ hipError_t launch_expert_combine_backward(const ExpertShape &s, const int32_t *p
                                           uint16_t *dx, int64_t lddx, int64_t cols,
                                           hipStream_t stream) {
     const int64_t groups = cols / 8;
-    // A wave per token, or a workgroup where its row is longer than 1024 columns.  us
-    // with a wave / a workgroup, of two choices without dx: 16384 tokens of 512 columns
-    // 11.2 / 22.4, of 1024 18.5 / 27.6; 4096 of 2048 10.5 / 11.2 (with dx 15.6 / 15.6, 8192
-    // with dx 38.5 / 34.4); 1024 of 8192 12.4 / 10.9, 64 of 8192 with dx 12.6 / 8.9.
+    // A wave per token, or a workgroup where its row is longer than 1024 columns, with and
+    // without dx: the weights' gradient has the same bits in both.  us with a wave / a
+    // workgroup, two choices, with dx and without:
+    //   1024 columns  16384 tokens 34.5 / 41.9, 19.4 / 28.3    1037 tokens 5.0 / 5.1, 3.7 / 4.2
+    //   1160          14463        39.5 / 40.8, 19.7 / 26.6                6.1 / 5.7, 4.4 / 4.4
+    //   1536          10922        36.6 / 35.9, 19.1 / 23.1                6.5 / 6.0, 4.6 / 4.6
+    //   2048           8192        38.3 / 34.5, 19.5 / 21.5                7.7 / 7.1, 5.6 / 5.7
+    //   4096           4096        39.2 / 35.0, 19.2 / 18.8               11.4 / 10.1, 8.0 / 8.0
+    //   8192           2048        40.3 / 38.3, 20.9 / 19.6               23.1 / 17.5, 12.6 / 11.8
+    // six choices, 1037 tokens: 1160 columns 12.6 / 10.6, 8.6 / 8.0; 2048 15.0 / 12.5, 10.0 /
+    // 9.2.  So many tokens without dx pay for it up to 2048 columns.
     const int tx_log2 = groups > 128 ? 8 : 6, tokens = THREADS >> tx_log2;
     const int64_t token_blocks = (s.tokens + tokens - 1) / tokens;
     const dim3 grid((unsigned)(token_blocks + (dx ? zero_blocks(s) : 0)));
