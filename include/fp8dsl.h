@@ -1061,7 +1061,9 @@ typedef struct fp8_adamw {
  * their distance from the lower one and u is a 16-bit random number.  Rounded to
  * nearest instead, v would not fall (a step takes 1 - beta2 of it, the format's
  * half step is 2^-4) and a bf16 parameter would not take small updates.  A v
- * above 0 is never stored as 0.  What is not finite is stored as the code 0x7F, in m
+ * above 0 is never stored as 0 but as 2^-9 of its scale at least: one more than
+ * about 2^17 below its block's largest is held too large, and its parameter moves
+ * less than in fp32.  What is not finite is stored as the code 0x7F, in m
  * a NaN, in v an infinity: a v that overflows (a gradient above 5e20 or so) then
  * holds its own parameter still, as it does in fp32.  The update of p uses m and v
  * before they are stored.  copy is p rounded to nearest even.
