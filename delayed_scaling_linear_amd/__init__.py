@@ -1240,20 +1240,19 @@ class AdamWTensor:
                     break                    # (one address is one device's)
             else:
                 return seen[3]
-        d = self._checked()
-        now = tuple(None if t is None else (t.data_ptr(), t.shape, t.dtype) for t in fields)
+        d, at = self._checked()
+        now = tuple(None if t is None else (p, t.shape, t.dtype) for t, p in zip(fields, at))
         # The bytes that a step writes, and the gradient's.
-        if seen is not None and now[2:] == seen[2][2:] and now[0] == seen[2][0]:
-            written = seen[4]
-        else:
-            written = tuple((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size())
-                            for t in fields[:1] + fields[2:] if t is not None and d.n > 0)
-        first = now[1][0]
-        grad = (first, first + d.n * (2 if now[1][2] is torch.bfloat16 else 4))
+        n = d.n
+        state, scale = (4 * n, 0) if at[4] is None else (n, -(-n // ADAMW_BLOCK) * 4)
+        sizes = (n * fields[0].element_size(), state, state, scale, scale, 2 * n)
+        written = tuple([(p, p + size) for p, size in zip(at[:1] + at[2:], sizes) if p and size])
+        grad = (at[1], at[1] + n * fields[1].element_size())
         self._seen = (self.weight_decay, _device(), now, d, written, grad)
         return d
 
-    def _checked(self) -> _AdamWTensorDesc:
+    def _checked(self):
+        """The descriptor, and the fields' pointers in their order."""
         p, g, m, v, copy = self.param, self.grad, self.m, self.v, self.copy
         for t, what in ((p, "param"), (g, "grad"), (m, "m"), (v, "v")):
             if t is None:
@@ -1267,23 +1266,20 @@ class AdamWTensor:
             raise ValueError("m_scale and v_scale come together")
         if copy is not None and p.dtype is not torch.float32:
             raise TypeError("a copy needs an fp32 param")
+        at = []
         for t, dtype, what in ((p, None, "param"), (g, None, "grad"), (m, state, "m"),
                                (v, state, "v"), (copy, torch.bfloat16, "copy")):
-            if t is None and what == "copy":
-                continue
-            if t.shape != shape:
+            if t is not None and t.shape != shape:
                 raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-            _ptr(t, dtype, what)
+            at.append(_ptr(t, dtype, what))
         blocks = (n + ADAMW_BLOCK - 1) // ADAMW_BLOCK
         _need_shape(self.m_scale, (blocks,), "m_scale")
         _need_shape(self.v_scale, (blocks,), "v_scale")
         _on_current_device(p, g, m, v, copy, self.m_scale, self.v_scale)
-        return _AdamWTensorDesc(
-            p.data_ptr(), g.data_ptr(), m.data_ptr(), v.data_ptr(),
-            _ptr(self.m_scale, torch.float32, "m_scale"),
-            _ptr(self.v_scale, torch.float32, "v_scale"),
-            None if copy is None else copy.data_ptr(), n, self.weight_decay,
-            _ADAMW_DTYPES[p.dtype], _ADAMW_DTYPES[g.dtype], 0)
+        at[4:4] = (_ptr(self.m_scale, torch.float32, "m_scale"),
+                   _ptr(self.v_scale, torch.float32, "v_scale"))
+        return _AdamWTensorDesc(*at, n, self.weight_decay, _ADAMW_DTYPES[p.dtype],
+                                _ADAMW_DTYPES[g.dtype], 0), tuple(at)
 
 
 class AdamW:
@@ -1298,13 +1294,13 @@ class AdamW:
         self._lr = lr if isinstance(lr, torch.Tensor) else \
             torch.full((1,), lr, dtype=torch.float32, device=device)
         self.betas, self.eps, self.seed = betas, eps, seed
-        self._array, self._descs = None, []
+        self._array = self._descs = None
         self._written, self._spans = [], []
         self.state = torch.zeros(ADAMW_STATE_BYTES // 8, dtype=torch.int64, device=self.lr.device)
 
     # A copy or an unpickled optimizer makes its own array of descriptors.
     def __getstate__(self):
-        return {**self.__dict__, "_array": None, "_descs": []}
+        return {**self.__dict__, "_array": None, "_descs": None}
 
     @property
     def lr(self) -> torch.Tensor:
@@ -1341,7 +1337,7 @@ class AdamW:
         return [t.grad for t in self.tensors]
 
     def desc(self) -> _AdamWDesc:
-        lr, state = self.lr, self.state
+        lr, state = self._lr, self.state
         _need_scalar(lr, "lr")
         _need_shape(state, (ADAMW_STATE_BYTES // 8,), "state")
         _on_current_device(lr, state)
@@ -1352,30 +1348,32 @@ class AdamW:
         """The tensors' descriptors as the C call takes them; those that have not changed
         stay in place."""
         descs = [t.desc() for t in self.tensors]
-        if self._array is None or len(descs) != len(self._descs):
-            self._array, self._descs = (_AdamWTensorDesc * len(descs))(), [None] * len(descs)
-        changed = [i for i, d in enumerate(descs) if d is not self._descs[i]]
-        if changed:
+        if descs != self._descs:                         # (by identity)
+            same = self._descs if self._descs and len(descs) == len(self._descs) else ()
+            array = self._array if same else (_AdamWTensorDesc * len(descs))()
+            changed = [i for i, d in enumerate(descs) if not same or d is not same[i]]
             self._need_separate(changed)
             for i in changed:
-                self._array[i] = self._descs[i] = descs[i]
+                array[i] = descs[i]
+            self._array, self._descs = array, descs
         return self._array, len(descs)
 
     def _need_separate(self, changed) -> None:
         """Refuses tensors whose steps would race: two that write the same memory, or a
         gradient in what is written (unless value for value by its own tensor's step).
         Gradients, which move between steps, are looked up in the sorted rest."""
-        written = [t._seen[4] for t in self.tensors]
+        written, spans = [t._seen[4] for t in self.tensors], self._spans
         if written != self._written:
-            spans = sorted(s for w in written for s in w)
+            spans = sorted([s for w in written for s in w])
             if any(first < end for (_, end), (first, _) in zip(spans, spans[1:])):
                 raise ValueError("tensors must not share what a step writes")
-            self._written, self._spans, changed = written, spans, range(len(written))
+            changed = range(len(written))
         for i in changed:
             first, end = grad = self.tensors[i]._seen[5]
-            at = bisect.bisect_left(self._spans, (end,)) - 1     # the last that begins before end
-            if first < end and at >= 0 and self._spans[at][1] > first and grad not in written[i]:
+            at = bisect.bisect_left(spans, (end,)) - 1           # the last that begins before end
+            if first < end and at >= 0 and spans[at][1] > first and grad not in written[i]:
                 raise ValueError("grad must not overlap what a step writes")
+        self._written, self._spans = written, spans
 
     def step(self, grad_scale: Optional[torch.Tensor] = None,
              noop_flag: Optional[torch.Tensor] = None, stream=None) -> None:

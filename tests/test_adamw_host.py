@@ -217,6 +217,7 @@ def test_tensors_share_nothing_that_is_written(monkeypatch):
             (b, "v_scale", d.m_scale, "share"), (c, "param", flat[768:][:512], "share"),
             (a, "copy", b16, "share"), (c, "grad", b.param, "grad"),
             (c, "grad", flat[4:][:512], "grad"), (b, "grad", b16, "grad"),
+            (a, "param", grads[512:][:512], "grad"),    # another tensor's gradient
             (d, "copy", torch.zeros(516, dtype=torch.bfloat16)[4:], None)):
         opt.tensors, old = [a, b, c, d], getattr(t, name)
         assert opt._tensor_array()[1] == 4
