@@ -28,6 +28,7 @@ from __future__ import annotations
 
 import bisect
 import ctypes
+import operator
 import os
 from dataclasses import dataclass, field
 from typing import Optional
@@ -1228,9 +1229,10 @@ class AdamWTensor:
         """The C descriptor, built at the first call and again if a field is a tensor
         elsewhere since, or of another shape or type.  Keeps no tensor alive: a gradient
         may be dropped between steps."""
-        fields = (self.param, self.grad, self.m, self.v, self.m_scale, self.v_scale, self.copy)
-        seen = self._seen
-        if seen is not None and seen[0] == self.weight_decay and seen[1] == _device():
+        fields = (self.param, self.m, self.v, self.m_scale, self.v_scale, self.copy)
+        seen, g = self._seen, self.grad
+        if seen is not None and g is not None and seen[0] == self.weight_decay \
+                and seen[1] == _device():
             for t, old in zip(fields, seen[2]):
                 if t is None or old is None:
                     if t is not old:
@@ -1239,47 +1241,77 @@ class AdamWTensor:
                         or not t.is_contiguous():
                     break                    # (one address is one device's)
             else:
-                return seen[3]
-        d, at = self._checked()
-        now = tuple(None if t is None else (p, t.shape, t.dtype) for t, p in zip(fields, at))
-        # The bytes that a step writes, and the gradient's.
-        n = d.n
-        state, scale = (4 * n, 0) if at[4] is None else (n, -(-n // ADAMW_BLOCK) * 4)
-        sizes = (n * fields[0].element_size(), state, state, scale, scale, 2 * n)
-        written = tuple([(p, p + size) for p, size in zip(at[:1] + at[2:], sizes) if p and size])
-        grad = (at[1], at[1] + n * fields[1].element_size())
-        self._seen = (self.weight_decay, _device(), now, d, written, grad)
+                old = seen[3]
+                if g.data_ptr() == old[0] and g.shape == old[1] and g.dtype is old[2] \
+                        and g.is_contiguous():
+                    return seen[4]
+                # A new gradient beside an otherwise unchanged tensor, as most steps bring.
+                at = self._grad_at(fields[0].shape)
+                _on_current_device(g)
+                d = _AdamWTensorDesc.from_buffer_copy(seen[4])
+                d.grad, d.grad_dtype = at, _ADAMW_DTYPES[g.dtype]
+                self._keep(seen[2], at, d, seen[5])
+                return d
+        d, at = self._checked(fields)
+        # The bytes that a step writes.
+        n, written = d.n, ()
+        if n > 0:
+            p, m, v, m_scale, v_scale, copy = at
+            state = 4 * n if m_scale is None else n
+            written = (p, p + n * fields[0].element_size()), (m, m + state), (v, v + state)
+            if m_scale is not None:
+                scales = -(-n // ADAMW_BLOCK) * 4
+                written += (m_scale, m_scale + scales), (v_scale, v_scale + scales)
+            if copy is not None:
+                written += (copy, copy + 2 * n),
+        self._keep([None if t is None else (p, t.shape, t.dtype) for t, p in zip(fields, at)],
+                   d.grad, d, written)
         return d
 
-    def _checked(self):
-        """The descriptor, and the fields' pointers in their order."""
-        p, g, m, v, copy = self.param, self.grad, self.m, self.v, self.copy
-        for t, what in ((p, "param"), (g, "grad"), (m, "m"), (v, "v")):
+    def _keep(self, rest, at, d, written) -> None:
+        """What desc() compares with, its result, and what the step writes and reads."""
+        g, at = self.grad, at or 0
+        self._seen = (self.weight_decay, _device(), rest, (at, g.shape, g.dtype), d, written,
+                      (at, at + d.n * g.element_size()))
+
+    def _grad_at(self, shape) -> int:
+        """The gradient's pointer."""
+        g = self.grad
+        if g.dtype not in _ADAMW_DTYPES:
+            raise TypeError(f"grad must be fp32 or bf16, got {g.dtype}")
+        if g.shape != shape:
+            raise ValueError(f"grad must have shape {tuple(shape)}, got {tuple(g.shape)}")
+        return _ptr(g, None, "grad")
+
+    def _checked(self, fields):
+        """The descriptor, and the pointers of `fields`, those but the gradient."""
+        p, m, v, m_scale, v_scale, copy = fields
+        for t, what in ((p, "param"), (self.grad, "grad"), (m, "m"), (v, "v")):
             if t is None:
                 raise ValueError(f"{what} is required")
         n, shape = p.numel(), p.shape
-        for t, what in ((p, "param"), (g, "grad")):
+        for t, what in ((p, "param"), (self.grad, "grad")):
             if t.dtype not in _ADAMW_DTYPES:
                 raise TypeError(f"{what} must be fp32 or bf16, got {t.dtype}")
-        state = torch.float32 if self.m_scale is None else torch.uint8
-        if (self.m_scale is None) != (self.v_scale is None):
+        if (m_scale is None) != (v_scale is None):
             raise ValueError("m_scale and v_scale come together")
         if copy is not None and p.dtype is not torch.float32:
             raise TypeError("a copy needs an fp32 param")
+        state = torch.float32 if m_scale is None else torch.uint8
+        blocks = (-(-n // ADAMW_BLOCK),)
         at = []
-        for t, dtype, what in ((p, None, "param"), (g, None, "grad"), (m, state, "m"),
-                               (v, state, "v"), (copy, torch.bfloat16, "copy")):
-            if t is not None and t.shape != shape:
-                raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        for t, dtype, want, what in ((p, None, shape, "param"), (m, state, shape, "m"),
+                                     (v, state, shape, "v"),
+                                     (m_scale, torch.float32, blocks, "m_scale"),
+                                     (v_scale, torch.float32, blocks, "v_scale"),
+                                     (copy, torch.bfloat16, shape, "copy")):
+            if t is not None and t.shape != want:
+                raise ValueError(f"{what} must have shape {tuple(want)}, got {tuple(t.shape)}")
             at.append(_ptr(t, dtype, what))
-        blocks = (n + ADAMW_BLOCK - 1) // ADAMW_BLOCK
-        _need_shape(self.m_scale, (blocks,), "m_scale")
-        _need_shape(self.v_scale, (blocks,), "v_scale")
-        _on_current_device(p, g, m, v, copy, self.m_scale, self.v_scale)
-        at[4:4] = (_ptr(self.m_scale, torch.float32, "m_scale"),
-                   _ptr(self.v_scale, torch.float32, "v_scale"))
-        return _AdamWTensorDesc(*at, n, self.weight_decay, _ADAMW_DTYPES[p.dtype],
-                                _ADAMW_DTYPES[g.dtype], 0), tuple(at)
+        grad = self._grad_at(shape)
+        _on_current_device(self.grad, *fields)
+        return _AdamWTensorDesc(at[0], grad, *at[1:], n, self.weight_decay, _ADAMW_DTYPES[p.dtype],
+                                _ADAMW_DTYPES[self.grad.dtype], 0), at
 
 
 class AdamW:
@@ -1295,7 +1327,7 @@ class AdamW:
             torch.full((1,), lr, dtype=torch.float32, device=device)
         self.betas, self.eps, self.seed = betas, eps, seed
         self._array = self._descs = None
-        self._written, self._spans = [], []
+        self._written, self._spans = [], ((), ())
         self.state = torch.zeros(ADAMW_STATE_BYTES // 8, dtype=torch.int64, device=self.lr.device)
 
     # A copy or an unpickled optimizer makes its own array of descriptors.
@@ -1362,18 +1394,19 @@ class AdamW:
         """Refuses tensors whose steps would race: two that write the same memory, or a
         gradient in what is written (unless value for value by its own tensor's step).
         Gradients, which move between steps, are looked up in the sorted rest."""
-        written, spans = [t._seen[4] for t in self.tensors], self._spans
+        written, (starts, ends) = [t._seen[5] for t in self.tensors], self._spans
         if written != self._written:
             spans = sorted([s for w in written for s in w])
-            if any(first < end for (_, end), (first, _) in zip(spans, spans[1:])):
+            starts, ends = [s for s, _ in spans], [e for _, e in spans]
+            if any(map(operator.gt, ends, starts[1:])):
                 raise ValueError("tensors must not share what a step writes")
             changed = range(len(written))
         for i in changed:
-            first, end = grad = self.tensors[i]._seen[5]
-            at = bisect.bisect_left(spans, (end,)) - 1           # the last that begins before end
-            if first < end and at >= 0 and spans[at][1] > first and grad not in written[i]:
+            first, end = grad = self.tensors[i]._seen[6]
+            at = bisect.bisect_left(starts, end) - 1             # the last that begins before end
+            if first < end and at >= 0 and ends[at] > first and grad not in written[i]:
                 raise ValueError("grad must not overlap what a step writes")
-        self._written, self._spans = written, spans
+        self._written, self._spans = written, (starts, ends)
 
     def step(self, grad_scale: Optional[torch.Tensor] = None,
              noop_flag: Optional[torch.Tensor] = None, stream=None) -> None:
