@@ -244,3 +244,36 @@ def test_assigned_learning_rate():
     assert opt.lr is schedule
     opt.lr = 3
     assert schedule.tolist() == [3.0] and lr.tolist() == [0.125]
+
+
+def test_a_new_gradient_is_checked(monkeypatch):
+    """Between steps a gradient may be another tensor, of the other type too; one that
+    the step does not take is refused as at the first step, and the rest is not stale."""
+    monkeypatch.setattr(dsl.torch.Tensor, "is_cuda", property(lambda t: True))
+    monkeypatch.setattr(dsl, "_on_current_device", lambda *tensors: None)
+    monkeypatch.setattr(dsl, "_device", lambda: -1)
+    param = torch.zeros(4, 75)
+    t = dsl.AdamWTensor.zeros(param, torch.zeros(4, 75), 8, weight_decay=0.5)
+    first = t.desc()
+    assert t.desc() is first and first.grad_dtype == 1
+    for dtype, code in ((torch.bfloat16, 0), (torch.float32, 1)):
+        t.grad = torch.zeros(4, 75, dtype=dtype)
+        d = t.desc()
+        assert d is not first and t.desc() is d
+        assert (d.grad, d.grad_dtype) == (t.grad.data_ptr(), code)
+        for name, _ in d._fields_:
+            if name not in ("grad", "grad_dtype"):
+                assert getattr(d, name) == getattr(first, name), name
+    good = t.grad
+    for bad, error in ((None, ValueError), (torch.zeros(4, 76), ValueError),
+                       (torch.zeros(4, 75, dtype=torch.float64), TypeError),
+                       (torch.zeros(75, 4).t(), ValueError), (torch.zeros(75 * 4), ValueError)):
+        t.grad = bad
+        with pytest.raises(error, match="grad"):
+            t.desc()
+        t.grad = good
+        assert t.desc().grad == good.data_ptr()
+    t.grad, t.weight_decay = torch.zeros(4, 75), 0.25
+    assert (t.desc().grad, t.desc().weight_decay) == (t.grad.data_ptr(), 0.25)
+    t.grad, t.v = torch.zeros(4, 75), torch.zeros(4, 75, dtype=torch.uint8)
+    assert (t.desc().grad, t.desc().v) == (t.grad.data_ptr(), t.v.data_ptr())
