@@ -28,6 +28,7 @@ from __future__ import annotations
 
 import bisect
 import ctypes
+import itertools
 import operator
 import os
 from dataclasses import dataclass, field
@@ -1253,17 +1254,17 @@ class AdamWTensor:
                 self._keep(seen[2], at, d, seen[5])
                 return d
         d, at = self._checked(fields)
-        # The bytes that a step writes.
+        # Where what a step writes begins and ends, in turn.
         n, written = d.n, ()
         if n > 0:
             p, m, v, m_scale, v_scale, copy = at
             state = 4 * n if m_scale is None else n
-            written = (p, p + n * fields[0].element_size()), (m, m + state), (v, v + state)
+            written = (p, p + n * fields[0].element_size(), m, m + state, v, v + state)
             if m_scale is not None:
                 scales = -(-n // ADAMW_BLOCK) * 4
-                written += (m_scale, m_scale + scales), (v_scale, v_scale + scales)
+                written += (m_scale, m_scale + scales, v_scale, v_scale + scales)
             if copy is not None:
-                written += (copy, copy + 2 * n),
+                written += (copy, copy + 2 * n)
         self._keep([None if t is None else (p, t.shape, t.dtype) for t, p in zip(fields, at)],
                    d.grad, d, written)
         return d
@@ -1286,13 +1287,12 @@ class AdamWTensor:
     def _checked(self, fields):
         """The descriptor, and the pointers of `fields`, those but the gradient."""
         p, m, v, m_scale, v_scale, copy = fields
-        for t, what in ((p, "param"), (self.grad, "grad"), (m, "m"), (v, "v")):
-            if t is None:
-                raise ValueError(f"{what} is required")
+        g = self.grad
+        if p is None or g is None or m is None or v is None:
+            raise ValueError("param, grad, m and v are required")
         n, shape = p.numel(), p.shape
-        for t, what in ((p, "param"), (self.grad, "grad")):
-            if t.dtype not in _ADAMW_DTYPES:
-                raise TypeError(f"{what} must be fp32 or bf16, got {t.dtype}")
+        if p.dtype not in _ADAMW_DTYPES or g.dtype not in _ADAMW_DTYPES:
+            raise TypeError(f"param and grad must be fp32 or bf16, got {p.dtype} and {g.dtype}")
         if (m_scale is None) != (v_scale is None):
             raise ValueError("m_scale and v_scale come together")
         if copy is not None and p.dtype is not torch.float32:
@@ -1309,9 +1309,9 @@ class AdamWTensor:
                 raise ValueError(f"{what} must have shape {tuple(want)}, got {tuple(t.shape)}")
             at.append(_ptr(t, dtype, what))
         grad = self._grad_at(shape)
-        _on_current_device(self.grad, *fields)
+        _on_current_device(g, *fields)
         return _AdamWTensorDesc(at[0], grad, *at[1:], n, self.weight_decay, _ADAMW_DTYPES[p.dtype],
-                                _ADAMW_DTYPES[self.grad.dtype], 0), at
+                                _ADAMW_DTYPES[g.dtype], 0), at
 
 
 class AdamW:
@@ -1379,15 +1379,17 @@ class AdamW:
     def _tensor_array(self):
         """The tensors' descriptors as the C call takes them; those that have not changed
         stay in place."""
-        descs = [t.desc() for t in self.tensors]
-        if descs != self._descs:                         # (by identity)
-            same = self._descs if self._descs and len(descs) == len(self._descs) else ()
-            array = self._array if same else (_AdamWTensorDesc * len(descs))()
-            changed = [i for i, d in enumerate(descs) if not same or d is not same[i]]
-            self._need_separate(changed)
-            for i in changed:
-                array[i] = descs[i]
-            self._array, self._descs = array, descs
+        descs, old = [t.desc() for t in self.tensors], self._descs
+        if descs != old:                                 # (by identity)
+            if old is None or len(descs) != len(old):
+                self._need_separate(range(len(descs)))
+                self._array = (_AdamWTensorDesc * len(descs))(*descs)
+            else:
+                changed = [i for i, d in enumerate(descs) if d is not old[i]]
+                self._need_separate(changed)
+                for i in changed:
+                    self._array[i] = descs[i]
+            self._descs = descs
         return self._array, len(descs)
 
     def _need_separate(self, changed) -> None:
@@ -1396,15 +1398,17 @@ class AdamW:
         Gradients, which move between steps, are looked up in the sorted rest."""
         written, (starts, ends) = [t._seen[5] for t in self.tensors], self._spans
         if written != self._written:
-            spans = sorted([s for w in written for s in w])
-            starts, ends = [s for s, _ in spans], [e for _, e in spans]
+            every = list(itertools.chain.from_iterable(written))
+            starts, ends = sorted(every[::2]), sorted(every[1::2])
+            # Apart, each ends before the next begins: both orders are the spans'.
             if any(map(operator.gt, ends, starts[1:])):
                 raise ValueError("tensors must not share what a step writes")
             changed = range(len(written))
         for i in changed:
-            first, end = grad = self.tensors[i]._seen[6]
+            first, end = self.tensors[i]._seen[6]
             at = bisect.bisect_left(starts, end) - 1             # the last that begins before end
-            if first < end and at >= 0 and ends[at] > first and grad not in written[i]:
+            if first < end and at >= 0 and ends[at] > first \
+                    and (first, end) not in zip(written[i][::2], written[i][1::2]):
                 raise ValueError("grad must not overlap what a step writes")
         self._written, self._spans = written, (starts, ends)
 

@@ -277,3 +277,33 @@ def test_a_new_gradient_is_checked(monkeypatch):
     assert (t.desc().grad, t.desc().weight_decay) == (t.grad.data_ptr(), 0.25)
     t.grad, t.v = torch.zeros(4, 75), torch.zeros(4, 75, dtype=torch.uint8)
     assert (t.desc().grad, t.desc().v) == (t.grad.data_ptr(), t.v.data_ptr())
+
+
+def test_shared_spans_by_brute_force():
+    """Every pair of spans, over small random layouts: half of them overlap."""
+    r = np.random.default_rng(2)
+    overlap = lambda a, b: max(a[0], b[0]) < min(a[1], b[1])
+    refused, layouts = 0, 4000
+    for _ in range(layouts):
+        opt, mine = dsl.AdamW([], device="cpu"), []
+        for _ in range(r.integers(1, 5)):
+            t = dsl.AdamWTensor(None, None, None, None)
+            starts = r.integers(0, 60, r.integers(0, 3)).tolist()
+            spans = [(a, a + int(r.integers(1, 9))) for a in starts]
+            a = int(r.integers(0, 60))
+            grad = spans[0] if spans and r.random() < 0.2 else (a, a + int(r.integers(0, 9)))
+            t._seen = (0.0, 0, (), (), None, tuple(x for s in spans for x in s), grad)
+            opt.tensors.append(t)
+            mine.append((spans, grad))
+        every = [(i, s) for i, (spans, _) in enumerate(mine) for s in spans]
+        bad = any(overlap(s, t) for k, (_, s) in enumerate(every) for _, t in every[:k]) or \
+            any(overlap(g, s) and not (i == j and s == g)
+                for j, (_, g) in enumerate(mine) for i, s in every)
+        refused += bad
+        for _ in range(2):                              # a refused call is looked at again
+            try:
+                opt._need_separate(range(len(mine)))
+                assert not bad
+            except ValueError:
+                assert bad
+    assert 0.3 < refused / layouts < 0.7
